@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import numpy as np
 
@@ -27,6 +27,8 @@ __all__ = [
     "fas_prepass_noalloc", "fas_forward_host", "fas_set_layout", "LAYOUTS", "fas_forward_ablation",
     "fas_prologue", "fas_prologue_fold_weights", "PROLOGUE_LAYOUTS",
     "fas_prologue_with_key_sums", "fas_prepass_with_key_sums", "key_sums_shape",
+    "fas_backward", "fas_residual_norm", "fas_residual_norm_backward", "Checkpoint", "fas_checkpoint_pack",
+    "fas_checkpoint_unpack",
 ]
 
 FAS_OK, FAS_ERR_ARG, FAS_ERR_STATE, FAS_ERR_ALIGN, FAS_ERR_CUDA, FAS_ERR_TIMEOUT, FAS_ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
@@ -37,6 +39,7 @@ MODES = {"auto": 0, "online": 1, "bounded": 2}
 LAYOUTS = {"hnd": 0, "nhd": 1}  # q, k, v, out as [H, N, d] or [N, H, d]
 PROLOGUE_LAYOUTS = {"hnd": 0, "nhd": 1, "a2a": 2}  # fas_prologue's outputs (a2a: [G, P, n, H/(G*P), d])
 RMS_EPS = 1e-6
+CHECKPOINT_BLOCK = 32  # elements of a checkpoint that share one scale
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -103,6 +106,18 @@ _SIGS = {
     "fas_last_launch_count": (ctypes.c_int, []),
     "fas_prepass_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p] + [ctypes.c_int] * 6 +
                             [ctypes.c_void_p] * 4),
+    "fas_backward": (ctypes.c_int, [ctypes.c_void_p] * 11),
+    "fas_residual_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 3 +
+                          [ctypes.c_float, ctypes.c_float, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                           ctypes.c_int] + [ctypes.c_void_p] * 8),
+    "fas_residual_norm_backward": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_int] + [ctypes.c_void_p] * 8 +
+                                   [ctypes.c_float, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int] +
+                                   [ctypes.c_void_p] * 6 + [ctypes.c_int64, ctypes.c_void_p]),
+    "fas_residual_norm_backward_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                                            ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]),
+    "fas_checkpoint_pack": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_int64, ctypes.c_void_p]),
+    "fas_checkpoint_unpack": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int, ctypes.c_int64, ctypes.c_void_p]),
     "fas_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fas_set_layout": (ctypes.c_int, [ctypes.c_int]),
 }
@@ -384,6 +399,236 @@ def _prologue(x, w_folded, cos, sin, heads, head_dim, layout, groups, ranks, q, 
                                            key_sums.data_ptr(), _stream_handle(stream))
     _check("fas_prologue_with_key_sums", rc)
     return (*outs, key_sums)
+
+
+def _check_device(*tensors):
+    """All tensors on the current device (the kernels launch there)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _own_until_run(stream, *temps):
+    """Keeps the memory of tensors the binding allocated for a call on
+    another stream than the current one until that stream has used it."""
+    import torch
+    if stream is None:
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream != torch.cuda.current_stream():
+        for t in temps:
+            t.record_stream(stream)
+
+
+def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None):
+    """The attention's backward pass (see ``fas_backward`` in fas.h): q, k, v,
+    out, lse as fas_forward took and returned them, dout the gradient of out
+    (bf16, the plan's layout).  Returns (dq, dk, dv)."""
+    import torch
+    shape = _qkv_shape()
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
+        _check_tensor(name, t, shape, torch.bfloat16)
+    _check_tensor("lse", lse, _lse_shape(), torch.float32)
+    grads = []
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        _check_tensor(name, t, shape, torch.bfloat16)
+        grads.append(t)
+    _check_device(q, k, v, out, lse, dout, *grads)
+    delta = torch.empty(_lse_shape(), dtype=torch.float32, device=q.device)
+    rc = load().fas_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                             dout.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
+                             delta.data_ptr(), _stream_handle(stream))
+    _check("fas_backward", rc)
+    _own_until_run(stream, delta, *grads)
+    return tuple(grads)
+
+
+class Checkpoint(NamedTuple):
+    """A tensor held in 8 bits: e4m3 codes in the tensor's shape and one
+    exponent byte per 32 elements of the last axis (value = code *
+    2^(scale - 127); see ``fas_checkpoint_pack`` in fas.h)."""
+    codes: "torch.Tensor"
+    scales: "torch.Tensor"
+
+
+def _dtype_code(name, t):
+    import torch
+    codes = {torch.bfloat16: 0, torch.float32: 1}
+    if not isinstance(t, torch.Tensor) or t.dtype not in codes:
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    return codes[t.dtype]
+
+
+def _checkpoint_empty(shape, device):
+    import torch
+    if not shape or shape[-1] % CHECKPOINT_BLOCK or 0 in shape:
+        raise ValueError(f"a checkpointed tensor's last axis must be a positive multiple of {CHECKPOINT_BLOCK} "
+                         f"and its shape not empty, got {tuple(shape)}")
+    return Checkpoint(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                      torch.empty((*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), dtype=torch.uint8, device=device))
+
+
+def _check_checkpoint(name, c, shape=None):
+    import torch
+    if not isinstance(c, tuple) or len(c) != 2:
+        raise TypeError(f"{name} must be a Checkpoint (codes, scales)")
+    c = Checkpoint(*c)
+    shape = tuple(c.codes.shape) if shape is None else tuple(shape)
+    if not shape or shape[-1] % CHECKPOINT_BLOCK:
+        raise ValueError(f"{name}: the last axis must be a multiple of {CHECKPOINT_BLOCK}, got {shape}")
+    _check_tensor(f"{name}.codes", c.codes, shape, torch.float8_e4m3fn)
+    _check_tensor(f"{name}.scales", c.scales, (*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), torch.uint8)
+    return c
+
+
+def fas_checkpoint_pack(x, out: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
+    """Holds x (bf16 or fp32, contiguous, last axis a multiple of 32) in 8
+    bits: see ``fas_checkpoint_pack`` in fas.h."""
+    dtype = _dtype_code("x", x)
+    _check_tensor("x", x, x.shape, x.dtype)
+    c = _checkpoint_empty(tuple(x.shape), x.device) if out is None else _check_checkpoint("out", out, x.shape)
+    _check_device(x, *c)
+    _check("fas_checkpoint_pack",
+           load().fas_checkpoint_pack(x.data_ptr(), dtype, c.codes.data_ptr(), c.scales.data_ptr(), x.numel(),
+                                      _stream_handle(stream)))
+    _own_until_run(stream, *c)
+    return c
+
+
+def fas_checkpoint_unpack(c: Checkpoint, dtype=None, out=None, stream=None):
+    """The tensor a checkpoint stands for, as bf16 (the default) or fp32."""
+    import torch
+    c = _check_checkpoint("c", c)
+    if out is None:
+        out = torch.empty(c.codes.shape, dtype=dtype or torch.bfloat16, device=c.codes.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    code = _dtype_code("out", out)
+    _check_tensor("out", out, c.codes.shape, out.dtype)
+    _check_device(out, *c)
+    _check("fas_checkpoint_unpack",
+           load().fas_checkpoint_unpack(c.codes.data_ptr(), c.scales.data_ptr(), out.data_ptr(), code, out.numel(),
+                                        _stream_handle(stream)))
+    _own_until_run(stream, out)
+    return out
+
+
+def _norm_frames(tokens: int, width: int, gate, frame_tokens):
+    """(gate pointer, host spans or None, number of frames)."""
+    import torch
+    if gate is None:
+        return None, None, 1
+    if gate.ndim != 2:
+        raise ValueError(f"gate must be [frames, width], got {tuple(gate.shape)}")
+    n = gate.shape[0]
+    _check_tensor("gate", gate, (n, width), torch.float32)
+    if frame_tokens is None or np.ndim(frame_tokens) == 0:
+        span = tokens // n if frame_tokens is None and n else frame_tokens
+        if n * int(span or 0) != tokens:
+            raise ValueError(f"gate has {n} frames of {span} tokens; x has {tokens} tokens")
+        return gate.data_ptr(), None, n
+    spans = np.ascontiguousarray(frame_tokens, dtype=np.int32)
+    if spans.ndim != 1 or len(spans) != n or int(spans.sum(dtype=np.int64)) != tokens:
+        raise ValueError(f"frame_tokens must hold {n} spans (one per row of gate) that add up to {tokens} tokens")
+    return gate.data_ptr(), spans, n
+
+
+def _empty_or(name, t, shape, dtype, device):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_tensor(name, t, shape, dtype)
+    return t
+
+
+def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None, alpha: float = 1.0,
+                      eps: float = RMS_EPS, checkpoint: bool = False, x_out=None, h=None, stream=None):
+    """The norm after a block, its gate and residual, and the norm before the
+    next one, in one kernel (see ``fas_residual_norm`` in fas.h):
+    x' = x + alpha * gate * rmsnorm(y) * gamma_post, h = rmsnorm(x') * gamma_pre.
+    y bf16 [N, C]; x bf16 or fp32 [N, C]; gammas fp32 [C]; gate fp32
+    [frames, C] or None; frame_tokens: tokens of each frame (one number, a
+    sequence, or None for equal frames).  x_out may be x and h may be y.
+    Returns (x', h, rstd [2, N]), and with ``checkpoint`` also the 8-bit
+    Checkpoints of y and of x'."""
+    import torch
+    residual = _dtype_code("x", x)
+    if x.ndim != 2:
+        raise ValueError(f"x must be [tokens, width], got {tuple(x.shape)}")
+    N, C = x.shape
+    _check_tensor("x", x, (N, C), x.dtype)
+    _check_tensor("y", y, (N, C), torch.bfloat16)
+    _check_tensor("gamma_post", gamma_post, (C,), torch.float32)
+    _check_tensor("gamma_pre", gamma_pre, (C,), torch.float32)
+    gate_ptr, spans, frames = _norm_frames(N, C, gate, frame_tokens)
+    x_out = _empty_or("x_out", x_out, (N, C), x.dtype, x.device)
+    h = _empty_or("h", h, (N, C), torch.bfloat16, x.device)
+    rstd = torch.empty((2, N), dtype=torch.float32, device=x.device)
+    held = (_checkpoint_empty((N, C), x.device), _checkpoint_empty((N, C), x.device)) if checkpoint else ()
+    parts = [t for c in held for t in c]
+    _check_device(y, x, gamma_post, gamma_pre, gate, x_out, h)
+    rc = load().fas_residual_norm(y.data_ptr(), x.data_ptr(), residual, gate_ptr, gamma_post.data_ptr(),
+                                  gamma_pre.data_ptr(), float(alpha), float(eps), N, C,
+                                  None if spans is None else spans.ctypes.data, frames, x_out.data_ptr(),
+                                  h.data_ptr(), rstd.data_ptr(), *([t.data_ptr() for t in parts] or [None] * 4),
+                                  _stream_handle(stream))
+    _check("fas_residual_norm", rc)
+    _own_until_run(stream, x_out, h, rstd, *parts)
+    return (x_out, h, rstd, *held)
+
+
+def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre, gate=None, frame_tokens=None,
+                               alpha: float = 1.0, dx=None, dy=None, stream=None):
+    """Backward pass of fas_residual_norm (see fas.h): dx_out the gradient of
+    x' (x's type), dh that of h; y and x_out as tensors or both as the
+    forward's Checkpoints; rstd as the forward returned it.  dx may be dx_out
+    and dy may be dh.  Returns (dx, dy, dgamma_post, dgamma_pre, dgate), dgate
+    None without a gate."""
+    import torch
+    residual = _dtype_code("dx_out", dx_out)
+    if dx_out.ndim != 2:
+        raise ValueError(f"dx_out must be [tokens, width], got {tuple(dx_out.shape)}")
+    N, C = dx_out.shape
+    _check_tensor("dx_out", dx_out, (N, C), dx_out.dtype)
+    _check_tensor("dh", dh, (N, C), torch.bfloat16)
+    if isinstance(y, torch.Tensor) != isinstance(x_out, torch.Tensor):
+        raise TypeError("y and x_out must both be tensors or both be Checkpoints")
+    if isinstance(y, torch.Tensor):
+        _check_tensor("y", y, (N, C), torch.bfloat16)
+        _check_tensor("x_out", x_out, (N, C), dx_out.dtype)
+        saved = [y, x_out]
+        ptrs = [y.data_ptr(), x_out.data_ptr(), residual] + [None] * 4
+    else:
+        saved = [*_check_checkpoint("y", y, (N, C)), *_check_checkpoint("x_out", x_out, (N, C))]
+        ptrs = [None, None, residual] + [t.data_ptr() for t in saved]
+    _check_tensor("rstd", rstd, (2, N), torch.float32)
+    _check_tensor("gamma_post", gamma_post, (C,), torch.float32)
+    _check_tensor("gamma_pre", gamma_pre, (C,), torch.float32)
+    gate_ptr, spans, frames = _norm_frames(N, C, gate, frame_tokens)
+    dx = _empty_or("dx", dx, (N, C), dx_out.dtype, dx_out.device)
+    dy = _empty_or("dy", dy, (N, C), torch.bfloat16, dx_out.device)
+    _check_device(dx_out, dh, *saved, rstd, gamma_post, gamma_pre, gate, dx, dy)
+    lib = load()
+    spans_ptr = None if spans is None else spans.ctypes.data
+    need = ctypes.c_int64()
+    _check("fas_residual_norm_backward",
+           lib.fas_residual_norm_backward_workspace(N, C, spans_ptr, frames, ctypes.byref(need)))
+    workspace = torch.empty(need.value, dtype=torch.uint8, device=dx_out.device)
+    dgammas = torch.empty((2, C), dtype=torch.float32, device=dx_out.device)  # C is a multiple of 8
+    dgate = None if gate is None else torch.empty_like(gate)
+    rc = lib.fas_residual_norm_backward(
+        dx_out.data_ptr(), dh.data_ptr(), *ptrs, rstd.data_ptr(), gate_ptr, gamma_post.data_ptr(),
+        gamma_pre.data_ptr(), float(alpha), N, C, spans_ptr, frames, dx.data_ptr(), dy.data_ptr(),
+        None if dgate is None else dgate.data_ptr(), dgammas[0].data_ptr(), dgammas[1].data_ptr(),
+        workspace.data_ptr(), need.value, _stream_handle(stream))
+    _check("fas_residual_norm_backward", rc)
+    _own_until_run(stream, workspace, dgammas, dx, dy, *([] if dgate is None else [dgate]))
+    return dx, dy, dgammas[0], dgammas[1], dgate
 
 
 def _check_host_tensor(name, t, shape, dtype):

@@ -856,6 +856,239 @@ int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded,
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
+int fas_backward(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
+                 void* dq, void* dk, void* dv, float* delta, void* cuda_stream) {
+  if (!g_state.planned) return FAS_ERR_STATE;
+  const void* ptrs[] = {q, k, v, out, lse, dout, dq, dk, dv, delta};
+  for (const void* ptr : ptrs)
+    if (!ptr) return FAS_ERR_ARG;
+  // Gradients are written while inputs are still read.
+  const void* outs[] = {dq, dk, dv, delta};
+  for (int i = 0; i < 4; ++i) {
+    for (const void* in : {q, k, v, out, (const void*)lse, dout})
+      if (outs[i] == in) return FAS_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] == outs[j]) return FAS_ERR_ARG;
+  }
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return FAS_ERR_ALIGN;
+  const int rc = check_device();
+  if (rc != FAS_OK) return rc;
+  const HostPlan& p = g_state.plan;
+  State& s = g_state;
+  fas::BwdParams b;
+  b.work = s.work;
+  b.table = s.table;
+  b.spans = s.spans;
+  b.q = static_cast<const uint16_t*>(q);
+  b.k = static_cast<const uint16_t*>(k);
+  b.v = static_cast<const uint16_t*>(v);
+  b.out = static_cast<const uint16_t*>(out);
+  b.dout = static_cast<const uint16_t*>(dout);
+  b.dq = static_cast<uint16_t*>(dq);
+  b.dk = static_cast<uint16_t*>(dk);
+  b.dv = static_cast<uint16_t*>(dv);
+  b.row_stride = row_stride();
+  b.head_stride = head_stride();
+  b.lse = lse;
+  b.delta = delta;
+  b.N = p.N;
+  b.scale = (float)(1.0 / sqrt((double)p.d));
+  const int n = fas::launch_attention_backward(p.d, b, p.n_work, static_cast<cudaStream_t>(cuda_stream));
+  s.last_launches = n > 0 ? n : 0;
+  return n > 0 ? FAS_OK : FAS_ERR_CUDA;
+}
+
+namespace {
+
+int device_sms(int* sms) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FAS_ERR_CUDA;
+  return FAS_OK;
+}
+
+// Checks the frames of a residual norm; without a gate the rows are one
+// frame.  Returns a FAS_* status.
+int norm_frames(int64_t tokens, const void* gate, const int32_t** spans, int* n_frames, int64_t* span) {
+  if (!gate) {
+    *spans = nullptr;
+    *n_frames = 1;
+    *span = tokens;
+    return FAS_OK;
+  }
+  if (*n_frames < 1) return FAS_ERR_ARG;
+  if (!*spans) {
+    if (tokens % *n_frames != 0) return FAS_ERR_ARG;
+    *span = tokens / *n_frames;
+    return FAS_OK;
+  }
+  if (*n_frames > fas::kNormMaxFrames) return FAS_ERR_UNSUPPORTED;
+  int64_t n = 0;
+  for (int f = 0; f < *n_frames; ++f) {
+    if ((*spans)[f] < 1) return FAS_ERR_ARG;
+    n += (*spans)[f];
+  }
+  return n == tokens ? FAS_OK : FAS_ERR_ARG;
+}
+
+int norm_shape(int64_t tokens, int width, int residual) {
+  if (tokens < 1 || tokens > INT32_MAX || width < 8 || width % 8 != 0) return FAS_ERR_ARG;
+  if (residual != FAS_DTYPE_BF16 && residual != FAS_DTYPE_F32) return FAS_ERR_ARG;
+  return width <= fas::kNormMaxWidth ? FAS_OK : FAS_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int fas_residual_norm(const void* y, const void* x, int residual, const float* gate, const float* gamma_post,
+                      const float* gamma_pre, float alpha, float eps, int64_t tokens, int width,
+                      const int32_t* frame_tokens, int n_frames, void* x_out, void* h, float* rstd, uint8_t* y_codes,
+                      uint8_t* y_scales, uint8_t* x_codes, uint8_t* x_scales, void* cuda_stream) {
+  if (!y || !x || !gamma_post || !gamma_pre || !x_out || !h || !rstd) return FAS_ERR_ARG;
+  int rc = norm_shape(tokens, width, residual);
+  if (rc != FAS_OK) return rc;
+  const int held = (y_codes != nullptr) + (y_scales != nullptr) + (x_codes != nullptr) + (x_scales != nullptr);
+  if ((held != 0 && held != 4) || (held && width % FAS_CHECKPOINT_BLOCK != 0)) return FAS_ERR_ARG;
+  if (!(eps >= 0.f)) return FAS_ERR_ARG;
+  int64_t span = 0;
+  rc = norm_frames(tokens, gate, &frame_tokens, &n_frames, &span);
+  if (rc != FAS_OK) return rc;
+  for (const void* ptr : {y, x, (const void*)gate, (const void*)gamma_post, (const void*)gamma_pre,
+                          (const void*)x_out, (const void*)h, (const void*)rstd, (const void*)y_codes,
+                          (const void*)x_codes})
+    if (!aligned16(ptr)) return FAS_ERR_ALIGN;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc != FAS_OK) return rc;
+  fas::NormArgs a;
+  a.y = y;
+  a.x = x;
+  a.gate = gate;
+  a.gamma_post = gamma_post;
+  a.gamma_pre = gamma_pre;
+  a.rstd = rstd;
+  a.x_out = x_out;
+  a.h = h;
+  a.y8 = y_codes;
+  a.y8_scale = y_scales;
+  a.x8 = x_codes;
+  a.x8_scale = x_scales;
+  a.rows = tokens;
+  a.width = width;
+  a.f32 = residual == FAS_DTYPE_F32;
+  a.alpha = alpha;
+  a.eps = eps;
+  const cudaError_t e =
+      fas::launch_residual_norm(a, frame_tokens, n_frames, span, sms, static_cast<cudaStream_t>(cuda_stream));
+  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
+}
+
+int fas_residual_norm_backward_workspace(int64_t tokens, int width, const int32_t* frame_tokens, int n_frames,
+                                         int64_t* bytes) {
+  if (!bytes) return FAS_ERR_ARG;
+  int rc = norm_shape(tokens, width, FAS_DTYPE_BF16);
+  if (rc != FAS_OK) return rc;
+  int64_t span = 0;
+  rc = norm_frames(tokens, bytes, &frame_tokens, &n_frames, &span);
+  if (rc != FAS_OK) return rc;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc != FAS_OK) return rc;
+  *bytes = fas::residual_norm_items(tokens, width, frame_tokens, n_frames, span, sms).bytes;
+  return FAS_OK;
+}
+
+int fas_residual_norm_backward(const void* dx_out, const void* dh, const void* y, const void* x_out, int residual,
+                               const uint8_t* y_codes, const uint8_t* y_scales, const uint8_t* x_codes,
+                               const uint8_t* x_scales, const float* rstd, const float* gate, const float* gamma_post,
+                               const float* gamma_pre, float alpha, int64_t tokens, int width,
+                               const int32_t* frame_tokens, int n_frames, void* dx, void* dy, float* dgate,
+                               float* dgamma_post, float* dgamma_pre, void* workspace, int64_t workspace_bytes,
+                               void* cuda_stream) {
+  if (!dx_out || !dh || !rstd || !gamma_post || !gamma_pre || !dx || !dy || !dgamma_post || !dgamma_pre || !workspace)
+    return FAS_ERR_ARG;
+  if ((gate == nullptr) != (dgate == nullptr)) return FAS_ERR_ARG;
+  const int plain = (y != nullptr) + (x_out != nullptr);
+  const int held = (y_codes != nullptr) + (y_scales != nullptr) + (x_codes != nullptr) + (x_scales != nullptr);
+  if (!((plain == 2 && held == 0) || (plain == 0 && held == 4))) return FAS_ERR_ARG;
+  int rc = norm_shape(tokens, width, residual);
+  if (rc != FAS_OK) return rc;
+  if (held && width % FAS_CHECKPOINT_BLOCK != 0) return FAS_ERR_ARG;
+  int64_t span = 0;
+  rc = norm_frames(tokens, gate, &frame_tokens, &n_frames, &span);
+  if (rc != FAS_OK) return rc;
+  for (const void* ptr : {dx_out, dh, y, x_out, (const void*)y_codes, (const void*)x_codes, (const void*)rstd,
+                          (const void*)gate, (const void*)gamma_post, (const void*)gamma_pre, (const void*)dx,
+                          (const void*)dy, (const void*)dgate, (const void*)dgamma_post, (const void*)dgamma_pre,
+                          (const void*)workspace})
+    if (!aligned16(ptr)) return FAS_ERR_ALIGN;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc != FAS_OK) return rc;
+  const fas::NormItems items = fas::residual_norm_items(tokens, width, frame_tokens, n_frames, span, sms);
+  if (workspace_bytes < items.bytes) return FAS_ERR_SCRATCH;
+  fas::NormArgs a;
+  a.y = y;
+  a.x = x_out;
+  a.gate = gate;
+  a.gamma_post = gamma_post;
+  a.gamma_pre = gamma_pre;
+  a.rstd = const_cast<float*>(rstd);
+  a.y8 = const_cast<uint8_t*>(y_codes);
+  a.y8_scale = const_cast<uint8_t*>(y_scales);
+  a.x8 = const_cast<uint8_t*>(x_codes);
+  a.x8_scale = const_cast<uint8_t*>(x_scales);
+  a.dx_out = dx_out;
+  a.dh = dh;
+  a.dx = dx;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.dgamma_post = dgamma_post;
+  a.dgamma_pre = dgamma_pre;
+  a.rows = tokens;
+  a.width = width;
+  a.f32 = residual == FAS_DTYPE_F32;
+  a.alpha = alpha;
+  const cudaError_t e = fas::launch_residual_norm_backward(a, items, frame_tokens, n_frames, span, workspace,
+                                                           static_cast<cudaStream_t>(cuda_stream));
+  g_state.last_launches = e == cudaSuccess ? 2 : 0;
+  return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
+}
+
+namespace {
+
+int checkpoint_args(const void* x, const void* codes, const void* scales, int64_t elements, int dtype) {
+  if (!x || !codes || !scales || elements < FAS_CHECKPOINT_BLOCK || elements % FAS_CHECKPOINT_BLOCK != 0 ||
+      elements > (int64_t)INT32_MAX * 1024)
+    return FAS_ERR_ARG;
+  if (dtype != FAS_DTYPE_BF16 && dtype != FAS_DTYPE_F32) return FAS_ERR_ARG;
+  return aligned16(x) && aligned16(codes) ? FAS_OK : FAS_ERR_ALIGN;
+}
+
+}  // namespace
+
+int fas_checkpoint_pack(const void* x, int dtype, uint8_t* codes, uint8_t* scales, int64_t elements,
+                        void* cuda_stream) {
+  const int rc = checkpoint_args(x, codes, scales, elements, dtype);
+  if (rc != FAS_OK) return rc;
+  const cudaError_t e = fas::launch_checkpoint_pack(x, dtype == FAS_DTYPE_F32, codes, scales, elements,
+                                                    static_cast<cudaStream_t>(cuda_stream));
+  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
+}
+
+int fas_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, int dtype, int64_t elements,
+                          void* cuda_stream) {
+  const int rc = checkpoint_args(x, codes, scales, elements, dtype);
+  if (rc != FAS_OK) return rc;
+  const cudaError_t e = fas::launch_checkpoint_unpack(codes, scales, x, dtype == FAS_DTYPE_F32, elements,
+                                                      static_cast<cudaStream_t>(cuda_stream));
+  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
+}
+
 int fas_set_layout(int layout) {
   if (layout != FAS_LAYOUT_HND && layout != FAS_LAYOUT_NHD) return FAS_ERR_ARG;
   if (!g_state.planned) return FAS_ERR_STATE;

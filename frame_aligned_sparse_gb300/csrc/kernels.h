@@ -157,6 +157,75 @@ cudaError_t launch_prologue(const CUtensorMap& tx, const CUtensorMap& tw, const 
 cudaError_t launch_fold_weights(const uint16_t* w, const float* gamma, uint16_t* out, int64_t rows, int width,
                                 cudaStream_t stream);
 
+// The attention backward pass.  Visibility is symmetric in the frames, so
+// `table` also lists the query ranges that see a key frame.
+struct BwdParams {
+  const int4* work;        // [n_work] {head, frame, 128-row tile, -}
+  const int4* table;       // [Nf] {start0, len0, start1, len1}
+  const int2* spans;       // [Nf] {first token, tokens} of each frame
+  const uint16_t *q, *k, *v, *out, *dout;  // bf16, row (h, j) at + h * head_stride + j * row_stride
+  uint16_t *dq, *dk, *dv;
+  int64_t row_stride, head_stride;         // elements
+  const float* lse;        // [H, N]
+  float* delta;            // [H, N] sum_c dout out, written by the query pass, read by the key pass
+  int64_t N;
+  float scale;             // 1 / sqrt(d)
+};
+
+// Launches the query pass (delta, dq) and the key pass (dk, dv) over `grid`
+// work items; returns the number of kernels, or a negative value on a
+// launch error.
+int launch_attention_backward(int d, const BwdParams& p, int grid, cudaStream_t stream);
+
+// The norms around a block with its gate and residual (residual_norm.cu).
+constexpr int kNormMaxFrames = 1024;   // frames of a ragged table (passed with the launch)
+constexpr int kNormMaxWidth = 16384;   // columns a row's warps hold in registers
+
+struct NormArgs {
+  const void* y = nullptr;        // bf16 [rows, width]
+  const void* x = nullptr;        // bf16 or fp32 [rows, width]: x (forward), x' (backward)
+  const float* gate = nullptr;    // null, or fp32 [frames, width]
+  const float* gamma_post = nullptr;
+  const float* gamma_pre = nullptr;
+  float* rstd = nullptr;          // [2, rows]: 1/rms of y, of x'
+  void* x_out = nullptr;          // forward outputs
+  void* h = nullptr;
+  uint8_t *y8 = nullptr, *y8_scale = nullptr;  // checkpoints of y and x' (null: none)
+  uint8_t *x8 = nullptr, *x8_scale = nullptr;
+  const void* dx_out = nullptr;   // backward: gradients of x' and h, outputs
+  const void* dh = nullptr;
+  void* dx = nullptr;
+  void* dy = nullptr;
+  float *dgate = nullptr, *dgamma_post = nullptr, *dgamma_pre = nullptr;
+  float *z_part = nullptr, *d_part = nullptr;    // [items, width] partial column sums
+  float *z_frame = nullptr, *d_frame = nullptr;  // [frames, width]
+  unsigned int* counter = nullptr;               // [counters]
+  int64_t rows = 0, items = 0, chunk = 0;
+  int width = 0, counters = 0;
+  int warps = 1, groups = 1;      // warps per row, rows per CTA (set by the launcher)
+  bool f32 = false;               // residual type
+  float alpha = 1.f, eps = 0.f;
+};
+
+// How the backward pass splits the rows, and its workspace.
+struct NormItems {
+  int64_t items = 0, chunk = 0, bytes = 0;
+  int counters = 0;
+};
+
+// spans: null (n_frames frames of `span` rows) or n_frames host row counts.
+NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms);
+cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
+                                 cudaStream_t stream);
+cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
+                                          int64_t span, void* workspace, cudaStream_t stream);
+
+// n elements (a multiple of 32) to and from 8-bit checkpoints.
+cudaError_t launch_checkpoint_pack(const void* x, bool f32, uint8_t* codes, uint8_t* scales, int64_t n,
+                                   cudaStream_t stream);
+cudaError_t launch_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, bool f32, int64_t n,
+                                     cudaStream_t stream);
+
 cudaError_t launch_wait_selftest(unsigned int* err, uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace fas

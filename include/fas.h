@@ -82,6 +82,12 @@ enum {
   FAS_MODE_BOUNDED = 2  /* every head bounded softmax (ablation; loose heads may underflow) */
 };
 
+/* Element types of the residual stream and of checkpointed tensors. */
+enum {
+  FAS_DTYPE_BF16 = 0,
+  FAS_DTYPE_F32 = 1
+};
+
 /* Per-head eligibility threshold: a head keeps the bounded softmax when the
  * guaranteed gap between every row's bound and its true maximum is at most
  * this many nats (e^-32 stays far above the fp32 underflow limit e^-87). */
@@ -370,6 +376,105 @@ int fas_prologue_with_key_sums(const void* x, const void* w_folded, const float*
  * gamma: device fp32 [width].  Asynchronous on cuda_stream. */
 int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded, int width, int out_features,
                               void* cuda_stream);
+
+/* The attention's backward pass.  With s = 1/sqrt(d), P = exp(s q.k - lse)
+ * over the pairs fas_forward attends to (recomputed, never stored) and
+ * delta_i = sum_c dout_ic out_ic:
+ *   dS_ij = P_ij (dout_i . v_j - delta_i)
+ *   dq_i = s sum_j dS_ij k_j   dk_j = s sum_i dS_ij q_i   dv_j = sum_i P_ij dout_i
+ * q, k, v, out, lse: fas_forward's inputs and outputs (any mode; the prepass
+ * is not needed again); dout: the gradient of out.  dq, dk, dv: outputs.  All
+ * bf16 in the current layout.  delta: device fp32 [H, N], receives delta_i
+ * (the caller's memory, so that calls on other streams, and captured graphs,
+ * share nothing but the plan's read-only tables).  Sums are fp32; P and dS
+ * are rounded to bf16 for the products.  Every output row is written exactly
+ * once, by one CTA in a fixed order: results are bit-reproducible.  Tokens a
+ * row does not see are not read into it, whatever they hold.  Needs a plan
+ * (uniform or ragged); an output that is also an input or another output
+ * returns FAS_ERR_ARG.  Asynchronous on cuda_stream; may be captured into a
+ * graph.  (The page has no training; its section "Deleting the Mask" gives
+ * the visibility.) */
+int fas_backward(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
+                 void* dq, void* dk, void* dv, float* delta, void* cuda_stream);
+
+/* The norms around a block, its gate and its residual, in one kernel.  For
+ * token n of frame f, with the block's output y (bf16 [tokens, width]) and
+ * the residual stream x (bf16 or fp32 [tokens, width], `residual`):
+ *   r_y = 1/sqrt(mean(y^2) + eps)    x' = x + alpha gate_f (y r_y gamma_post)
+ *   r_x = 1/sqrt(mean(x'^2) + eps)   h  = x' r_x gamma_pre
+ * x' before its rounding enters r_x and h.
+ *   gate       : null (gate 1), or device fp32 [n_frames, width];
+ *   gamma_post,
+ *   gamma_pre  : device fp32 [width];
+ *   frame_tokens: host int32 [n_frames] token counts (read during the call;
+ *                at most 1024 frames), each at least 1, their sum `tokens`;
+ *                or null: n_frames frames of tokens / n_frames each.  Both
+ *                are ignored without a gate.  The spans need not be
+ *                multiples of 16, and no plan is needed;
+ *   x_out      : x' in x's type; may be x itself (updated in place);
+ *   h          : bf16 [tokens, width]; may be y itself;
+ *   rstd       : fp32 [2, tokens], r_y then r_x, for the backward pass;
+ *   y_codes ... x_scales: null, or 8-bit checkpoints of y and of x' as
+ *                stored (see fas_checkpoint_pack), written in the same pass.
+ * Outputs that overlap inputs or each other in any other way are not
+ * supported.  width: a multiple of 8 (of 32 with checkpoints), at most
+ * 16384 (FAS_ERR_UNSUPPORTED above); eps >= 0; tokens >= 1.  Pointers
+ * 16-byte aligned (scales: any).  Sums are fp32.  Asynchronous on
+ * cuda_stream; allocates nothing. */
+int fas_residual_norm(const void* y, const void* x, int residual, const float* gate, const float* gamma_post,
+                      const float* gamma_pre, float alpha, float eps, int64_t tokens, int width,
+                      const int32_t* frame_tokens, int n_frames, void* x_out, void* h, float* rstd, uint8_t* y_codes,
+                      uint8_t* y_scales, uint8_t* x_codes, uint8_t* x_scales, void* cuda_stream);
+
+/* Backward pass of fas_residual_norm.  With yh = y r_y, xh = x' r_x (rstd as
+ * the forward wrote it) and the gradients dx_out of x' (x's type) and dh of h:
+ *   a = dh gamma_pre;          g = dx_out + r_x (a - xh mean(a xh));   dx = g
+ *   b = alpha gate_f g gamma_post;   dy = r_y (b - yh mean(b yh))
+ *   dgate_f = alpha gamma_post sum_{n in f} yh g
+ *   dgamma_post = alpha sum_n gate_f yh g;   dgamma_pre = sum_n dh xh
+ * y and x' come either as tensors (y bf16, x_out in x's type; the four
+ * checkpoint pointers null) or as the forward's 8-bit checkpoints (y and
+ * x_out null).  dx: x's type, may be dx_out itself; dy: bf16, may be dh
+ * itself; dgate (null exactly when gate is): fp32 [n_frames, width];
+ * dgamma_post, dgamma_pre: fp32 [width].  workspace: device memory of at
+ * least fas_residual_norm_backward_workspace bytes (FAS_ERR_SCRATCH if
+ * smaller), the call's own until it has run.  Column sums are added in a
+ * fixed order: results are bit-reproducible on one device type.  Other
+ * arguments and limits as fas_residual_norm.  Two kernels, asynchronous on
+ * cuda_stream. */
+int fas_residual_norm_backward(const void* dx_out, const void* dh, const void* y, const void* x_out, int residual,
+                               const uint8_t* y_codes, const uint8_t* y_scales, const uint8_t* x_codes,
+                               const uint8_t* x_scales, const float* rstd, const float* gate, const float* gamma_post,
+                               const float* gamma_pre, float alpha, int64_t tokens, int width,
+                               const int32_t* frame_tokens, int n_frames, void* dx, void* dy, float* dgate,
+                               float* dgamma_post, float* dgamma_pre, void* workspace, int64_t workspace_bytes,
+                               void* cuda_stream);
+
+/* Bytes of workspace for fas_residual_norm_backward on the current device
+ * (without a gate: pass frame_tokens null, n_frames 1). */
+int fas_residual_norm_backward_workspace(int64_t tokens, int width, const int32_t* frame_tokens, int n_frames,
+                                         int64_t* bytes);
+
+/* Elements of a checkpoint that share one scale. */
+#define FAS_CHECKPOINT_BLOCK 32
+
+/* 8-bit activation checkpoints.  Each block of 32 consecutive elements holds
+ * e4m3 codes (codes[i], one byte an element) under one power of two
+ * 2^(scales[i / 32] - 127): the smallest one under which the block's largest
+ * finite magnitude is at most 448, never below 2^-127.  Each code is the
+ * nearest to element / scale, ties to even, so nothing saturates and a value
+ * is off by at most 2^-4 of itself (or 2^-10 of the scale, if that is more).
+ * Elements that are not finite become NaN.  x: device, `dtype` (FAS_DTYPE_*),
+ * contiguous; elements: a positive multiple of 32 (a row of the checkpointed
+ * tensor must be a multiple of 32 for blocks to stay inside rows).  x and
+ * codes 16-byte aligned.  One kernel, asynchronous on cuda_stream. */
+int fas_checkpoint_pack(const void* x, int dtype, uint8_t* codes, uint8_t* scales, int64_t elements,
+                        void* cuda_stream);
+
+/* The values a checkpoint stands for (exact in both types, apart from those
+ * below the type's smallest normal number). */
+int fas_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, int dtype, int64_t elements,
+                          void* cuda_stream);
 
 /* Kernel launches issued by the last fas_prepass / fas_forward call. */
 int fas_last_launch_count(void);

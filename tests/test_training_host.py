@@ -1,0 +1,155 @@
+"""Training operators, host side (no GPU): the references agree with
+differences and with each other, and bad arguments are refused before any
+device work."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import frame_aligned_sparse_gb300 as fas
+import training_reference as ref
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    from frame_aligned_sparse_gb300 import build
+    build.build()
+    return fas.load()
+
+
+@pytest.mark.parametrize("spans,R0,r", [([16, 32, 16, 48], 1, 1), ([16, 16, 32], 0, 0), ([16, 48], 2, 1)])
+def test_attention_backward_reference_matches_differences(spans, R0, r):
+    """The gradient formulas against central differences of the forward in 64
+    bits: step 1e-5, so truncation 1e-10 and cancellation 1e-11 relative."""
+    g = torch.Generator().manual_seed(0)
+    h, n, d = 2, sum(spans), 64
+    x = [torch.randn(h, n, d, generator=g, dtype=torch.float64) for _ in range(4)]
+    q, k, v, dout = x
+    out, lse = ref.attention(q, k, v, spans, R0, r)
+    res = ref.attention_backward(q, k, v, out, lse, dout, spans, R0, r)
+    for name, i in (("dq", 0), ("dk", 1), ("dv", 2)):
+        u = torch.randn(h, n, d, generator=g, dtype=torch.float64)
+        ends = []
+        for step in (1e-5, -1e-5):
+            y = [t + step * u if j == i else t for j, t in enumerate(x[:3])]
+            ends.append((ref.attention(*y, spans, R0, r)[0] * dout).sum())
+        diff = (ends[0] - ends[1]) / 2e-5
+        got = (res[name][0] * u).sum()
+        assert abs(got - diff) <= 1e-6 * (res[name][0] * u).abs().sum(), name
+
+
+@pytest.mark.parametrize("gated", [True, False])
+def test_residual_norm_backward_reference_matches_differences(gated):
+    g = torch.Generator().manual_seed(1)
+    spans, c = [3, 1, 4], 24
+    f = ref.frame_ids(spans)
+    rnd = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)
+    args = {"y": rnd(8, c), "x": rnd(8, c), "gamma_post": rnd(c), "gamma_pre": rnd(c), "gate": rnd(3, c) if gated else None}
+    dx_out, dh = rnd(8, c), rnd(8, c)
+    loss = lambda a: sum((o * w).sum() for o, w in zip(ref.residual_norm(**a, frame=f, alpha=0.7, eps=1e-6), (dx_out, dh)))
+    xn, _, rstd = ref.residual_norm(**args, frame=f, alpha=0.7, eps=1e-6)
+    dx, dy, dpost, dpre, dgate = ref.residual_norm_backward(dx_out, dh, args["y"], xn, rstd, args["gamma_post"],
+                                                            args["gamma_pre"], args["gate"], f, 0.7)
+    for name, grad in (("x", dx), ("y", dy), ("gamma_post", dpost), ("gamma_pre", dpre), ("gate", dgate)):
+        if grad is None:
+            continue
+        u = rnd(*grad.shape)
+        diff = (loss({**args, name: args[name] + 1e-5 * u}) - loss({**args, name: args[name] - 1e-5 * u})) / 2e-5
+        assert abs((grad * u).sum() - diff) <= 1e-6 * (grad * u).abs().sum(), name
+
+
+def test_checkpoint_reference_is_nearest():
+    """The search-based packing reference against torch's e4m3 conversion on
+    scaled values, and its error bound: half a step, 2^-4 of the value or
+    2^-10 of the scale."""
+    x = np.random.default_rng(0).standard_normal((64, 96)).astype(np.float32) * 3
+    codes, scales = ref.checkpoint_pack(x)
+    s = 2.0 ** (scales.astype(np.float64).repeat(32, -1) - 127)
+    want = torch.from_numpy(x / s.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(codes, want)
+    err = np.abs(ref.checkpoint_unpack(codes, scales) - x)
+    assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * s))
+
+
+P = ctypes.c_void_p
+A = 0x1000  # an aligned address; never dereferenced by a refused call
+
+
+def test_backward_refuses_without_plan():
+    lib = fas.load()
+    lib.fas_free()
+    assert lib.fas_backward(*[P(A * (i + 1)) for i in range(10)], None) == fas.FAS_ERR_STATE
+
+
+def norm_call(**kw):
+    a = dict(y=A, x=2 * A, residual=0, gate=None, gp=3 * A, gq=4 * A, alpha=1.0, eps=1e-6, tokens=4, width=64, spans=None,
+             frames=1, x_out=5 * A, h=6 * A, rstd=7 * A, yc=None, ys=None, xc=None, xs=None)
+    a.update(kw)
+    if isinstance(a["spans"], list):
+        keep = np.array(a["spans"], dtype=np.int32)
+        a["spans"] = keep.ctypes.data
+    return fas.load().fas_residual_norm(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=0), fas.FAS_ERR_ARG), (dict(width=0), fas.FAS_ERR_ARG), (dict(width=12), fas.FAS_ERR_ARG),
+    (dict(width=16392), fas.FAS_ERR_UNSUPPORTED), (dict(residual=2), fas.FAS_ERR_ARG), (dict(eps=-1.0), fas.FAS_ERR_ARG),
+    (dict(eps=float("nan")), fas.FAS_ERR_ARG), (dict(y=None), fas.FAS_ERR_ARG), (dict(rstd=None), fas.FAS_ERR_ARG),
+    (dict(x=2 * A + 8), fas.FAS_ERR_ALIGN), (dict(yc=A), fas.FAS_ERR_ARG),
+    (dict(yc=A, ys=A, xc=A, xs=A, width=72), fas.FAS_ERR_ARG),
+    (dict(gate=A, frames=0), fas.FAS_ERR_ARG), (dict(gate=A, frames=3), fas.FAS_ERR_ARG),
+    (dict(gate=A, frames=2, spans=[1, 2]), fas.FAS_ERR_ARG), (dict(gate=A, frames=2, spans=[4, 0]), fas.FAS_ERR_ARG),
+    (dict(gate=A, frames=2, spans=[5, -1]), fas.FAS_ERR_ARG),
+    (dict(gate=A, frames=1025, tokens=1025, spans=[1] * 1025), fas.FAS_ERR_UNSUPPORTED),
+])
+def test_residual_norm_refuses(kw, code):
+    assert norm_call(**kw) == code
+
+
+def norm_bwd_call(**kw):
+    a = dict(dx_out=A, dh=2 * A, y=3 * A, x_out=4 * A, residual=0, yc=None, ys=None, xc=None, xs=None, rstd=5 * A, gate=None,
+             gp=6 * A, gq=7 * A, alpha=1.0, tokens=4, width=64, spans=None, frames=1, dx=8 * A, dy=9 * A, dgate=None,
+             dgp=10 * A, dgq=11 * A, ws=12 * A, wsb=1 << 30)
+    a.update(kw)
+    return fas.load().fas_residual_norm_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=0), fas.FAS_ERR_ARG), (dict(width=20), fas.FAS_ERR_ARG), (dict(width=1 << 15), fas.FAS_ERR_UNSUPPORTED),
+    (dict(gate=A), fas.FAS_ERR_ARG), (dict(dgate=A), fas.FAS_ERR_ARG), (dict(y=None), fas.FAS_ERR_ARG),
+    (dict(yc=A, ys=A, xc=A, xs=A), fas.FAS_ERR_ARG), (dict(y=None, x_out=None, yc=A, ys=A, xc=A), fas.FAS_ERR_ARG),
+    (dict(y=None, x_out=None, yc=A, ys=A, xc=A, xs=A, width=72), fas.FAS_ERR_ARG),
+    (dict(ws=None), fas.FAS_ERR_ARG), (dict(ws=12 * A + 8), fas.FAS_ERR_ALIGN), (dict(dgp=None), fas.FAS_ERR_ARG),
+])
+def test_residual_norm_backward_refuses(kw, code):
+    assert norm_bwd_call(**kw) == code
+
+
+@pytest.mark.parametrize("args,code", [
+    ((None, 0, A, A, 32), fas.FAS_ERR_ARG), ((A, 0, A, A, 0), fas.FAS_ERR_ARG), ((A, 0, A, A, 48), fas.FAS_ERR_ARG),
+    ((A, 2, A, A, 32), fas.FAS_ERR_ARG), ((A + 4, 0, A, A, 32), fas.FAS_ERR_ALIGN), ((A, 0, A + 8, A, 32), fas.FAS_ERR_ALIGN),
+    ((A, 0, A, A, -32), fas.FAS_ERR_ARG),
+])
+def test_checkpoint_calls_refuse(args, code):
+    lib = fas.load()
+    x, dtype, codes, scales, n = args
+    assert lib.fas_checkpoint_pack(x, dtype, codes, scales, n, None) == code
+    assert lib.fas_checkpoint_unpack(codes, scales, x, dtype, n, None) == code
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    g = torch.zeros(64)
+    with pytest.raises(TypeError, match="CUDA"):
+        fas.fas_residual_norm(x, x, g, g)
+    with pytest.raises(TypeError, match="CUDA"):
+        fas.fas_residual_norm_backward(x, x, x, x, torch.zeros(2, 4), g, g)
+    with pytest.raises(TypeError):
+        fas.fas_residual_norm(x, x.half(), g, g)
+    with pytest.raises(TypeError, match="CUDA"):
+        fas.fas_checkpoint_pack(x)
+    with pytest.raises(TypeError):
+        fas.fas_checkpoint_pack(x.half())
+    with pytest.raises(TypeError):
+        fas.fas_checkpoint_unpack(x)
