@@ -439,12 +439,12 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
         _check_tensor(name, t, shape, torch.bfloat16)
         grads.append(t)
     _check_device(q, k, v, out, lse, dout, *grads)
-    delta = torch.empty(_lse_shape(), dtype=torch.float32, device=q.device)
+    stats = torch.empty((2, *_lse_shape()), dtype=torch.float32, device=q.device)
     rc = load().fas_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              dout.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
-                             delta.data_ptr(), _stream_handle(stream))
+                             stats.data_ptr(), _stream_handle(stream))
     _check("fas_backward", rc)
-    _own_until_run(stream, delta, *grads)
+    _own_until_run(stream, stats, *grads)
     return tuple(grads)
 
 

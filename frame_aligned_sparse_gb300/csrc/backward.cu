@@ -1,17 +1,40 @@
-// Backward pass of the frame-aligned sparse attention.
+// Backward pass of the frame-aligned sparse attention for sm_103a.
 //
 // With s = 1/sqrt(d), for row i and the keys j its frame sees:
 //   P_ij = exp(s q_i.k_j - lse_i)          (recomputed, lse from the forward)
 //   delta_i = sum_c dout_ic out_ic         dS_ij = P_ij (dout_i.v_j - delta_i)
 //   dq_i = s sum_j dS_ij k_j    dk_j = s sum_i dS_ij q_i    dv_j = sum_i P_ij dout_i
 // Visibility is symmetric in the frames, so the queries that see a key frame
-// are the same table ranges that the frame's own queries see.  Two kernels,
-// each output row written once by one warp: no atomics, results are
-// bit-reproducible.
+// are the same table ranges that the frame's own queries see, and both
+// passes walk the plan's work list ("Deleting the Mask": the visible tokens
+// are at most two contiguous ranges).
+//
+// Two kernels.  The query pass owns 128 query rows and accumulates dq over
+// the visible keys; the key pass owns 128 key rows and accumulates dk and dv
+// over the queries that see them.  Together they compute S and dP twice (7
+// products for the 5 that the gradients need), but every gradient stays in
+// TMEM until its one store: no fp32 gradient goes through memory, no atomics,
+// bit-reproducible results.
+//
+// A visible range is walked in blocks; its last block is shortened to the
+// tokens it has (a multiple of 16) through the MMA's N or its K steps, so no
+// hidden token enters a product, whatever it holds, and no mask is needed.
+//
+// Precision: S, dP, the gradients, P and dS are fp32; P and dS are rounded to
+// bf16 as operands of the products, as P is in the forward.  Since sum_j
+// dS_ij = 0 up to out's rounding, a common component c of the keys cancels in
+// dq, but the roundings of dS times c do not: the query pass sums what
+// rounding added to each row and takes it out along c (the mean of the first
+// block's keys), which leaves the roundings times k - c.  (Keys with a common
+// component three times their spread, as the prepass's mean-centring is for,
+// tripled dq's error without it.)
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
+#include "attention_core.cuh"
 #include "fas.h"
 #include "internal.h"
 #include "kernels.h"
@@ -20,94 +43,707 @@
 namespace fas {
 namespace {
 
-constexpr int kWarpsB = 8;
+using core::drain_wait;
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+constexpr int kRowsB = kQTile;  // rows of a work item (MMA M)
+constexpr int kSoftThreads = 256;
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10;
+constexpr int kThreadsB = 32 * 11;
+constexpr int kMaxStagesB = 6;
+constexpr uint32_t kTmemAll = 512;
+constexpr float kLog2eB = 1.4426950408889634f;
+
+// Blocks of one item's two visible ranges.
+struct Blocks {
+  int4 r;
+  int nb0, nb;
+  int B;
+  __device__ __forceinline__ Blocks(int4 rng, int b) : r(rng), nb0((rng.y + b - 1) / b), B(b) {
+    nb = nb0 + (rng.w + b - 1) / b;
+  }
+  __device__ __forceinline__ int start(int j) const { return j < nb0 ? r.x + j * B : r.z + (j - nb0) * B; }
+  __device__ __forceinline__ int count(int j) const {
+    const int left = j < nb0 ? r.y - j * B : r.w - (j - nb0) * B;
+    return left < B ? left : B;
+  }
+};
+
+struct BarsB {
+  uint64_t tile_full;
+  uint64_t full[2][kMaxStagesB];   // [ring][stage]
+  uint64_t empty[2][kMaxStagesB];
+  uint64_t s_full[2], dp_full[2];
+  uint64_t s_free[2];              // query pass: S read into registers
+  uint64_t p_full, ds_full[2];
+  uint64_t acc_full, drain;
+  uint32_t tmem_base;
+  int abort, skip;
+};
+
+__device__ __forceinline__ void init_bars(BarsB& b, int soft_arrivals) {
+  auto one = [](uint64_t& x, int n) { ptx::mbar_init(ptx::smem_addr(&x), n); };
+  one(b.tile_full, 1);
+  for (int i = 0; i < 2; ++i) {
+    for (int s = 0; s < kMaxStagesB; ++s) {
+      one(b.full[i][s], 1);
+      one(b.empty[i][s], 1);
+    }
+    one(b.s_full[i], 1);
+    one(b.dp_full[i], 1);
+    one(b.s_free[i], soft_arrivals);
+    one(b.ds_full[i], soft_arrivals);
+  }
+  one(b.p_full, soft_arrivals);
+  one(b.acc_full, 1);
+  one(b.drain, 1);
+  b.abort = 0;
+  ptx::fence_mbar_init();
+  ptx::fence_proxy_async_smem();
 }
 
-// One lane's D / 32 consecutive elements of a bf16 row.
+// 1D bulk copy (16-byte aligned addresses, bytes a multiple of 16).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Loads a 128-row tile: by frame (rows past the frame's end read zeros), or
+// by token when frames are ragged (the next frame's rows, computed and
+// discarded).
 template <int D>
-__device__ __forceinline__ void load_row(const uint16_t* p, int lane, float (&x)[D / 32]) {
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, const BwdParams& p,
+                                          int first, int f, int h, int t) {
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(p)[lane * (D / 64) + e];
-    x[2 * e] = __uint_as_float(w << 16);
-    x[2 * e + 1] = __uint_as_float(w & 0xFFFF0000u);
+  for (int half = 0; half < D / 64; ++half) {
+    if (p.by_frame)
+      ptx::tma_load_4d(dst + half * (kRowsB * 128), tm, bar, half * 64, t * kRowsB, f, h);
+    else
+      ptx::tma_load_3d(dst + half * (kRowsB * 128), tm, bar, half * 64, first + t * kRowsB, h);
   }
 }
-template <int D>
-__device__ __forceinline__ void store_row(uint16_t* p, int lane, const float (&x)[D / 32], float scale) {
+
+// One ring's producer: block j into stage j % depth.  kStats: the blocks'
+// softmax statistics (two fp32 rows of N) travel with it.
+template <int D, int B, bool kStats>
+__device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap* tm, int depth, uint32_t s0, int h,
+                                        const Blocks& blk, const BwdParams& p, uint32_t stat_s0) {
+  constexpr uint32_t kBytes = B * D * 2;
+  volatile int* abort_flag = &bars.abort;
+  int j = 0;
+  bool ok = true;
+  for (; j < blk.nb; ++j) {
+    const int st = j % depth, u = j / depth;
+    if (u >= 1) ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.empty[ring][st]), (u - 1) & 1, abort_flag, p.err,
+                                          kErrWaitProducer, p.limit_ns);
+    if (!ok) break;
+    const uint32_t fb = ptx::smem_addr(&bars.full[ring][st]);
+    const uint32_t n4 = kStats ? (uint32_t)blk.count(j) * 4 : 0;
+    ptx::mbar_arrive_expect_tx(fb, kBytes + 2 * n4);
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e)
-    reinterpret_cast<uint32_t*>(p)[lane * (D / 64) + e] = ptx::pack_bf16x2(x[2 * e] * scale, x[2 * e + 1] * scale);
+    for (int half = 0; half < D / 64; ++half)
+      ptx::tma_load_3d(s0 + st * kBytes + half * (B * 128), tm, fb, half * 64, blk.start(j), h);
+    if (kStats) {
+      const float* src = p.stats + (int64_t)h * p.N + blk.start(j);
+      bulk_load(stat_s0 + st * (2 * B * 4), src, n4, fb);
+      bulk_load(stat_s0 + st * (2 * B * 4) + B * 4, src + (int64_t)p.H * p.N, n4, fb);
+    }
+  }
+  if (!ok)  // let every copy this thread started land before the CTA exits
+    for (int i = (j > depth ? j - depth : 0); i < j; ++i)
+      drain_wait(ptx::smem_addr(&bars.full[ring][i % depth]), (i / depth) & 1, p.err, p.limit_ns);
 }
 
-// A warp per row of the tile: query rows (kKeys false: delta and dq) or key
-// rows (dk and dv), over the visible tokens of the other side.
-template <int D, bool kKeys>
-__global__ void __launch_bounds__(32 * kWarpsB) attention_bwd(const BwdParams p) {
-  constexpr int E = D / 32;
-  const int4 item = p.work[blockIdx.x];
-  const int h = item.x, f = item.y;
-  const int lane = threadIdx.x % 32;
-  const int2 sp = p.spans[f];
-  const int4 rng = p.table[f];
-  const int64_t hb = (int64_t)h * p.head_stride, lb = (int64_t)h * p.N;
-  for (int r = item.z * kQTile + threadIdx.x / 32; r < min((item.z + 1) * kQTile, sp.y); r += kWarpsB) {
-    const int64_t row = (int64_t)sp.x + r, at = hb + row * p.row_stride;
-    float a[E], b[E], g0[E] = {}, g1[E] = {};  // (q, dout) or (k, v); dq or (dk, dv)
-    load_row<D>((kKeys ? p.k : p.q) + at, lane, a);
-    load_row<D>((kKeys ? p.v : p.dout) + at, lane, b);
-    float lse = 0.f, delta = 0.f;
-    if (!kKeys) {
-      float o[E];
-      load_row<D>(p.out + at, lane, o);
+// D[128 x n] = A[128 x D] . B^T, A in TMEM (bf16 pairs) or K-major shared
+// memory, B the first n rows of a K-major block of kB rows.
+template <int D, int kB, bool kATmem>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint64_t a_desc, uint64_t b_desc, int n) {
+  const uint32_t idesc = ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false);
 #pragma unroll
-      for (int e = 0; e < E; ++e) delta = fmaf(b[e], o[e], delta);
-      delta = warp_sum(delta);
-      lse = p.lse[lb + row];
-      if (lane == 0) p.delta[lb + row] = delta;
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t b = b_desc + (((kk >> 2) * (kB * 128) + (kk & 3) * 32) >> 4);
+    if (kATmem)
+      ptx::mma_ts(d, a_tmem + kk * 8, b, idesc, kk > 0 ? 1u : 0u);
+    else
+      ptx::mma_ss(d, a_desc + (((kk >> 2) * (kRowsB * 128) + (kk & 3) * 32) >> 4), b, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+// D[128 x D] += A[128 x n] . B[n x D]: A's bf16 chunks of 16 columns in TMEM
+// (each in the first 8 columns of its 16), B a block read along its rows.
+template <int D, int kB>
+__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t b_desc, int n, bool first) {
+  constexpr uint32_t idesc = ptx::idesc_bf16_f32(kRowsB, D, true);
+  if (n == kB) {
+#pragma unroll
+    for (int kk = 0; kk < kB / 16; ++kk)
+      ptx::mma_ts(d, a + kk * 16, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
+  } else {
+    for (int kk = 0; kk < n / 16; ++kk)
+      ptx::mma_ts(d, a + kk * 16, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
+  }
+}
+
+// A 128-row K-major tile into TMEM as an A operand.
+template <int D>
+__device__ __forceinline__ void tile_to_tmem(uint32_t col, uint64_t desc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    ptx::tmem_cp_128x256b(col + kk * 8, desc + (((kk >> 2) * (kRowsB * 128) + (kk & 3) * 32) >> 4));
+}
+
+// Writes 16 * N columns of an fp32 accumulator row, scaled, as bf16.
+template <int N>
+__device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float scale, bool valid) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    uint32_t o[16];
+    ptx::tmem_ld16(taddr + u * 16, o);
+    ptx::tmem_ld_wait(o);
+    uint32_t pk[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      pk[e] = ptx::pack_bf16x2(__uint_as_float(o[2 * e]) * scale, __uint_as_float(o[2 * e + 1]) * scale);
+    if (valid) {
+      uint4* d4 = reinterpret_cast<uint4*>(dst + u * 16);
+      d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
     }
-    for (int part = 0; part < 2; ++part) {
-      const int t0 = part ? rng.z : rng.x, n = part ? rng.w : rng.y;
-      for (int t = t0; t < t0 + n; ++t) {
-        const int64_t ot = hb + (int64_t)t * p.row_stride;
-        float c[E], e2[E];
-        load_row<D>((kKeys ? p.q : p.k) + ot, lane, c);
-        load_row<D>((kKeys ? p.dout : p.v) + ot, lane, e2);
-        if (kKeys) {
-          lse = p.lse[lb + t];
-          delta = p.delta[lb + t];
+  }
+}
+
+// Common start of both kernels: error check, barriers, TMEM.
+#define FAS_BWD_PROLOGUE(soft_arrivals)                                                              \
+  if (threadIdx.x == 0) bars.skip = *reinterpret_cast<volatile unsigned int*>(p.err) != 0u;          \
+  __syncthreads();                                                                                   \
+  if (bars.skip) return;                                                                             \
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;                                        \
+  const int4 item = p.work[blockIdx.x];                                                              \
+  const int h = item.x, f = item.y, tile = item.z;                                                   \
+  const int2 sp = p.spans[f];                                                                        \
+  if (threadIdx.x == 0) init_bars(bars, soft_arrivals);                                              \
+  if (warp == kWarpMma) {                                                                            \
+    ptx::tmem_alloc(ptx::smem_addr(&bars.tmem_base), kTmemAll);                                      \
+    ptx::tmem_relinquish();                                                                          \
+  }                                                                                                  \
+  ptx::tc_fence_before_sync();                                                                       \
+  __syncthreads();                                                                                   \
+  ptx::tc_fence_after_sync();                                                                        \
+  const uint32_t tmem = bars.tmem_base;                                                              \
+  volatile int* abort_flag = &bars.abort
+
+// ------------------------------------------------------------- query pass
+//
+// Q and dO of the tile sit in TMEM as A operands; K and V blocks of 64 keys
+// stream through two rings.  Two S and two dP buffers: warpgroup g takes the
+// blocks j with j % 2 == g, so each group's waits hide behind the other's
+// arithmetic.  Tensor order: S(j+2), dQ(j), dP(j+2) for j = 0, 1, ...: S(j+2)
+// only needs S(j) to have been read into registers, and the group has 1024
+// clocks of tensor work (at d = 128) between the end of dP(j) and dQ(j).
+constexpr int kBq = 64;  // keys per block
+
+template <int D>
+struct QLayout {
+  static constexpr uint32_t kAcc = 0, kS = D, kDp = D + 2 * kBq, kQ = D + 4 * kBq, kDo = kQ + D / 2;
+  static_assert(kDo + D / 2 <= kTmemAll, "TMEM columns");
+  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBq * D * 2;
+  static constexpr int kStK = D == 128 ? 5 : 6, kStV = D == 128 ? 4 : 6;  // K blocks stay from S(j) to dQ(j)
+  static constexpr size_t kSmem = 1024 + 2 * kTile + (kStK + kStV) * kBlock;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    attention_bwd_q(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const BwdParams p) {
+  using L = QLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ BarsB bars;
+  __shared__ float red[4][128];  // partial sums: delta halves, then the keys' mean, then the rows' roundings
+  __shared__ float centre[D];
+  const uint32_t q_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t do_s = q_s + L::kTile, k_s0 = do_s + L::kTile, v_s0 = k_s0 + L::kStK * L::kBlock;
+  FAS_BWD_PROLOGUE(128);
+  const Blocks blk(p.table[f], kBq);
+
+  if (warp == kWarpK || warp == kWarpV) {
+    if (lane == 0) {
+      if (warp == kWarpK) {
+        const uint32_t tb = ptx::smem_addr(&bars.tile_full);
+        ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
+        load_tile<D>(q_s, &tm_q, tb, p, sp.x, f, h, tile);
+        load_tile<D>(do_s, &tm_do, tb, p, sp.x, f, h, tile);
+        produce<D, kBq, false>(bars, 0, &tm_k, L::kStK, k_s0, h, blk, p, 0);
+        if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
+      } else {
+        produce<D, kBq, false>(bars, 1, &tm_v, L::kStV, v_s0, h, blk, p, 0);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    if (ptx::elect_one()) {
+      auto wait = [&](uint64_t& b, int parity) {
+        return ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitMma, p.limit_ns);
+      };
+      const uint64_t kd = ptx::smem_desc_sw128(k_s0, 16, 1024), vd = ptx::smem_desc_sw128(v_s0, 16, 1024);
+      const uint64_t kmn = ptx::smem_desc_sw128(k_s0, kBq * 128, 1024);
+      constexpr uint64_t kStep = L::kBlock >> 4;
+      auto s_mma = [&](int j) {
+        const int st = j % L::kStK;
+        if (!wait(bars.full[0][st], j / L::kStK)) return false;
+        mma_rows<D, kBq, true>(tmem + L::kS + (j & 1) * kBq, tmem + L::kQ, 0, kd + st * kStep, blk.count(j));
+        ptx::mma_commit(ptx::smem_addr(&bars.s_full[j & 1]));
+        return true;
+      };
+      auto dp_mma = [&](int j) {
+        const int st = j % L::kStV;
+        if (!wait(bars.full[1][st], j / L::kStV)) return false;
+        mma_rows<D, kBq, true>(tmem + L::kDp + (j & 1) * kBq, tmem + L::kDo, 0, vd + st * kStep, blk.count(j));
+        ptx::mma_commit(ptx::smem_addr(&bars.dp_full[j & 1]));
+        ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
+        return true;
+      };
+      bool ok = wait(bars.tile_full, 0);
+      if (ok) {
+        tile_to_tmem<D>(tmem + L::kQ, ptx::smem_desc_sw128(q_s, 16, 1024));
+        tile_to_tmem<D>(tmem + L::kDo, ptx::smem_desc_sw128(do_s, 16, 1024));
+      }
+      for (int j = 0; ok && j < 2 && j < blk.nb; ++j) ok = s_mma(j) && dp_mma(j);
+      for (int j = 0; ok && j < blk.nb; ++j) {
+        const bool more = j + 2 < blk.nb;
+        if (more) {
+          ok = wait(bars.s_free[j & 1], j >> 1);
+          ptx::tc_fence_after_sync();
+          ok = ok && s_mma(j + 2);
         }
-        float s = 0.f, dp = 0.f;
+        ok = ok && wait(bars.ds_full[j & 1], j >> 1);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        mma_acc<D, kBq>(tmem + L::kAcc, tmem + L::kDp + (j & 1) * kBq, kmn + (j % L::kStK) * kStep, blk.count(j),
+                        j == 0);
+        ptx::mma_commit(ptx::smem_addr(&bars.empty[0][j % L::kStK]));
+        if (more) ok = dp_mma(j + 2);
+      }
+      ptx::mma_commit(ptx::smem_addr(&bars.acc_full));
+      ptx::mma_commit(ptx::smem_addr(&bars.drain));
+      drain_wait(ptx::smem_addr(&bars.drain), 0, p.err, p.limit_ns);
+      if (!ok) bars.abort = 1;
+    }
+    __syncwarp();
+  } else {
+    const int g = warp / 4, trow = (warp % 4) * 32 + lane, tid = threadIdx.x;
+    const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
+    const int row = tile * kRowsB + trow;
+    const bool valid = row < sp.y;
+    const int64_t token = (int64_t)sp.x + row, at = (int64_t)h * p.head_stride + token * p.row_stride;
+    auto wait = [&](uint64_t& b, int parity) {
+      const bool got = ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitSoftmax,
+                                             p.limit_ns);
+      return (bool)__all_sync(0xffffffffu, got);
+    };
+    // delta: each group takes half of the row's columns.
+    float delta = 0.f;
+    if (valid) {
+      const uint4* o4 = reinterpret_cast<const uint4*>(p.out + at + g * (D / 2));
+      const uint4* d4 = reinterpret_cast<const uint4*>(p.dout + at + g * (D / 2));
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          s = fmaf(a[e], c[e], s);
-          dp = fmaf(b[e], e2[e], dp);
-        }
-        s = warp_sum(s);
-        dp = warp_sum(dp);
-        const float pr = __expf(s * p.scale - lse), ds = pr * (dp - delta);
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 a = o4[c], b = d4[c];
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          g0[e] = fmaf(ds, c[e], g0[e]);
-          if (kKeys) g1[e] = fmaf(pr, e2[e], g1[e]);
+        for (int e = 0; e < 4; ++e) {
+          delta = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(bw[e] << 16), delta);
+          delta = fmaf(__uint_as_float(aw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), delta);
         }
       }
     }
-    store_row<D>((kKeys ? p.dk : p.dq) + at, lane, g0, p.scale);
-    if (kKeys) store_row<D>(p.dv + at, lane, g1, 1.f);
+    red[g][trow] = delta;
+    ptx::named_barrier_sync(1, kSoftThreads);
+    delta = red[0][trow] + red[1][trow];
+    // A row past the frame's end gets P = 0 and is never stored.
+    const float nl = valid ? -p.lse[(int64_t)h * p.N + token] * kLog2eB : -INFINITY;
+    if (valid && g == 0) {
+      float* st = p.stats + (int64_t)h * p.N + token;
+      st[0] = nl;
+      st[(int64_t)p.H * p.N] = -delta;
+    }
+    ptx::named_barrier_sync(1, kSoftThreads);
+    // The mean of the first block's keys, from its shared-memory stage (the
+    // 128-byte swizzle permutes the 16-byte pieces of a row by row % 8).
+    bool ok = wait(bars.full[0][0], 0);
+    {
+      constexpr int kParts = kSoftThreads / (D / 2);
+      const int cp = tid % (D / 2), part = tid / (D / 2), n = blk.count(0);
+      float c0 = 0.f, c1 = 0.f;
+      if (ok)
+        for (int r = part; r < n; r += kParts) {
+          const uint32_t off = (cp / 32) * (kBq * 128) + r * 128 + ((((cp % 32) / 4) ^ (r & 7)) * 16) + (cp % 4) * 4;
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(smem_raw + (k_s0 - ptx::smem_addr(smem_raw)) + off);
+          c0 += __uint_as_float(w << 16);
+          c1 += __uint_as_float(w & 0xFFFF0000u);
+        }
+      red[0][part * D + 2 * cp] = c0;
+      red[0][part * D + 2 * cp + 1] = c1;
+      ptx::consume(c0, c1);
+      ptx::fence_proxy_async_smem();
+      ptx::named_barrier_sync(1, kSoftThreads);
+      if (tid < D) {
+        float c = 0.f;
+        for (int i = 0; i < kParts; ++i) c += red[0][i * D + tid];
+        centre[tid] = c / (float)n;
+      }
+      ptx::named_barrier_sync(1, kSoftThreads);
+    }
+    const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB), nl2 = ptx::f32x2(nl, nl);
+    const float nd = -delta;
+    float e0 = 0.f, e1 = 0.f;  // what rounding dS to bf16 added to the row
+    constexpr int kCh = kBq / 16;
+    for (int j = g; ok && j < blk.nb; j += 2) {
+      const int nch = blk.count(j) / 16;
+      ok = wait(bars.s_full[g], j >> 1);
+      if (!ok) break;
+      ptx::tc_fence_after_sync();
+      uint32_t r[kCh][16];
+      core::load_chunks<0, kCh>(tmem + lane_base + L::kS + g * kBq, r);
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(ptx::smem_addr(&bars.s_free[g]));
+      float pr[kCh][16];
+#pragma unroll
+      for (int u = 0; u < kCh; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x0, x1;
+          ptx::fma_f32x2(x0, x1, __uint_as_float(r[u][2 * e]), __uint_as_float(r[u][2 * e + 1]), c2, nl2);
+          pr[u][2 * e] = ptx::ex2(x0);
+          pr[u][2 * e + 1] = ptx::ex2(x1);
+        }
+      ok = wait(bars.dp_full[g], j >> 1);
+      if (!ok) break;
+      ptx::tc_fence_after_sync();
+      const uint32_t dbase = tmem + lane_base + L::kDp + g * kBq;
+      core::load_chunks<0, kCh>(dbase, r);
+#pragma unroll
+      for (int u = 0; u < kCh; ++u) {
+        uint32_t pk[8];
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x0 = __uint_as_float(r[u][2 * e]), x1 = __uint_as_float(r[u][2 * e + 1]);
+          ptx::add_f32x2(x0, x1, nd, nd);
+          mul_f32x2(x0, x1, x0, x1, pr[u][2 * e], pr[u][2 * e + 1]);
+          pk[e] = ptx::pack_bf16x2(x0, x1);
+          ptx::add_f32x2(a0, a1, __uint_as_float(pk[e] << 16) - x0, __uint_as_float(pk[e] & 0xFFFF0000u) - x1);
+        }
+        // Columns past the range's end hold leftovers: not part of the sum.
+        e0 += u < nch ? a0 : 0.f;
+        e1 += u < nch ? a1 : 0.f;
+        ptx::tmem_st8(dbase + u * 16, pk);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[g]));
+    }
+    red[g][trow] = e0 + e1;
+    ok = ok && wait(bars.acc_full, 0);
+    ptx::named_barrier_sync(1, kSoftThreads);
+    if (ok && !bars.abort) {
+      ptx::tc_fence_after_sync();
+      const float extra = red[0][trow] + red[1][trow];
+      constexpr int kOut = D / 32;  // chunks of 16 columns per group
+#pragma unroll
+      for (int u = 0; u < kOut; ++u) {
+        const int c0 = (g * kOut + u) * 16;
+        uint32_t o[16], pk[8];
+        ptx::tmem_ld16(tmem + lane_base + L::kAcc + c0, o);
+        ptx::tmem_ld_wait(o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          pk[e] = ptx::pack_bf16x2(fmaf(-extra, centre[c0 + 2 * e], __uint_as_float(o[2 * e])) * p.scale,
+                                   fmaf(-extra, centre[c0 + 2 * e + 1], __uint_as_float(o[2 * e + 1])) * p.scale);
+        if (valid) {
+          uint4* d4 = reinterpret_cast<uint4*>(p.dq + at + c0);
+          d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+      }
+    }
   }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+// --------------------------------------------------------------- key pass
+//
+// Rows are keys, so S and dP are computed transposed: S^T = K.Q^T and dP^T =
+// V.dO^T with the tile's K and V as A operands and blocks of Q and dO as B;
+// P^T and dS^T then are the A operands of dv += P^T.dO and dk += dS^T.Q, whose
+// B operands are the same Q and dO blocks read along their rows.  The two
+// accumulators and one S^T and dP^T buffer each fill TMEM; both warpgroups
+// work on the same block, each on half of its columns.  Tensor order: dV(j),
+// S(j+1), dK(j), dP(j+1): P(j+1) is computed under dK(j) and dP(j+1), dS(j)
+// under dV(j) and S(j+1).
+template <int D, int BQ, bool kKT, bool kVT>
+struct KLayout {
+  static constexpr uint32_t kDk = 0, kDv = D, kS = 2 * D, kDp = 2 * D + BQ, kK = 2 * D + 2 * BQ,
+                            kV = kK + (kKT ? D / 2 : 0);
+  static_assert(kV + (kVT ? D / 2 : 0) <= kTmemAll, "TMEM columns");
+  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = BQ * D * 2;
+  static constexpr int kFit = (int)((232448 - 1024 - 2 * kTile - 1024 - 2048) / (2 * kBlock + 2 * BQ * 4));
+  static constexpr int kStages = kFit < kMaxStagesB ? kFit : kMaxStagesB;
+  static constexpr size_t kSmem = 1024 + 2 * kTile + 2 * kStages * kBlock + kStages * 2 * BQ * 4;
+};
+
+template <int D, int BQ, bool kKT, bool kVT>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    attention_bwd_k(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                    const BwdParams p) {
+  using L = KLayout<D, BQ, kKT, kVT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ BarsB bars;
+  const uint32_t k_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t v_s = k_s + L::kTile, q_s0 = v_s + L::kTile, do_s0 = q_s0 + L::kStages * L::kBlock;
+  const uint32_t stat_s0 = do_s0 + L::kStages * L::kBlock;
+  FAS_BWD_PROLOGUE(kSoftThreads);
+  const Blocks blk(p.table[f], BQ);
+
+  if (warp == kWarpK || warp == kWarpV) {
+    if (lane == 0) {
+      if (warp == kWarpK) {
+        const uint32_t tb = ptx::smem_addr(&bars.tile_full);
+        ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
+        load_tile<D>(k_s, &tm_k, tb, p, sp.x, f, h, tile);
+        load_tile<D>(v_s, &tm_v, tb, p, sp.x, f, h, tile);
+        produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
+        if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
+      } else {
+        produce<D, BQ, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    if (ptx::elect_one()) {
+      auto wait = [&](uint64_t& b, int parity) {
+        return ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitMma, p.limit_ns);
+      };
+      const uint64_t kdesc = ptx::smem_desc_sw128(k_s, 16, 1024), vdesc = ptx::smem_desc_sw128(v_s, 16, 1024);
+      const uint64_t qd = ptx::smem_desc_sw128(q_s0, 16, 1024), dod = ptx::smem_desc_sw128(do_s0, 16, 1024);
+      const uint64_t qmn = ptx::smem_desc_sw128(q_s0, BQ * 128, 1024), domn = ptx::smem_desc_sw128(do_s0, BQ * 128, 1024);
+      constexpr uint64_t kStep = L::kBlock >> 4;
+      auto s_mma = [&](int j) {
+        const int st = j % L::kStages;
+        if (!wait(bars.full[0][st], j / L::kStages)) return false;
+        mma_rows<D, BQ, kKT>(tmem + L::kS, tmem + L::kK, kdesc, qd + st * kStep, blk.count(j));
+        ptx::mma_commit(ptx::smem_addr(&bars.s_full[0]));
+        return true;
+      };
+      auto dp_mma = [&](int j) {
+        const int st = j % L::kStages;
+        if (!wait(bars.full[1][st], j / L::kStages)) return false;
+        mma_rows<D, BQ, kVT>(tmem + L::kDp, tmem + L::kV, vdesc, dod + st * kStep, blk.count(j));
+        ptx::mma_commit(ptx::smem_addr(&bars.dp_full[0]));
+        return true;
+      };
+      bool ok = wait(bars.tile_full, 0);
+      if (ok) {
+        if (kKT) tile_to_tmem<D>(tmem + L::kK, kdesc);
+        if (kVT) tile_to_tmem<D>(tmem + L::kV, vdesc);
+        ok = s_mma(0) && dp_mma(0);
+      }
+      for (int j = 0; ok && j < blk.nb; ++j) {
+        const int st = j % L::kStages, n = blk.count(j);
+        const bool more = j + 1 < blk.nb;
+        ok = wait(bars.p_full, j);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        mma_acc<D, BQ>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
+        if (more) ok = s_mma(j + 1);
+        ok = ok && wait(bars.ds_full[0], j);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        mma_acc<D, BQ>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
+        ptx::mma_commit(ptx::smem_addr(&bars.empty[0][st]));
+        if (more) ok = dp_mma(j + 1);
+      }
+      ptx::mma_commit(ptx::smem_addr(&bars.acc_full));
+      ptx::mma_commit(ptx::smem_addr(&bars.drain));
+      drain_wait(ptx::smem_addr(&bars.drain), 0, p.err, p.limit_ns);
+      if (!ok) bars.abort = 1;
+    }
+    __syncwarp();
+  } else {
+    const int g = warp / 4, trow = (warp % 4) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
+    auto wait = [&](uint64_t& b, int parity) {
+      const bool got = ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitSoftmax,
+                                             p.limit_ns);
+      return (bool)__all_sync(0xffffffffu, got);
+    };
+    const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB);
+    constexpr int kCh = BQ / 32;  // chunks of 16 columns per group
+    const float* const stat0 =
+        reinterpret_cast<const float*>(smem_raw + (stat_s0 - ptx::smem_addr(smem_raw))) + g * (BQ / 2);
+    const uint32_t sbase = tmem + lane_base + L::kS + g * (BQ / 2), dbase = tmem + lane_base + L::kDp + g * (BQ / 2);
+    bool ok = true;
+    for (int j = 0; ok && j < blk.nb; ++j) {
+      const int st = j % L::kStages;
+      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(stat0 + st * (2 * BQ));
+      const float4* nd = reinterpret_cast<const float4*>(stat0 + st * (2 * BQ) + BQ);
+      // The block's statistics came with its Q block (complete before S).
+      ok = wait(bars.full[0][st], j / L::kStages) && wait(bars.s_full[0], j);
+      if (!ok) break;
+      ptx::tc_fence_after_sync();
+      uint32_t r[kCh][16];
+      core::load_chunks<0, kCh>(sbase, r);
+      float pr[kCh][16];
+#pragma unroll
+      for (int u = 0; u < kCh; ++u) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const ulonglong2 l = nl[u * 4 + e];
+          float x0, x1, x2, x3;
+          ptx::fma_f32x2(x0, x1, __uint_as_float(r[u][4 * e]), __uint_as_float(r[u][4 * e + 1]), c2, l.x);
+          ptx::fma_f32x2(x2, x3, __uint_as_float(r[u][4 * e + 2]), __uint_as_float(r[u][4 * e + 3]), c2, l.y);
+          pr[u][4 * e] = ptx::ex2(x0);
+          pr[u][4 * e + 1] = ptx::ex2(x1);
+          pr[u][4 * e + 2] = ptx::ex2(x2);
+          pr[u][4 * e + 3] = ptx::ex2(x3);
+          pk[2 * e] = ptx::pack_bf16x2(pr[u][4 * e], pr[u][4 * e + 1]);
+          pk[2 * e + 1] = ptx::pack_bf16x2(pr[u][4 * e + 2], pr[u][4 * e + 3]);
+        }
+        ptx::tmem_st8(sbase + u * 16, pk);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(ptx::smem_addr(&bars.p_full));
+      ok = wait(bars.dp_full[0], j);
+      if (!ok) break;
+      ptx::tc_fence_after_sync();
+      core::load_chunks<0, kCh>(dbase, r);
+#pragma unroll
+      for (int u = 0; u < kCh; ++u) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 d = nd[u * 4 + e];
+          float x0 = __uint_as_float(r[u][4 * e]), x1 = __uint_as_float(r[u][4 * e + 1]);
+          float x2 = __uint_as_float(r[u][4 * e + 2]), x3 = __uint_as_float(r[u][4 * e + 3]);
+          ptx::add_f32x2(x0, x1, d.x, d.y);
+          ptx::add_f32x2(x2, x3, d.z, d.w);
+          mul_f32x2(x0, x1, x0, x1, pr[u][4 * e], pr[u][4 * e + 1]);
+          mul_f32x2(x2, x3, x2, x3, pr[u][4 * e + 2], pr[u][4 * e + 3]);
+          pk[2 * e] = ptx::pack_bf16x2(x0, x1);
+          pk[2 * e + 1] = ptx::pack_bf16x2(x2, x3);
+        }
+        ptx::tmem_st8(dbase + u * 16, pk);
+      }
+      ptx::tmem_st_wait();
+      // The statistics' stage goes back to the producer behind dK(j): these
+      // reads come before its next copy.
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[0]));
+    }
+    ok = ok && wait(bars.acc_full, 0);
+    if (ok && !bars.abort) {
+      ptx::tc_fence_after_sync();
+      const int row = tile * kRowsB + trow;
+      const int64_t at = (int64_t)h * p.head_stride + ((int64_t)sp.x + row) * p.row_stride;
+      if (g == 0)
+        store_acc<D / 16>(tmem + lane_base + L::kDk, p.dk + at, p.scale, row < sp.y);
+      else
+        store_acc<D / 16>(tmem + lane_base + L::kDv, p.dv + at, 1.f, row < sp.y);
+    }
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+#undef FAS_BWD_PROLOGUE
+
+#ifndef FAS_BWD_BQ
+#define FAS_BWD_BQ 96
+#endif
+#ifndef FAS_BWD_KT
+#define FAS_BWD_KT false
+#endif
+#ifndef FAS_BWD_VT
+#define FAS_BWD_VT true
+#endif
+
+// Queries per block of the key pass, and which operand tiles go to TMEM.
+template <int D>
+struct KConfig;
+template <>
+struct KConfig<128> {
+  static constexpr int kB = FAS_BWD_BQ;
+  static constexpr bool kKT = FAS_BWD_KT, kVT = FAS_BWD_VT;
+};
+template <>
+struct KConfig<64> {
+  static constexpr int kB = 128;
+  static constexpr bool kKT = true, kVT = true;
+};
+
+// Tensor maps: 128-row tiles ({d, T, Nf, H} by frame or {d, N, H} by token)
+// and blocks of `box` tokens.
+int tile_map(CUtensorMap* m, const void* base, int d, const BwdParams& p) {
+  const cuuint64_t D = (cuuint64_t)d, rs = (cuuint64_t)p.row_stride * 2, hs = (cuuint64_t)p.head_stride * 2;
+  if (p.by_frame) {
+    const cuuint64_t dims[4] = {D, (cuuint64_t)p.T, (cuuint64_t)p.Nf, (cuuint64_t)p.H};
+    const cuuint64_t strides[3] = {rs, (cuuint64_t)p.T * rs, hs};
+    const cuuint32_t box[4] = {64, (cuuint32_t)kRowsB, 1, 1};
+    return bf16_tensor_map(m, base, 4, dims, strides, box);
+  }
+  const cuuint64_t dims[3] = {D, (cuuint64_t)p.N, (cuuint64_t)p.H};
+  const cuuint64_t strides[2] = {rs, hs};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kRowsB, 1};
+  return bf16_tensor_map(m, base, 3, dims, strides, box);
+}
+int block_map(CUtensorMap* m, const void* base, int d, int rows, const BwdParams& p) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.N, (cuuint64_t)p.H};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.row_stride * 2, (cuuint64_t)p.head_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  return bf16_tensor_map(m, base, 3, dims, strides, box);
 }
 
 template <int D>
 int launch(const BwdParams& p, int grid, cudaStream_t st) {
-  attention_bwd<D, false><<<grid, 32 * kWarpsB, 0, st>>>(p);
+  using C = KConfig<D>;
+  using LQ = QLayout<D>;
+  using LK = KLayout<D, C::kB, C::kKT, C::kVT>;
+  CUtensorMap tq, tdo, tk, tv, bq, bdo, bk, bv;
+  if (tile_map(&tq, p.q, D, p) != FAS_OK || tile_map(&tdo, p.dout, D, p) != FAS_OK ||
+      tile_map(&tk, p.k, D, p) != FAS_OK || tile_map(&tv, p.v, D, p) != FAS_OK ||
+      block_map(&bk, p.k, D, kBq, p) != FAS_OK || block_map(&bv, p.v, D, kBq, p) != FAS_OK ||
+      block_map(&bq, p.q, D, C::kB, p) != FAS_OK || block_map(&bdo, p.dout, D, C::kB, p) != FAS_OK)
+    return -1;
+  auto kq = attention_bwd_q<D>;
+  auto kk = attention_bwd_k<D, C::kB, C::kKT, C::kVT>;
+  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LQ::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LK::kSmem) != cudaSuccess)
+    return -1;
+  kq<<<grid, kThreadsB, LQ::kSmem, st>>>(tq, tdo, bk, bv, p);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  attention_bwd<D, true><<<grid, 32 * kWarpsB, 0, st>>>(p);
+  kk<<<grid, kThreadsB, LK::kSmem, st>>>(tk, tv, bq, bdo, p);
   return cudaGetLastError() == cudaSuccess ? 2 : -1;
 }
 

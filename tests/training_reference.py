@@ -64,7 +64,16 @@ def attention_backward(q, k, v, out, lse, dout, spans, ref, radius, rows=None):
     p, ds, ep, eds = block(None, None, f[rows], f, q[:, rows], k, v, dout[:, rows], out[:, rows], lse[:, rows])
     dq = s * ds @ k
     m = 8 * U32 * 64  # fp32 accumulation of the products, in 64-row steps
-    bound = s * ((ds.abs() * (U16 + m) + eds) @ k.abs()) * 2 + U16 * dq.abs()
+    # With r_j the rounding of dS_ij (|r_j| <= u |dS_ij|) the kernel's dq is s (sum_j (dS_ij + r_j) k_j - (sum_j r_j) c),
+    # off by s |sum_j r_j (k_j - c)| <= s u sum_j |dS_ij| (|k_j| + |c|), c the mean key of the first 64 tokens seen.
+    at = np.concatenate([[0], np.cumsum(spans)])
+    c = torch.zeros(len(spans), h, d, dtype=torch.float64, device=q.device)
+    for g in range(len(spans)):
+        sees = [x for x in range(len(spans)) if g < ref or x < ref or abs(g - x) <= radius]
+        run = next((i for i in range(1, len(sees)) if sees[i] != sees[i - 1] + 1), len(sees))  # the first range's frames
+        c[g] = k[:, at[sees[0]]:min(at[sees[0]] + 64, at[sees[run - 1] + 1])].mean(1).abs()
+    spread = ds.abs().sum(2, keepdim=True) * c[f[rows]].transpose(0, 1)
+    bound = s * ((ds.abs() * (U16 + m) + eds) @ k.abs() + (U16 + m) * spread) * 1.01 + U16 * dq.abs()
     kc = k - k.mean(1, keepdim=True)
     sd = torch.sqrt((s * s * U16 ** 2 / 3) * (ds ** 2 @ kc ** 2) + (U16 * dq) ** 2 / 3 + (s * (eds @ k.abs())) ** 2)
     res["dq"] = (dq, bound, sd)
