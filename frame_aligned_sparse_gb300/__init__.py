@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -150,7 +151,8 @@ def _check(call: str, rc: int) -> None:
 def _stream_handle(stream) -> Optional[int]:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # The raw handle: building the Stream object costs more than a launch.
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -227,6 +229,8 @@ def fas_plan_describe(frame_tokens, n_frames: int, ref_frames: int, window_radiu
 
 def _check_tensor(name, t, shape, dtype):
     import torch
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return  # the usual case, in one expression
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -406,7 +410,7 @@ def _check_device(*tensors):
     import torch
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
 
 
@@ -527,7 +531,7 @@ def _norm_frames(tokens: int, width: int, gate, frame_tokens):
         raise ValueError(f"gate must be [frames, width], got {tuple(gate.shape)}")
     n = gate.shape[0]
     _check_tensor("gate", gate, (n, width), torch.float32)
-    if frame_tokens is None or np.ndim(frame_tokens) == 0:
+    if frame_tokens is None or isinstance(frame_tokens, int) or np.ndim(frame_tokens) == 0:
         span = tokens // n if frame_tokens is None and n else frame_tokens
         if n * int(span or 0) != tokens:
             raise ValueError(f"gate has {n} frames of {span} tokens; x has {tokens} tokens")
@@ -536,6 +540,15 @@ def _norm_frames(tokens: int, width: int, gate, frame_tokens):
     if spans.ndim != 1 or len(spans) != n or int(spans.sum(dtype=np.int64)) != tokens:
         raise ValueError(f"frame_tokens must hold {n} spans (one per row of gate) that add up to {tokens} tokens")
     return gate.data_ptr(), spans, n
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(tokens: int, width: int, spans: Optional[bytes], frames: int, device: int) -> int:
+    """Workspace bytes of the backward norm for a shape on a device."""
+    need = ctypes.c_int64()
+    _check("fas_residual_norm_backward",
+           load().fas_residual_norm_backward_workspace(tokens, width, spans, frames, ctypes.byref(need)))
+    return need.value
 
 
 def _empty_or(name, t, shape, dtype, device):
@@ -615,20 +628,18 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
     _check_device(dx_out, dh, *saved, rstd, gamma_post, gamma_pre, gate, dx, dy)
     lib = load()
     spans_ptr = None if spans is None else spans.ctypes.data
-    need = ctypes.c_int64()
-    _check("fas_residual_norm_backward",
-           lib.fas_residual_norm_backward_workspace(N, C, spans_ptr, frames, ctypes.byref(need)))
-    workspace = torch.empty(need.value, dtype=torch.uint8, device=dx_out.device)
-    dgammas = torch.empty((2, C), dtype=torch.float32, device=dx_out.device)  # C is a multiple of 8
+    need = _norm_workspace(N, C, None if spans is None else spans.tobytes(), frames, dx_out.get_device())
+    workspace = torch.empty(need, dtype=torch.uint8, device=dx_out.device)
+    dpost, dpre = torch.empty((2, C), dtype=torch.float32, device=dx_out.device).unbind()  # C is a multiple of 8
     dgate = None if gate is None else torch.empty_like(gate)
     rc = lib.fas_residual_norm_backward(
         dx_out.data_ptr(), dh.data_ptr(), *ptrs, rstd.data_ptr(), gate_ptr, gamma_post.data_ptr(),
         gamma_pre.data_ptr(), float(alpha), N, C, spans_ptr, frames, dx.data_ptr(), dy.data_ptr(),
-        None if dgate is None else dgate.data_ptr(), dgammas[0].data_ptr(), dgammas[1].data_ptr(),
-        workspace.data_ptr(), need.value, _stream_handle(stream))
+        None if dgate is None else dgate.data_ptr(), dpost.data_ptr(), dpre.data_ptr(),
+        workspace.data_ptr(), need, _stream_handle(stream))
     _check("fas_residual_norm_backward", rc)
-    _own_until_run(stream, workspace, dgammas, dx, dy, *([] if dgate is None else [dgate]))
-    return dx, dy, dgammas[0], dgammas[1], dgate
+    _own_until_run(stream, workspace, dpost, dx, dy, *([] if dgate is None else [dgate]))
+    return dx, dy, dpost, dpre, dgate
 
 
 def _check_host_tensor(name, t, shape, dtype):

@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include "fas.h"
+#include "vec8.cuh"
 
 namespace fas {
 namespace ckpt {
@@ -46,7 +47,13 @@ __device__ __forceinline__ uint32_t encode2(float x0, float x1) {
 // This lane's eight elements of a block as codes (first element in the low
 // byte) and the block's scale byte.  All lanes of the warp take part; the
 // block is the four lanes 4i .. 4i + 3.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t& byte) {
+__device__ __forceinline__ uint2 encode8(const vec::P2 (&p)[4], uint32_t& byte) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = vec::lo(p[e]);
+    x[2 * e + 1] = vec::hi(p[e]);
+  }
   float amax = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite(x[e]) ? fabsf(x[e]) : 0.f);
@@ -61,8 +68,8 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t& byte) {
 }
 
 // The eight values that codes c under the scale byte stand for (exact).
-__device__ __forceinline__ void decode8(uint2 c, uint32_t byte, float (&x)[8]) {
-  const float s = scale_of(byte);
+__device__ __forceinline__ void decode8(uint2 c, uint32_t byte, vec::P2 (&x)[4]) {
+  const vec::P2 s = vec::both(scale_of(byte));
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -72,8 +79,7 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t byte, float (&x)[8]) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(h2));
-    x[2 * i] = lo * s;
-    x[2 * i + 1] = hi * s;
+    x[i] = vec::mul2(vec::pair(lo, hi), s);
   }
 }
 

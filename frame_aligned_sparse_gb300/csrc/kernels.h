@@ -202,10 +202,8 @@ struct NormArgs {
   void* dy = nullptr;
   float *dgate = nullptr, *dgamma_post = nullptr, *dgamma_pre = nullptr;
   float *z_part = nullptr, *d_part = nullptr;    // [items, width] partial column sums
-  float *z_frame = nullptr, *d_frame = nullptr;  // [frames, width]
-  unsigned int* counter = nullptr;               // [counters]
   int64_t rows = 0, items = 0, chunk = 0;
-  int width = 0, counters = 0;
+  int width = 0;
   int warps = 1, groups = 1;      // warps per row, rows per CTA (set by the launcher)
   bool f32 = false;               // residual type
   float alpha = 1.f, eps = 0.f;
@@ -214,7 +212,6 @@ struct NormArgs {
 // How the backward pass splits the rows, and its workspace.
 struct NormItems {
   int64_t items = 0, chunk = 0, bytes = 0;
-  int counters = 0;
 };
 
 // spans: null (n_frames frames of `span` rows) or n_frames host row counts.

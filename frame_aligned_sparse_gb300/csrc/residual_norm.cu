@@ -16,14 +16,14 @@
 // a row's values stay in registers from its load to its stores, and the two
 // row sums are warp shuffles and one exchange through shared memory each.
 // Both kernels are bound by HBM.  Groups are persistent over consecutive
-// rows: gamma and gate stay in registers, the next row is loaded while the
-// current one is reduced.
+// rows: gamma and gate stay in registers, and the next rows are on their way
+// into a ring in shared memory.  Each thread copies just the bytes it will
+// read itself (cp.async), so the ring needs no barrier.
 //
 // Backward: a group's rows never cross frames, so it adds its columns of Z
 // and of dgamma_pre in registers and writes one partial row of each at its
 // end; a second kernel adds the partials frame by frame and then frame after
-// frame, in a fixed order (no atomics on values: results are
-// bit-reproducible).
+// frame, in a fixed order (no atomics: results are bit-reproducible).
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -61,114 +61,224 @@ struct Ragged {
   __device__ __forceinline__ int64_t end(int f) const { return start[f + 1]; }
 };
 
-// Sum over the W warps of the row group; `slot` alternates so that one
-// barrier a sum is enough (a slot is written again two sums later).
-__device__ __forceinline__ float group_sum(float v, float (*red)[kMaxWarps], int slot, int warps, int w, int lane,
+// Sums over the W warps of the row group.  `slot` alternates, so that one
+// barrier a call is enough (a slot is written again two calls later).
+template <int N>
+struct Exchange {
+  float v[2][N][kMaxWarps];
+};
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], Exchange<N>& ex, int slot, int warps, int w, int lane,
                                            int group) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (warps == 1) return v;
-  if (lane == 0) red[slot][w] = v;
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (warps == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) ex.v[slot][i][w] = v[i];
   ptx::named_barrier_sync(1 + group, warps * 32);
-  float s = 0.f;
-  for (int i = 0; i < warps; ++i) s += red[slot][i];
-  return s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (int k = 0; k < warps; k += 4)  // the row's tail is zero
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 p = *reinterpret_cast<const float4*>(&ex.v[slot][i][k]);
+      v[i] += (p.x + p.y) + (p.z + p.w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void clear_exchange(Exchange<N> (&ex)[kMaxGroups]) {
+  float* p = reinterpret_cast<float*>(ex);
+  for (int i = threadIdx.x; i < (int)(sizeof(ex) / 4); i += blockDim.x) p[i] = 0.f;
+  __syncthreads();
 }
 
-template <class R, int V, bool kCkpt, class Frames>
-__global__ void __launch_bounds__(32 * kMaxWarps)
+// Stages of a row ring: as many as keep the widest row's ring in shared
+// memory (V = 4: 16,384 columns, 192 KB a stage in the fp32 backward).
+template <int V>
+constexpr int kRing = V == 1 ? 4 : V == 2 ? 2 : 1;
+
+// Asynchronous copies of this thread's bytes into its own shared memory.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  static_assert(kBytes == 8 || kBytes == 16, "");
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// A thread's place in the ring: piece i of slot q at base + (q * pieces + i)
+// * step, step = 16 bytes a thread of the CTA, so that a warp's accesses are
+// consecutive.  `off` is the byte offset of the current slot.
+struct RingPos {
+  uint32_t off, slot_bytes, end;
+  __device__ __forceinline__ RingPos(uint32_t bytes, int slots) : off(0), slot_bytes(bytes), end(bytes * slots) {}
+  __device__ __forceinline__ void next() {
+    off += slot_bytes;
+    if (off == end) off = 0;
+  }
+};
+template <class X>
+__device__ __forceinline__ void ring_load(uint32_t dst, uint32_t step, const uint8_t* src) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(X) / 16; ++i) copy_async<16>(dst + i * step, src + i * 16);
+}
+__device__ __forceinline__ uint4 ring_piece(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+template <class X>
+__device__ __forceinline__ X ring_read(uint32_t addr, uint32_t step) {
+  X x;
+  uint4* p = reinterpret_cast<uint4*>(&x);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(X) / 16; ++i) p[i] = ring_piece(addr + i * step);
+  return x;
+}
+__device__ __forceinline__ const uint8_t* bytes_of(const void* p) { return static_cast<const uint8_t*>(p); }
+__device__ __forceinline__ uint8_t* bytes_of(void* p) { return static_cast<uint8_t*>(p); }
+
+// Eight consecutive fp32 parameters.
+__device__ __forceinline__ void load_param(const float* p, vec::P2 (&x)[4]) {
+  vec::F32 v;
+  v.load(p, 0);
+  v.get(x);
+}
+
+// kWide: rows of more than eight warps (512 threads a CTA); else 256.
+template <class R, int V, bool kCkpt, bool kWide, class Frames>
+__global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : kCkpt ? 3 : 4)
     residual_norm_fwd(const NormArgs a, const __grid_constant__ Frames frames) {
-  __shared__ float red[kMaxGroups][4][kMaxWarps];
+  using namespace vec;
+  __shared__ __align__(16) Exchange<1> ex[kMaxGroups];
+  clear_exchange(ex);
   const int W = a.warps, G = a.groups;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp / W, w = warp % W;
   const int C = a.width;
   const int64_t ngroups = (int64_t)gridDim.x * G, gi = (int64_t)blockIdx.x * G + group;
-  const int64_t r0 = a.rows * gi / ngroups, r1 = a.rows * (gi + 1) / ngroups;
+  const int64_t r0 = a.rows * gi / ngroups;
+  const int n = (int)(a.rows * (gi + 1) / ngroups - r0);
   const float inv_c = 1.0f / (float)C;
-  int col[V];
+  extern __shared__ uint4 ring[];
+  constexpr int S = kRing<V>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
+  const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   bool in[V];
-  float gpost[V][8], gpre[V][8], coef[V][8];
+  int col[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     col[v] = (v * W * 32 + w * 32 + lane) * 8;
     in[v] = col[v] < C;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      gpost[v][e] = in[v] ? a.gamma_post[col[v] + e] * a.alpha : 0.f;
-      gpre[v][e] = in[v] ? a.gamma_pre[col[v] + e] : 0.f;
-      coef[v][e] = gpost[v][e];
-    }
   }
-  vec::Bf16 yv[V];
-  R xv[V];
-  auto load = [&](int64_t r) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (in[v]) {
-        yv[v].load(a.y, r * C + col[v]);
-        xv[v].load(a.x, r * C + col[v]);
-      }
-  };
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    yv[v] = vec::Bf16{};
-    xv[v] = R{};
-  }
-  if (r0 < r1) load(r0);
-  int64_t frame_end = a.gate ? -1 : a.rows;
-  int slot = 0;
-  for (int64_t r = r0; r < r1; ++r) {
-    float y[V][8], x[V][8];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      yv[v].get(y[v]);
-      xv[v].get(x[v]);
-    }
-    if (r + 1 < r1) load(r + 1);
-    if (r >= frame_end) {
-      const int f = frames.frame(r);
-      frame_end = frames.end(f);
+  // Pointers to this thread's first vector, advanced row by row.
+  const int64_t at0 = r0 * C + col[0];
+  const int vstep = W * 32 * 8;  // columns between a thread's vectors
+  const uint8_t *py = bytes_of(a.y) + at0 * 2, *px = bytes_of(a.x) + at0 * kElem;
+  uint8_t *ph = bytes_of(a.h) + at0 * 2, *po = bytes_of(a.x_out) + at0 * kElem;
+  RingPos ld(V * kVec * step, S), rd(V * kVec * step, S);
+  int left = n;  // rows not yet asked for
+  auto load = [&]() {
+    if (left > 0) {
+      --left;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (in[v])
-#pragma unroll
-          for (int e = 0; e < 8; ++e) coef[v][e] = gpost[v][e] * a.gate[(int64_t)f * C + col[v] + e];
+        if (in[v]) {
+          const uint32_t dst = base + ld.off + v * kVec * step;
+          ring_load<Bf16>(dst, step, py + v * vstep * 2);
+          ring_load<R>(dst + step, step, px + v * vstep * kElem);
+        }
+      py += C * 2;
+      px += (int64_t)C * kElem;
+      ld.next();
     }
-    float ss = 0.f;
+    copy_commit();
+  };
+  for (int i = 0; i < S; ++i) load();
+  P2 gpre[V][4], coef[V][4];
+  const P2 alpha = both(a.alpha), zero = both(0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[v][e], y[v][e], ss);
-    const float ry = rsqrtf(group_sum(ss, red[group], slot, W, w, lane, group) * inv_c + a.eps);
-    float sx = 0.f;
+    for (int e = 0; e < 4; ++e) gpre[v][e] = coef[v][e] = zero;
+    if (in[v]) load_param(a.gamma_pre + col[v], gpre[v]);
+  }
+  int frame_end = 0;  // row of this group at which the frame ends
+  for (int i = 0; i < n; ++i) {
+    if (i >= frame_end) {  // a new frame: alpha gate gamma_post
+      const int f = a.gate ? frames.frame(r0 + i) : 0;
+      frame_end = a.gate ? (int)min(frames.end(f) - r0, (int64_t)n) : n;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v)
+        if (in[v]) {
+          load_param(a.gamma_post + col[v], coef[v]);
+          P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
+          if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[v][e] = fmaf(y[v][e] * ry, coef[v][e], x[v][e]);
-        sx = fmaf(x[v][e], x[v][e], sx);
-      }
-    const float rx = rsqrtf(group_sum(sx, red[group], slot + 1, W, w, lane, group) * inv_c + a.eps);
-    slot ^= 2;
+          for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], alpha), gt[e]);
+        }
+    }
+    copy_wait<S - 1>();
+    P2 y[V][4], x[V][4], acc = zero;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int64_t at = r * C + col[v];
-      float h[8];
+      Bf16 yv{};
+      R xv{};
+      if (in[v]) {
+        const uint32_t src = base + rd.off + v * kVec * step;
+        yv = ring_read<Bf16>(src, step);
+        xv = ring_read<R>(src + step, step);
+      }
+      yv.get(y[v]);
+      xv.get(x[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = x[v][e] * rx * gpre[v][e];
-      vec::Bf16 hv;
+      for (int e = 0; e < 4; ++e) acc = fma2(y[v][e], y[v][e], acc);
+    }
+    rd.next();
+    load();
+    float s[1] = {sum(acc)};
+    group_sums(s, ex[group], 0, W, w, lane, group);
+    const float ry = rsqrtf(s[0] * inv_c + a.eps);
+    const P2 ry2 = both(ry);
+    acc = zero;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[v][e] = fma2(mul2(y[v][e], ry2), coef[v][e], x[v][e]);
+        acc = fma2(x[v][e], x[v][e], acc);
+      }
+    s[0] = sum(acc);
+    group_sums(s, ex[group], 1, W, w, lane, group);
+    const float rx = rsqrtf(s[0] * inv_c + a.eps);
+    const P2 rx2 = both(rx);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      P2 h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = mul2(mul2(x[v][e], rx2), gpre[v][e]);
+      Bf16 hv;
       R ov;
       hv.set(h);
-      ov.set(x[v]);  // x becomes what is stored: the checkpoint is of that
+      ov.set(x[v]);
       if (in[v]) {
-        hv.store(a.h, at);
-        ov.store(a.x_out, at);
+        hv.store(ph + v * vstep * 2, 0);
+        ov.store(po + v * vstep * kElem, 0);
       }
       if constexpr (kCkpt) {
+        ov.get(x[v]);  // the checkpoint is of x' as stored
         uint32_t by, bx;
         const uint2 cy = ckpt::encode8(y[v], by), cx = ckpt::encode8(x[v], bx);
         if (in[v]) {
+          const int64_t at = (r0 + i) * C + col[v];
           *reinterpret_cast<uint2*>(a.y8 + at) = cy;
           *reinterpret_cast<uint2*>(a.x8 + at) = cx;
           if ((lane & 3) == 0) {
@@ -178,9 +288,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         }
       }
     }
+    ph += C * 2;
+    po += (int64_t)C * kElem;
     if (w == 0 && lane == 0) {
-      a.rstd[r] = ry;
-      a.rstd[a.rows + r] = rx;
+      a.rstd[r0 + i] = ry;
+      a.rstd[a.rows + r0 + i] = rx;
     }
   }
 }
@@ -215,137 +327,210 @@ template <class R, bool k8>
 struct Held;
 template <class R>
 struct Held<R, false> {
-  vec::Bf16 y;
-  R x;
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t at) {
-    y.load(a.y, at);
-    x.load(a.x, at);
+  static constexpr int kPieces = 1 + sizeof(R) / 16, kElem = sizeof(R) / 8;
+  const uint8_t *y, *x;
+  __device__ __forceinline__ Held(const NormArgs& a, int64_t at) : y(bytes_of(a.y) + at * 2), x(bytes_of(a.x) + at * kElem) {}
+  __device__ __forceinline__ void load(uint32_t dst, uint32_t step, int cols) const {
+    ring_load<vec::Bf16>(dst, step, y + cols * 2);
+    ring_load<R>(dst + step, step, x + cols * kElem);
   }
-  __device__ __forceinline__ void get(float (&yf)[8], float (&xf)[8]) const {
-    y.get(yf);
-    x.get(xf);
+  __device__ __forceinline__ void next(int c) {
+    y += c * 2;
+    x += (int64_t)c * kElem;
+  }
+  static __device__ __forceinline__ void get(uint32_t src, uint32_t step, uint32_t, uint32_t, vec::P2 (&yf)[4],
+                                             vec::P2 (&xf)[4]) {
+    ring_read<vec::Bf16>(src, step).get(yf);
+    ring_read<R>(src + step, step).get(xf);
   }
 };
 template <class R>
 struct Held<R, true> {
-  uint2 y, x;
-  uint32_t b;
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t at) {
-    y = *reinterpret_cast<const uint2*>(a.y8 + at);
-    x = *reinterpret_cast<const uint2*>(a.x8 + at);
-    b = a.y8_scale[at / ckpt::kBlock] | (uint32_t)a.x8_scale[at / ckpt::kBlock] << 8;
+  static constexpr int kPieces = 1;  // both codes' eight bytes
+  const uint8_t *y, *x;
+  __device__ __forceinline__ Held(const NormArgs& a, int64_t at) : y(a.y8 + at), x(a.x8 + at) {}
+  __device__ __forceinline__ void load(uint32_t dst, uint32_t, int cols) const {
+    copy_async<8>(dst, y + cols);
+    copy_async<8>(dst + 8, x + cols);
   }
-  __device__ __forceinline__ void get(float (&yf)[8], float (&xf)[8]) const {
-    ckpt::decode8(y, b & 255u, yf);
-    ckpt::decode8(x, b >> 8, xf);
+  __device__ __forceinline__ void next(int c) {
+    y += c;
+    x += c;
+  }
+  static __device__ __forceinline__ void get(uint32_t src, uint32_t, uint32_t by, uint32_t bx, vec::P2 (&yf)[4],
+                                             vec::P2 (&xf)[4]) {
+    const uint4 c = ring_piece(src);
+    ckpt::decode8(make_uint2(c.x, c.y), by, yf);
+    ckpt::decode8(make_uint2(c.z, c.w), bx, xf);
   }
 };
 
-template <class R, int V, bool k8, class Items>
-__global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_bwd(const NormArgs a, const __grid_constant__ Items items) {
-  __shared__ float red[kMaxGroups][4][kMaxWarps];
+// Both row means come from one exchange: with t = dx' + r_x a (g = t - r_x xh
+// m1), sum(b yh) = sum(coef yh t) - r_x m1 sum(coef yh xh), coef = alpha gate
+// gamma_post, so the three sums of a xh, coef yh t and coef yh xh give both.
+template <class R, int V, bool k8, bool kWide, class Items>
+__global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
+    residual_norm_bwd(const NormArgs a, const __grid_constant__ Items items) {
+  using namespace vec;
+  __shared__ __align__(16) Exchange<3> ex[kMaxGroups];
+  clear_exchange(ex);
   const int W = a.warps, G = a.groups;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp / W, w = warp % W;
   const int C = a.width;
   const float inv_c = 1.0f / (float)C;
-  // The second kernel's counters (one per column block) start at zero.
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.counters; i += blockDim.x) a.counter[i] = 0u;
+  ptx::grid_launch_next();
   const int64_t item = (int64_t)blockIdx.x * G + group;
   if (item >= a.items) return;  // whole groups: the group's barrier is its own
   const int f = items.frame(item);
   const int64_t r0 = items.start(f) + (item - items.first(f)) * a.chunk;
-  const int64_t r1 = min(r0 + a.chunk, items.end(f));
+  const int n = (int)(min(r0 + a.chunk, items.end(f)) - r0);
+  extern __shared__ uint4 ring[];
+  using H = Held<R, k8>;
+  constexpr int S = kRing<V>, kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
+  const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   int col[V];
   bool in[V];
-  float coef[V][8], gpre[V][8], z[V][8], dg[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     col[v] = (v * W * 32 + w * 32 + lane) * 8;
     in[v] = col[v] < C;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      coef[v][e] = in[v] ? a.gamma_post[col[v] + e] * a.alpha : 0.f;
-      if (in[v] && a.gate) coef[v][e] *= a.gate[(int64_t)f * C + col[v] + e];
-      gpre[v][e] = in[v] ? a.gamma_pre[col[v] + e] : 0.f;
-      z[v][e] = dg[v][e] = 0.f;
-    }
   }
-  vec::Bf16 hv[V];
-  R gv[V];
-  Held<R, k8> held[V];
-  float ry, rx;
-  auto load = [&](int64_t r) {
+  const int64_t at0 = r0 * C + col[0];
+  const int vstep = W * 32 * 8;  // columns between a thread's vectors
+  const uint8_t *pg = bytes_of(a.dx_out) + at0 * kElem, *ph = bytes_of(a.dh) + at0 * 2;
+  uint8_t *pdx = bytes_of(a.dx) + at0 * kElem, *pdy = bytes_of(a.dy) + at0 * 2;
+  H held(a, at0);
+  RingPos ld(V * kVec * step, S), rd(V * kVec * step, S);
+  int left = n;  // rows not yet asked for
+  auto load = [&]() {
+    if (left > 0) {
+      --left;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (in[v]) {
-        const int64_t at = r * C + col[v];
-        gv[v].load(a.dx_out, at);
-        hv[v].load(a.dh, at);
-        held[v].load(a, at);
-      }
-    ry = a.rstd[r];
-    rx = a.rstd[a.rows + r];
+      for (int v = 0; v < V; ++v)
+        if (in[v]) {
+          const uint32_t dst = base + ld.off + v * kVec * step;
+          ring_load<R>(dst, step, pg + v * vstep * kElem);
+          ring_load<Bf16>(dst + kG * step, step, ph + v * vstep * 2);
+          held.load(dst + (kG + 1) * step, step, v * vstep);
+        }
+      pg += (int64_t)C * kElem;
+      ph += C * 2;
+      held.next(C);
+      ld.next();
+    }
+    copy_commit();
   };
+  for (int i = 0; i < S; ++i) load();
+  // The row's small inputs come through registers, two rows ahead, and are
+  // not touched before their row (an instruction that uses one waits for it).
+  struct Small {
+    float ry, rx;
+    uint32_t by[V], bx[V];
+  };
+  const float* pr = a.rstd + r0;
+  const uint8_t *sy = nullptr, *sx = nullptr;
+  if (k8) {
+    sy = a.y8_scale + at0 / ckpt::kBlock;
+    sx = a.x8_scale + at0 / ckpt::kBlock;
+  }
+  auto load_small = [&](int i, Small& s) {
+    if (i < n) {
+      s.ry = pr[i];
+      s.rx = pr[i + a.rows];
+      if (k8)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (in[v]) {
+            s.by[v] = sy[(int64_t)i * (C / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
+            s.bx[v] = sx[(int64_t)i * (C / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
+          }
+    }
+  };
+  Small small[2] = {};
+  load_small(0, small[0]);
+  load_small(1, small[1]);
+  const P2 zero = both(0.f);
+  P2 coef[V][4], gpre[V][4], z[V][4], dg[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    gv[v] = R{};
-    hv[v] = vec::Bf16{};
-    held[v] = Held<R, k8>{};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) coef[v][e] = gpre[v][e] = z[v][e] = dg[v][e] = zero;
+    if (in[v]) {
+      load_param(a.gamma_post + col[v], coef[v]);
+      load_param(a.gamma_pre + col[v], gpre[v]);
+      P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
+      if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], both(a.alpha)), gt[e]);
+    }
   }
-  if (r0 < r1) load(r0);
-  int slot = 0;
-  for (int64_t r = r0; r < r1; ++r) {
-    float y[V][8], x[V][8], g[V][8], h[V][8];
-    const float ryc = ry, rxc = rx;
-    float s = 0.f;
+  auto row = [&](int i, Small& sm, int slot) {
+    P2 y[V][4], x[V][4], t[V][4];
+    const float rx = sm.rx;
+    const P2 ry2 = both(sm.ry), rx2 = both(rx);
+    P2 sa = zero, sb = zero, sc = zero;
+    copy_wait<S - 1>();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      held[v].get(y[v], x[v]);
-      gv[v].get(g[v]);
-      hv[v].get(h[v]);
+      P2 h[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[v][e] *= ryc;
-        x[v][e] *= rxc;
-        dg[v][e] = fmaf(h[v][e], x[v][e], dg[v][e]);
-        h[v][e] *= gpre[v][e];
-        s = fmaf(h[v][e], x[v][e], s);
+      for (int e = 0; e < 4; ++e) y[v][e] = x[v][e] = t[v][e] = h[e] = zero;
+      if (in[v]) {
+        const uint32_t src = base + rd.off + v * kVec * step;
+        ring_read<R>(src, step).get(t[v]);
+        ring_read<Bf16>(src + kG * step, step).get(h);
+        H::get(src + (kG + 1) * step, step, sm.by[v], sm.bx[v], y[v], x[v]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[v][e] = mul2(y[v][e], ry2);
+        x[v][e] = mul2(x[v][e], rx2);
+        dg[v][e] = fma2(h[e], x[v][e], dg[v][e]);
+        const P2 ah = mul2(h[e], gpre[v][e]);
+        sa = fma2(ah, x[v][e], sa);
+        t[v][e] = fma2(rx2, ah, t[v][e]);
+        const P2 cy = mul2(coef[v][e], y[v][e]);
+        sb = fma2(cy, t[v][e], sb);
+        sc = fma2(cy, x[v][e], sc);
       }
     }
-    if (r + 1 < r1) load(r + 1);
-    const float m1 = group_sum(s, red[group], slot, W, w, lane, group) * inv_c;
-    float s2 = 0.f;
+    rd.next();
+    load();
+    load_small(i + 2, sm);
+    float s[3] = {sum(sa), sum(sb), sum(sc)};
+    group_sums(s, ex[group], slot, W, w, lane, group);
+    const float rm1 = rx * s[0] * inv_c, m2 = (s[1] - rm1 * s[2]) * inv_c;
+    const P2 nrm1 = both(-rm1), nm2 = both(-m2);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      P2 d[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        g[v][e] = fmaf(rxc, fmaf(-x[v][e], m1, h[v][e]), g[v][e]);
-        z[v][e] = fmaf(y[v][e], g[v][e], z[v][e]);
-        s2 = fmaf(g[v][e] * coef[v][e], y[v][e], s2);
+      for (int e = 0; e < 4; ++e) {
+        t[v][e] = fma2(nrm1, x[v][e], t[v][e]);  // g
+        z[v][e] = fma2(y[v][e], t[v][e], z[v][e]);
+        d[e] = mul2(ry2, fma2(nm2, y[v][e], mul2(coef[v][e], t[v][e])));
       }
-    const float m2 = group_sum(s2, red[group], slot + 1, W, w, lane, group) * inv_c;
-    slot ^= 2;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
+      Bf16 dv;
+      R ov;
+      dv.set(d);
+      ov.set(t[v]);
       if (in[v]) {
-        float d[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = ryc * fmaf(-y[v][e], m2, g[v][e] * coef[v][e]);
-        vec::Bf16 dv;
-        R ov;
-        dv.set(d);
-        ov.set(g[v]);
-        const int64_t at = r * C + col[v];
-        dv.store(a.dy, at);
-        ov.store(a.dx, at);
+        dv.store(pdy + v * vstep * 2, 0);
+        ov.store(pdx + v * vstep * kElem, 0);
       }
+    }
+    pdx += (int64_t)C * kElem;
+    pdy += C * 2;
+  };
+  for (int i = 0; i < n; i += 2) {
+    row(i, small[0], 0);
+    if (i + 1 < n) row(i + 1, small[1], 1);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
     if (in[v]) {
-      vec::F32 o;
+      F32 o;
       o.set(z[v]);
       o.store(a.z_part, item * C + col[v]);
       o.set(dg[v]);
@@ -353,65 +538,70 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_bwd(const NormAr
     }
 }
 
-// Adds the partials: CTA (column block, frame) sums its frame's items, 8
-// lanes of items by 32 columns; the last CTA of a column block to arrive
-// (a counter) then adds the frames in order.
-constexpr int kSumCols = 32, kSumLanes = 8;
+// Adds the partials: a CTA per 32 columns, 128 lanes of four-column loads.
+// A frame's items are split over `sub` lanes, so that each lane has few loads
+// and all are in flight at once; then the frame's lanes are added, and the
+// frames, each in a fixed order.
+constexpr int kSumCols = 32, kSumLanes = 128, kSumThreads = kSumCols / 4 * kSumLanes;
 
 template <class Items>
-__global__ void __launch_bounds__(kSumCols* kSumLanes)
+__global__ void __launch_bounds__(kSumThreads)
     residual_norm_sums(const NormArgs a, const __grid_constant__ Items items, int n_frames) {
-  __shared__ float red[2][kSumLanes][kSumCols];
-  __shared__ bool last;
-  const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
-  const int c = blockIdx.y * kSumCols + tx, f = blockIdx.x, C = a.width;
-  const bool in = c < C;
-  auto reduce = [&](float z, float d) {
-    __syncthreads();
-    red[0][ty][tx] = z;
-    red[1][ty][tx] = d;
-    __syncthreads();
-  };
-  float z = 0.f, d = 0.f;
-  const int64_t i1 = f + 1 < n_frames ? items.first(f + 1) : a.items;
-  if (in)
-    for (int64_t i = items.first(f) + ty; i < i1; i += kSumLanes) {
-      z += a.z_part[i * C + c];
-      d += a.d_part[i * C + c];
+  __shared__ __align__(16) float zr[kSumLanes][kSumCols], dr[kSumLanes][kSumCols];
+  const int tx = threadIdx.x % (kSumCols / 4), lane = threadIdx.x / (kSumCols / 4);
+  const int C = a.width, c0 = blockIdx.x * kSumCols;
+  const bool in = c0 + tx * 4 < C;  // C is a multiple of 8
+  const int sub = n_frames >= kSumLanes ? 1 : kSumLanes / n_frames, par = kSumLanes / sub;
+  const int ct = threadIdx.x % kSumCols, wt = threadIdx.x / kSumCols;  // one column a thread, 32 warps
+  const bool ct_in = c0 + ct < C;
+  const float post = ct_in ? a.gamma_post[c0 + ct] * a.alpha : 0.f;
+  ptx::grid_wait_previous();
+  float4 d = {0.f, 0.f, 0.f, 0.f};
+  float zs = 0.f;  // warp 0: dgamma_post
+  for (int f0 = 0; f0 < n_frames; f0 += par) {
+    const int f = f0 + lane / sub, s = lane % sub;
+    float4 z = {0.f, 0.f, 0.f, 0.f};
+    if (in && lane / sub < par && f < n_frames) {
+      const int64_t i1 = f + 1 < n_frames ? items.first(f + 1) : a.items;
+#pragma unroll 4
+      for (int64_t i = items.first(f) + s; i < i1; i += sub) {
+        const float4 p = *reinterpret_cast<const float4*>(a.z_part + i * C + c0 + tx * 4);
+        const float4 q = *reinterpret_cast<const float4*>(a.d_part + i * C + c0 + tx * 4);
+        z.x += p.x; z.y += p.y; z.z += p.z; z.w += p.w;
+        d.x += q.x; d.y += q.y; d.z += q.z; d.w += q.w;
+      }
     }
-  reduce(z, d);
-  const float post = in ? a.gamma_post[c] : 0.f;
-  if (ty == 0 && in) {
-    z = d = 0.f;
-    for (int l = 0; l < kSumLanes; ++l) {
-      z += red[0][l][tx];
-      d += red[1][l][tx];
+    *reinterpret_cast<float4*>(&zr[lane][tx * 4]) = z;
+    __syncthreads();
+    const int nf = n_frames - f0 < par ? n_frames - f0 : par;
+    for (int k = wt; k < nf; k += kSumThreads / kSumCols) {
+      float v = 0.f;
+      for (int l = 0; l < sub; ++l) v += zr[k * sub + l][ct];
+      if (a.gate && ct_in) {
+        const int64_t at = (int64_t)(f0 + k) * C + c0 + ct;
+        a.dgate[at] = post * v;
+        v *= a.gate[at];
+      }
+      zr[k * sub][ct] = v;
     }
-    if (a.gate) a.dgate[(int64_t)f * C + c] = a.alpha * post * z;
-    a.z_frame[(int64_t)f * C + c] = a.gate ? a.alpha * a.gate[(int64_t)f * C + c] * z : a.alpha * z;
-    a.d_frame[(int64_t)f * C + c] = d;
-    __threadfence();
+    __syncthreads();
+    if (wt == 0)
+      for (int k = 0; k < nf; ++k) zs += zr[k * sub][ct];
+    __syncthreads();
   }
+  *reinterpret_cast<float4*>(&dr[lane][tx * 4]) = d;
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&a.counter[blockIdx.y], 1u) == (unsigned)n_frames - 1u;
+  constexpr int kPer = kSumLanes / (kSumThreads / kSumCols);  // lanes a warp adds first
+  float v = 0.f;
+#pragma unroll
+  for (int l = 0; l < kPer; ++l) v += dr[wt * kPer + l][ct];
+  zr[wt][ct] = v;
   __syncthreads();
-  if (!last) return;
-  __threadfence();
-  z = d = 0.f;
-  if (in)
-    for (int g = ty; g < n_frames; g += kSumLanes) {
-      z += __ldcg(a.z_frame + (int64_t)g * C + c);
-      d += __ldcg(a.d_frame + (int64_t)g * C + c);
-    }
-  reduce(z, d);
-  if (ty == 0 && in) {
-    z = d = 0.f;
-    for (int l = 0; l < kSumLanes; ++l) {
-      z += red[0][l][tx];
-      d += red[1][l][tx];
-    }
-    a.dgamma_post[c] = z;
-    a.dgamma_pre[c] = d;
+  if (wt == 0 && ct_in) {
+    float ds = 0.f;
+    for (int l = 0; l < kSumThreads / kSumCols; ++l) ds += zr[l][ct];
+    a.dgamma_post[c0 + ct] = a.alpha * zs;
+    a.dgamma_pre[c0 + ct] = ds;
   }
 }
 
@@ -428,26 +618,43 @@ Shape shape_of(int width) {
 
 // Row groups that run at once for a kernel of `threads` a CTA on the device.
 template <class K>
-int64_t resident_groups(K kern, const Shape& s, int sms) {
+int64_t resident_groups(K kern, const Shape& s, size_t smem, int sms) {
   int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * s.W * s.G, 0) != cudaSuccess || per_sm < 1)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * s.W * s.G, smem) != cudaSuccess || per_sm < 1)
     return 0;
   return (int64_t)per_sm * sms * s.G;
 }
 
-template <class R, int V, bool kCkpt, class Frames>
+// Opt-in shared memory of a kernel's ring (per launch: it belongs to the
+// device's context; up to 48 KB with the static part goes without).
+template <class K>
+cudaError_t allow_ring(K kern, size_t smem) {
+  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                          : cudaSuccess;
+}
+
+template <class R, int V, bool kCkpt, bool kWide, class Frames>
 cudaError_t fwd(NormArgs a, const Frames& fr, const Shape& s, int sms, cudaStream_t st) {
-  auto kern = residual_norm_fwd<R, V, kCkpt, Frames>;
-  const int64_t res = resident_groups(kern, s, sms);
-  if (res == 0) return cudaErrorInvalidConfiguration;
-  const int64_t groups = std::min(a.rows, res);
-  kern<<<(unsigned)((groups + s.G - 1) / s.G), 32 * s.W * s.G, 0, st>>>(a, fr);
+  auto kern = residual_norm_fwd<R, V, kCkpt, kWide, Frames>;
+  const size_t smem = (size_t)32 * s.W * s.G * kRing<V> * V * (16 + sizeof(R));
+  const cudaError_t e = allow_ring(kern, smem);
+  if (e != cudaSuccess) return e;
+  int64_t groups = a.rows;
+  if (groups > s.G * sms) {  // more rows than groups that surely fit
+    const int64_t res = resident_groups(kern, s, smem, sms);
+    if (res == 0) return cudaErrorInvalidConfiguration;
+    groups = std::min(groups, res);
+  }
+  kern<<<(unsigned)((groups + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, fr);
   return cudaGetLastError();
 }
 
 template <class R, int V, class Frames>
 cudaError_t fwd_c(const NormArgs& a, const Frames& fr, const Shape& s, int sms, cudaStream_t st) {
-  return a.y8 ? fwd<R, V, true>(a, fr, s, sms, st) : fwd<R, V, false>(a, fr, s, sms, st);
+  if (s.W > kMaxGroups) return a.y8 ? fwd<R, V, true, true>(a, fr, s, sms, st) : fwd<R, V, false, true>(a, fr, s, sms, st);
+  if constexpr (V == 1)
+    return a.y8 ? fwd<R, V, true, false>(a, fr, s, sms, st) : fwd<R, V, false, false>(a, fr, s, sms, st);
+  return cudaErrorInvalidValue;  // V > 1 only for rows of more than eight warps
 }
 template <class Frames>
 cudaError_t fwd_all(const NormArgs& a, const Frames& fr, const Shape& s, int sms, cudaStream_t st) {
@@ -456,15 +663,20 @@ cudaError_t fwd_all(const NormArgs& a, const Frames& fr, const Shape& s, int sms
   return a.f32 ? fwd_c<vec::F32, 4>(a, fr, s, sms, st) : fwd_c<vec::Bf16, 4>(a, fr, s, sms, st);
 }
 
-template <class R, int V, bool k8, class Items>
+template <class R, int V, bool k8, bool kWide, class Items>
 cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  residual_norm_bwd<R, V, k8, Items>
-      <<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, 0, st>>>(a, it);
+  auto kern = residual_norm_bwd<R, V, k8, kWide, Items>;
+  const size_t smem = (size_t)32 * s.W * s.G * kRing<V> * V * (sizeof(R) + 16 + 16 * Held<R, k8>::kPieces);
+  const cudaError_t e = allow_ring(kern, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
   return cudaGetLastError();
 }
 template <class R, int V, class Items>
 cudaError_t bwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  return a.y8 ? bwd<R, V, true>(a, it, s, st) : bwd<R, V, false>(a, it, s, st);
+  if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true>(a, it, s, st) : bwd<R, V, false, true>(a, it, s, st);
+  if constexpr (V == 1) return a.y8 ? bwd<R, V, true, false>(a, it, s, st) : bwd<R, V, false, false>(a, it, s, st);
+  return cudaErrorInvalidValue;  // V > 1 only for rows of more than eight warps
 }
 template <class Items>
 cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shape& s, cudaStream_t st) {
@@ -476,9 +688,16 @@ cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shap
   else
     e = a.f32 ? bwd_c<vec::F32, 4>(a, it, s, st) : bwd_c<vec::Bf16, 4>(a, it, s, st);
   if (e != cudaSuccess) return e;
-  residual_norm_sums<Items><<<dim3((unsigned)n_frames, (unsigned)a.counters), kSumCols * kSumLanes, 0, st>>>(a, it,
-                                                                                                         n_frames);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.width + kSumCols - 1) / kSumCols));
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts in the first kernel's tail
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, residual_norm_sums<Items>, a, it, n_frames);
 }
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -519,9 +738,7 @@ NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int
   NormItems r;
   r.chunk = lo;
   r.items = count(lo);
-  r.counters = (width + kSumCols - 1) / kSumCols;
-  const int64_t part = align256(r.items * width * 4), frame = align256((int64_t)n_frames * width * 4);
-  r.bytes = 2 * part + 2 * frame + align256((int64_t)r.counters * 4);
+  r.bytes = 2 * align256(r.items * width * 4);
   return r;
 }
 
@@ -532,14 +749,10 @@ cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const 
   a.groups = s.G;
   a.items = n.items;
   a.chunk = n.chunk;
-  a.counters = n.counters;
-  const int64_t part = align256(n.items * a.width * 4), frame = align256((int64_t)n_frames * a.width * 4);
+  const int64_t part = align256(n.items * a.width * 4);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.z_part = reinterpret_cast<float*>(ws);
   a.d_part = reinterpret_cast<float*>(ws + part);
-  a.z_frame = reinterpret_cast<float*>(ws + 2 * part);
-  a.d_frame = reinterpret_cast<float*>(ws + 2 * part + frame);
-  a.counter = reinterpret_cast<unsigned int*>(ws + 2 * part + 2 * frame);
   if (!spans) return bwd_all(a, UniformItems{span, (int)((span + n.chunk - 1) / n.chunk)}, n_frames, s, st);
   RaggedItems it;
   it.n = n_frames;
