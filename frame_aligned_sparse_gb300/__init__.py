@@ -443,12 +443,12 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
         _check_tensor(name, t, shape, torch.bfloat16)
         grads.append(t)
     _check_device(q, k, v, out, lse, dout, *grads)
-    stats = torch.empty((2, *_lse_shape()), dtype=torch.float32, device=q.device)
+    workspace = torch.empty((32, *_lse_shape()), dtype=torch.uint8, device=q.device)  # FAS_BACKWARD_WORKSPACE
     rc = load().fas_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              dout.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
-                             stats.data_ptr(), _stream_handle(stream))
+                             workspace.data_ptr(), _stream_handle(stream))
     _check("fas_backward", rc)
-    _own_until_run(stream, stats, *grads)
+    _own_until_run(stream, workspace, *grads)
     return tuple(grads)
 
 

@@ -857,13 +857,13 @@ int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded,
 }
 
 int fas_backward(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
-                 void* dq, void* dk, void* dv, float* stats, void* cuda_stream) {
+                 void* dq, void* dk, void* dv, void* workspace, void* cuda_stream) {
   if (!g_state.planned) return FAS_ERR_STATE;
-  const void* ptrs[] = {q, k, v, out, lse, dout, dq, dk, dv, stats};
+  const void* ptrs[] = {q, k, v, out, lse, dout, dq, dk, dv, workspace};
   for (const void* ptr : ptrs)
     if (!ptr) return FAS_ERR_ARG;
   // Gradients are written while inputs are still read.
-  const void* outs[] = {dq, dk, dv, stats};
+  const void* outs[] = {dq, dk, dv, workspace};
   for (int i = 0; i < 4; ++i) {
     for (const void* in : {q, k, v, out, (const void*)lse, dout})
       if (outs[i] == in) return FAS_ERR_ARG;
@@ -880,7 +880,6 @@ int fas_backward(const void* q, const void* k, const void* v, const void* out, c
   b.work = s.work;
   b.table = s.table;
   b.spans = s.spans;
-  b.by_frame = p.ragged ? 0 : 1;
   b.q = static_cast<const uint16_t*>(q);
   b.k = static_cast<const uint16_t*>(k);
   b.v = static_cast<const uint16_t*>(v);
@@ -892,11 +891,9 @@ int fas_backward(const void* q, const void* k, const void* v, const void* out, c
   b.row_stride = row_stride();
   b.head_stride = head_stride();
   b.lse = lse;
-  b.stats = stats;
+  b.stats = static_cast<uint8_t*>(workspace);
   b.err = s.err;
   b.N = p.N;
-  b.T = p.T;
-  b.Nf = p.Nf;
   b.H = p.H;
   b.limit_ns = fas::kWaitLimitNs;
   b.scale = (float)(1.0 / sqrt((double)p.d));

@@ -69,31 +69,32 @@ struct Blocks {
 };
 
 struct BarsB {
-  uint64_t tile_full;
+  uint64_t tile_full, tile_free;   // the tiles have landed; they have been copied to TMEM
   uint64_t full[2][kMaxStagesB];   // [ring][stage]
   uint64_t empty[2][kMaxStagesB];
-  uint64_t s_full[2], dp_full[2];
-  uint64_t s_free[2];              // query pass: S read into registers
+  uint64_t s_full, dp_full;
+  uint64_t s_free;                 // query pass: S read into registers
   uint64_t p_full, ds_full[2];
   uint64_t acc_full, drain;
   uint32_t tmem_base;
   int abort, skip;
 };
 
-__device__ __forceinline__ void init_bars(BarsB& b, int soft_arrivals) {
+__device__ __forceinline__ void init_bars(BarsB& b) {
   auto one = [](uint64_t& x, int n) { ptx::mbar_init(ptx::smem_addr(&x), n); };
   one(b.tile_full, 1);
+  one(b.tile_free, 1);
   for (int i = 0; i < 2; ++i) {
     for (int s = 0; s < kMaxStagesB; ++s) {
       one(b.full[i][s], 1);
       one(b.empty[i][s], 1);
     }
-    one(b.s_full[i], 1);
-    one(b.dp_full[i], 1);
-    one(b.s_free[i], soft_arrivals);
-    one(b.ds_full[i], soft_arrivals);
+    one(b.ds_full[i], kSoftThreads);
   }
-  one(b.p_full, soft_arrivals);
+  one(b.s_full, 1);
+  one(b.dp_full, 1);
+  one(b.s_free, kSoftThreads);
+  one(b.p_full, kSoftThreads);
   one(b.acc_full, 1);
   one(b.drain, 1);
   b.abort = 0;
@@ -108,6 +109,23 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// x as the sum of three bf16 values (24 bits: exact to fp32 rounding) in the
+// first three elements of a 16-byte row, the others zero.
+__device__ __forceinline__ uint4 split3(float x) {
+  const uint32_t a = ptx::pack_bf16x2(x, 0.f) & 0xFFFFu;
+  const float r1 = x - __uint_as_float(a << 16);
+  const uint32_t b = ptx::pack_bf16x2(r1, 0.f) & 0xFFFFu;
+  const float r2 = r1 - __uint_as_float(b << 16);
+  return make_uint4(a | b << 16, ptx::pack_bf16x2(r2, 0.f) & 0xFFFFu, 0u, 0u);
+}
+
+// Descriptor of a K-major operand without swizzle: 8-row groups of 128 bytes
+// (16 bytes a row) one after the other, the next 8 columns lbo_bytes on.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo_bytes) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
+}
+
 __device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
   asm("{\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%2, %3};\n\t"
@@ -118,45 +136,47 @@ __device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// Loads a 128-row tile: by frame (rows past the frame's end read zeros), or
-// by token when frames are ragged (the next frame's rows, computed and
-// discarded).
+// Loads a 128-row tile.  Rows past the frame's end are the next frame's (or
+// zeros past the last token): every row of a tile is computed by itself, and
+// those are never stored.
 template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, const BwdParams& p,
-                                          int first, int f, int h, int t) {
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int first, int h) {
 #pragma unroll
-  for (int half = 0; half < D / 64; ++half) {
-    if (p.by_frame)
-      ptx::tma_load_4d(dst + half * (kRowsB * 128), tm, bar, half * 64, t * kRowsB, f, h);
-    else
-      ptx::tma_load_3d(dst + half * (kRowsB * 128), tm, bar, half * 64, first + t * kRowsB, h);
-  }
+  for (int half = 0; half < D / 64; ++half) ptx::tma_load_3d(dst + half * (kRowsB * 128), tm, bar, half * 64, first, h);
 }
 
-// One ring's producer: block j into stage j % depth.  kStats: the blocks'
-// softmax statistics (two fp32 rows of N) travel with it.
+// One ring's producer: block j into stage j % depth.  Stage depth - 1 is at
+// `last` (a tile's slot, once the tile is in TMEM) when last is not zero.
+// kStats: the tokens' softmax statistics (kStatBytes each, two arrays) travel
+// with the block.
+constexpr uint32_t kStatBytes = 16;
 template <int D, int B, bool kStats>
-__device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap* tm, int depth, uint32_t s0, int h,
-                                        const Blocks& blk, const BwdParams& p, uint32_t stat_s0) {
+__device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap* tm, int depth, uint32_t s0,
+                                        uint32_t last, int h, const Blocks& blk, const BwdParams& p,
+                                        uint32_t stat_s0) {
   constexpr uint32_t kBytes = B * D * 2;
   volatile int* abort_flag = &bars.abort;
   int j = 0;
   bool ok = true;
   for (; j < blk.nb; ++j) {
     const int st = j % depth, u = j / depth;
-    if (u >= 1) ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.empty[ring][st]), (u - 1) & 1, abort_flag, p.err,
-                                          kErrWaitProducer, p.limit_ns);
+    if (u >= 1)
+      ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.empty[ring][st]), (u - 1) & 1, abort_flag, p.err,
+                                kErrWaitProducer, p.limit_ns);
+    else if (last && st == depth - 1)
+      ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.tile_free), 0, abort_flag, p.err, kErrWaitProducer, p.limit_ns);
     if (!ok) break;
     const uint32_t fb = ptx::smem_addr(&bars.full[ring][st]);
-    const uint32_t n4 = kStats ? (uint32_t)blk.count(j) * 4 : 0;
-    ptx::mbar_arrive_expect_tx(fb, kBytes + 2 * n4);
+    const uint32_t dst = last && st == depth - 1 ? last : s0 + st * kBytes;
+    const uint32_t nb = kStats ? (uint32_t)blk.count(j) * kStatBytes : 0;
+    ptx::mbar_arrive_expect_tx(fb, kBytes + 2 * nb);
 #pragma unroll
     for (int half = 0; half < D / 64; ++half)
-      ptx::tma_load_3d(s0 + st * kBytes + half * (B * 128), tm, fb, half * 64, blk.start(j), h);
+      ptx::tma_load_3d(dst + half * (B * 128), tm, fb, half * 64, blk.start(j), h);
     if (kStats) {
-      const float* src = p.stats + (int64_t)h * p.N + blk.start(j);
-      bulk_load(stat_s0 + st * (2 * B * 4), src, n4, fb);
-      bulk_load(stat_s0 + st * (2 * B * 4) + B * 4, src + (int64_t)p.H * p.N, n4, fb);
+      const uint8_t* src = p.stats + ((int64_t)h * p.N + blk.start(j)) * kStatBytes;
+      bulk_load(stat_s0 + st * (2 * B * kStatBytes), src, nb, fb);
+      bulk_load(stat_s0 + st * (2 * B * kStatBytes) + B * kStatBytes, src + (int64_t)p.H * p.N * kStatBytes, nb, fb);
     }
   }
   if (!ok)  // let every copy this thread started land before the CTA exits
@@ -166,30 +186,31 @@ __device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap
 
 // D[128 x n] = A[128 x D] . B^T, A in TMEM (bf16 pairs) or K-major shared
 // memory, B the first n rows of a K-major block of kB rows.
-template <int D, int kB, bool kATmem>
+template <int D, int kB, bool kATmem, bool kAdd = false>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint64_t a_desc, uint64_t b_desc, int n) {
   const uint32_t idesc = ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint64_t b = b_desc + (((kk >> 2) * (kB * 128) + (kk & 3) * 32) >> 4);
     if (kATmem)
-      ptx::mma_ts(d, a_tmem + kk * 8, b, idesc, kk > 0 ? 1u : 0u);
+      ptx::mma_ts(d, a_tmem + kk * 8, b, idesc, kAdd || kk > 0 ? 1u : 0u);
     else
-      ptx::mma_ss(d, a_desc + (((kk >> 2) * (kRowsB * 128) + (kk & 3) * 32) >> 4), b, idesc, kk > 0 ? 1u : 0u);
+      ptx::mma_ss(d, a_desc + (((kk >> 2) * (kRowsB * 128) + (kk & 3) * 32) >> 4), b, idesc, kAdd || kk > 0 ? 1u : 0u);
   }
 }
 
 // D[128 x D] += A[128 x n] . B[n x D]: A's bf16 chunks of 16 columns in TMEM
 // (each in the first 8 columns of its 16), B a block read along its rows.
-template <int D, int kB>
+// kPart 0, 1: the first or second half of the chunks of each half of a full
+// block (the warpgroups release them in that order); 2: all.
+template <int D, int kB, int kPart>
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t b_desc, int n, bool first) {
   constexpr uint32_t idesc = ptx::idesc_bf16_f32(kRowsB, D, true);
-  if (n == kB) {
+  constexpr int kCh = kB / 16, kHalf = kCh / 2, kFirst = (kHalf + 1) / 2;
 #pragma unroll
-    for (int kk = 0; kk < kB / 16; ++kk)
-      ptx::mma_ts(d, a + kk * 16, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
-  } else {
-    for (int kk = 0; kk < n / 16; ++kk)
+  for (int kk = 0; kk < kCh; ++kk) {
+    const bool mine = kPart == 2 || (kk % kHalf < kFirst) == (kPart == 0);
+    if (mine && (n == kB || kk * 16 < n))
       ptx::mma_ts(d, a + kk * 16, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
   }
 }
@@ -223,7 +244,7 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 }
 
 // Common start of both kernels: error check, barriers, TMEM.
-#define FAS_BWD_PROLOGUE(soft_arrivals)                                                              \
+#define FAS_BWD_PROLOGUE()                                                                          \
   if (threadIdx.x == 0) bars.skip = *reinterpret_cast<volatile unsigned int*>(p.err) != 0u;          \
   __syncthreads();                                                                                   \
   if (bars.skip) return;                                                                             \
@@ -231,7 +252,7 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
   const int4 item = p.work[blockIdx.x];                                                              \
   const int h = item.x, f = item.y, tile = item.z;                                                   \
   const int2 sp = p.spans[f];                                                                        \
-  if (threadIdx.x == 0) init_bars(bars, soft_arrivals);                                              \
+  if (threadIdx.x == 0) init_bars(bars);                                                             \
   if (warp == kWarpMma) {                                                                            \
     ptx::tmem_alloc(ptx::smem_addr(&bars.tmem_base), kTmemAll);                                      \
     ptx::tmem_relinquish();                                                                          \
@@ -244,21 +265,25 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 
 // ------------------------------------------------------------- query pass
 //
-// Q and dO of the tile sit in TMEM as A operands; K and V blocks of 64 keys
-// stream through two rings.  Two S and two dP buffers: warpgroup g takes the
-// blocks j with j % 2 == g, so each group's waits hide behind the other's
-// arithmetic.  Tensor order: S(j+2), dQ(j), dP(j+2) for j = 0, 1, ...: S(j+2)
-// only needs S(j) to have been read into registers, and the group has 1024
-// clocks of tensor work (at d = 128) between the end of dP(j) and dQ(j).
-constexpr int kBq = 64;  // keys per block
+// Q and dO of the tile sit in TMEM as A operands; K and V blocks of 128 keys
+// stream through two rings (whose last stages are the tiles' own slots, free
+// once the tiles are in TMEM).  Both warpgroups work on the same block, each
+// on half of its columns.  Tensor order: S(j+1), dQ(j), dP(j+1): S(j+1) only
+// needs S(j) to have been read into registers, so dS(j) is computed under it
+// and P(j+1) under dQ(j) and dP(j+1).  dS is released in two halves, so that
+// dQ(j) starts on the first.  (Blocks of 64 keys in two S and two dP buffers,
+// the warpgroups alternating, left the tensor pipe half idle: an MMA of N =
+// 64 takes 32 clocks, less than the issue of the next.)
+constexpr int kBk = 128;  // keys per block
 
 template <int D>
 struct QLayout {
-  static constexpr uint32_t kAcc = 0, kS = D, kDp = D + 2 * kBq, kQ = D + 4 * kBq, kDo = kQ + D / 2;
+  static constexpr uint32_t kAcc = 0, kS = D, kDp = D + kBk, kQ = D + 2 * kBk, kDo = kQ + D / 2;
   static_assert(kDo + D / 2 <= kTmemAll, "TMEM columns");
-  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBq * D * 2;
-  static constexpr int kStK = D == 128 ? 5 : 6, kStV = D == 128 ? 4 : 6;  // K blocks stay from S(j) to dQ(j)
-  static constexpr size_t kSmem = 1024 + 2 * kTile + (kStK + kStV) * kBlock;
+  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBk * D * 2;
+  static_assert(kTile == kBlock, "a block reuses a tile's slot");
+  static constexpr int kStages = 3;  // per ring, the tile's slot among them
+  static constexpr size_t kSmem = 1024 + 2 * kStages * kBlock;
 };
 
 template <int D>
@@ -267,26 +292,27 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const BwdParams p) {
   using L = QLayout<D>;
+  constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ BarsB bars;
   __shared__ float red[4][128];  // partial sums: delta halves, then the keys' mean, then the rows' roundings
   __shared__ float centre[D];
-  const uint32_t q_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t do_s = q_s + L::kTile, k_s0 = do_s + L::kTile, v_s0 = k_s0 + L::kStK * L::kBlock;
-  FAS_BWD_PROLOGUE(128);
-  const Blocks blk(p.table[f], kBq);
+  const uint32_t k_s0 = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, q_s = k_s0 + (S - 1) * L::kBlock;
+  const uint32_t v_s0 = q_s + L::kTile, do_s = v_s0 + (S - 1) * L::kBlock;
+  FAS_BWD_PROLOGUE();
+  const Blocks blk(p.table[f], kBk);
 
   if (warp == kWarpK || warp == kWarpV) {
     if (lane == 0) {
       if (warp == kWarpK) {
         const uint32_t tb = ptx::smem_addr(&bars.tile_full);
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
-        load_tile<D>(q_s, &tm_q, tb, p, sp.x, f, h, tile);
-        load_tile<D>(do_s, &tm_do, tb, p, sp.x, f, h, tile);
-        produce<D, kBq, false>(bars, 0, &tm_k, L::kStK, k_s0, h, blk, p, 0);
+        load_tile<D>(q_s, &tm_q, tb, sp.x + tile * kRowsB, h);
+        load_tile<D>(do_s, &tm_do, tb, sp.x + tile * kRowsB, h);
+        produce<D, kBk, false>(bars, 0, &tm_k, S, k_s0, q_s, h, blk, p, 0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, kBq, false>(bars, 1, &tm_v, L::kStV, v_s0, h, blk, p, 0);
+        produce<D, kBk, false>(bars, 1, &tm_v, S, v_s0, do_s, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -294,44 +320,61 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       auto wait = [&](uint64_t& b, int parity) {
         return ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitMma, p.limit_ns);
       };
+      // Stage st of either ring is at its base + st * block (the tile's slot
+      // follows the dedicated stages).
       const uint64_t kd = ptx::smem_desc_sw128(k_s0, 16, 1024), vd = ptx::smem_desc_sw128(v_s0, 16, 1024);
-      const uint64_t kmn = ptx::smem_desc_sw128(k_s0, kBq * 128, 1024);
+      const uint64_t kmn = ptx::smem_desc_sw128(k_s0, kBk * 128, 1024);
       constexpr uint64_t kStep = L::kBlock >> 4;
-      auto s_mma = [&](int j) {
-        const int st = j % L::kStK;
-        if (!wait(bars.full[0][st], j / L::kStK)) return false;
-        mma_rows<D, kBq, true>(tmem + L::kS + (j & 1) * kBq, tmem + L::kQ, 0, kd + st * kStep, blk.count(j));
-        ptx::mma_commit(ptx::smem_addr(&bars.s_full[j & 1]));
+      int ks = 0, kph = 0, vs = 0, vph = 0, os = 0;  // ring positions: S's K, dP's V, dQ's K
+      auto s_mma = [&](int n) {
+        if (!wait(bars.full[0][ks], kph)) return false;
+        mma_rows<D, kBk, true>(tmem + L::kS, tmem + L::kQ, 0, kd + ks * kStep, n);
+        ptx::mma_commit(ptx::smem_addr(&bars.s_full));
+        if (++ks == S) {
+          ks = 0;
+          kph ^= 1;
+        }
         return true;
       };
-      auto dp_mma = [&](int j) {
-        const int st = j % L::kStV;
-        if (!wait(bars.full[1][st], j / L::kStV)) return false;
-        mma_rows<D, kBq, true>(tmem + L::kDp + (j & 1) * kBq, tmem + L::kDo, 0, vd + st * kStep, blk.count(j));
-        ptx::mma_commit(ptx::smem_addr(&bars.dp_full[j & 1]));
-        ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
+      auto dp_mma = [&](int n) {
+        if (!wait(bars.full[1][vs], vph)) return false;
+        mma_rows<D, kBk, true>(tmem + L::kDp, tmem + L::kDo, 0, vd + vs * kStep, n);
+        ptx::mma_commit(ptx::smem_addr(&bars.dp_full));
+        ptx::mma_commit(ptx::smem_addr(&bars.empty[1][vs]));
+        if (++vs == S) {
+          vs = 0;
+          vph ^= 1;
+        }
         return true;
       };
       bool ok = wait(bars.tile_full, 0);
+      int n = blk.count(0);
       if (ok) {
         tile_to_tmem<D>(tmem + L::kQ, ptx::smem_desc_sw128(q_s, 16, 1024));
         tile_to_tmem<D>(tmem + L::kDo, ptx::smem_desc_sw128(do_s, 16, 1024));
+        ptx::mma_commit(ptx::smem_addr(&bars.tile_free));
+        ok = s_mma(n) && dp_mma(n);
       }
-      for (int j = 0; ok && j < 2 && j < blk.nb; ++j) ok = s_mma(j) && dp_mma(j);
       for (int j = 0; ok && j < blk.nb; ++j) {
-        const bool more = j + 2 < blk.nb;
+        const bool more = j + 1 < blk.nb;
+        const int n1 = more ? blk.count(j + 1) : 0;
         if (more) {
-          ok = wait(bars.s_free[j & 1], j >> 1);
+          ok = wait(bars.s_free, j);
           ptx::tc_fence_after_sync();
-          ok = ok && s_mma(j + 2);
+          ok = ok && s_mma(n1);
         }
-        ok = ok && wait(bars.ds_full[j & 1], j >> 1);
+        ok = ok && wait(bars.ds_full[0], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBq>(tmem + L::kAcc, tmem + L::kDp + (j & 1) * kBq, kmn + (j % L::kStK) * kStep, blk.count(j),
-                        j == 0);
-        ptx::mma_commit(ptx::smem_addr(&bars.empty[0][j % L::kStK]));
-        if (more) ok = dp_mma(j + 2);
+        mma_acc<D, kBk, 0>(tmem + L::kAcc, tmem + L::kDp, kmn + os * kStep, n, j == 0);
+        ok = wait(bars.ds_full[1], j);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        mma_acc<D, kBk, 1>(tmem + L::kAcc, tmem + L::kDp, kmn + os * kStep, n, false);
+        ptx::mma_commit(ptx::smem_addr(&bars.empty[0][os]));
+        if (++os == S) os = 0;
+        if (more) ok = dp_mma(n1);
+        n = n1;
       }
       ptx::mma_commit(ptx::smem_addr(&bars.acc_full));
       ptx::mma_commit(ptx::smem_addr(&bars.drain));
@@ -370,23 +413,24 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     ptx::named_barrier_sync(1, kSoftThreads);
     delta = red[0][trow] + red[1][trow];
     // A row past the frame's end gets P = 0 and is never stored.
-    const float nl = valid ? -p.lse[(int64_t)h * p.N + token] * kLog2eB : -INFINITY;
-    if (valid && g == 0) {
-      float* st = p.stats + (int64_t)h * p.N + token;
-      st[0] = nl;
-      st[(int64_t)p.H * p.N] = -delta;
+    const float lse = valid ? p.lse[(int64_t)h * p.N + token] : INFINITY;
+    const float nl = -lse * kLog2eB;
+    if (valid) {  // group 0: -lse / s, group 1: -delta, as the key pass's MMA takes them
+      uint8_t* st = p.stats + ((int64_t)g * p.H * p.N + (int64_t)h * p.N + token) * kStatBytes;
+      *reinterpret_cast<uint4*>(st) = split3(g == 0 ? -lse / p.scale : -delta);
     }
     ptx::named_barrier_sync(1, kSoftThreads);
-    // The mean of the first block's keys, from its shared-memory stage (the
-    // 128-byte swizzle permutes the 16-byte pieces of a row by row % 8).
+    // The mean of the first block's keys (64 of them at most), from its
+    // shared-memory stage (the 128-byte swizzle permutes the 16-byte pieces
+    // of a row by row % 8).
     bool ok = wait(bars.full[0][0], 0);
     {
       constexpr int kParts = kSoftThreads / (D / 2);
-      const int cp = tid % (D / 2), part = tid / (D / 2), n = blk.count(0);
+      const int cp = tid % (D / 2), part = tid / (D / 2), n = min(blk.count(0), 64);
       float c0 = 0.f, c1 = 0.f;
       if (ok)
         for (int r = part; r < n; r += kParts) {
-          const uint32_t off = (cp / 32) * (kBq * 128) + r * 128 + ((((cp % 32) / 4) ^ (r & 7)) * 16) + (cp % 4) * 4;
+          const uint32_t off = (cp / 32) * (kBk * 128) + r * 128 + ((((cp % 32) / 4) ^ (r & 7)) * 16) + (cp % 4) * 4;
           const uint32_t w = *reinterpret_cast<const uint32_t*>(smem_raw + (k_s0 - ptx::smem_addr(smem_raw)) + off);
           c0 += __uint_as_float(w << 16);
           c1 += __uint_as_float(w & 0xFFFF0000u);
@@ -406,16 +450,17 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB), nl2 = ptx::f32x2(nl, nl);
     const float nd = -delta;
     float e0 = 0.f, e1 = 0.f;  // what rounding dS to bf16 added to the row
-    constexpr int kCh = kBq / 16;
-    for (int j = g; ok && j < blk.nb; j += 2) {
-      const int nch = blk.count(j) / 16;
-      ok = wait(bars.s_full[g], j >> 1);
+    constexpr int kCh = kBk / 32, kFirst = (kCh + 1) / 2;  // chunks of 16 columns per group
+    const uint32_t sbase = tmem + lane_base + L::kS + g * (kBk / 2), dbase = tmem + lane_base + L::kDp + g * (kBk / 2);
+    for (int j = 0; ok && j < blk.nb; ++j) {
+      const int nch = blk.count(j) / 16 - g * kCh;  // this half's chunks that hold keys
+      ok = wait(bars.s_full, j);
       if (!ok) break;
       ptx::tc_fence_after_sync();
       uint32_t r[kCh][16];
-      core::load_chunks<0, kCh>(tmem + lane_base + L::kS + g * kBq, r);
+      core::load_chunks<0, kCh>(sbase, r);
       ptx::tc_fence_before_sync();
-      ptx::mbar_arrive(ptx::smem_addr(&bars.s_free[g]));
+      ptx::mbar_arrive(ptx::smem_addr(&bars.s_free));
       float pr[kCh][16];
 #pragma unroll
       for (int u = 0; u < kCh; ++u)
@@ -426,31 +471,41 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           pr[u][2 * e] = ptx::ex2(x0);
           pr[u][2 * e + 1] = ptx::ex2(x1);
         }
-      ok = wait(bars.dp_full[g], j >> 1);
+      ok = wait(bars.dp_full, j);
       if (!ok) break;
       ptx::tc_fence_after_sync();
-      const uint32_t dbase = tmem + lane_base + L::kDp + g * kBq;
       core::load_chunks<0, kCh>(dbase, r);
+      uint32_t pk[kCh][8];
 #pragma unroll
       for (int u = 0; u < kCh; ++u) {
-        uint32_t pk[8];
-        float a0 = 0.f, a1 = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float x0 = __uint_as_float(r[u][2 * e]), x1 = __uint_as_float(r[u][2 * e + 1]);
           ptx::add_f32x2(x0, x1, nd, nd);
-          mul_f32x2(x0, x1, x0, x1, pr[u][2 * e], pr[u][2 * e + 1]);
-          pk[e] = ptx::pack_bf16x2(x0, x1);
-          ptx::add_f32x2(a0, a1, __uint_as_float(pk[e] << 16) - x0, __uint_as_float(pk[e] & 0xFFFF0000u) - x1);
+          mul_f32x2(pr[u][2 * e], pr[u][2 * e + 1], x0, x1, pr[u][2 * e], pr[u][2 * e + 1]);  // dS
+          pk[u][e] = ptx::pack_bf16x2(pr[u][2 * e], pr[u][2 * e + 1]);
         }
-        // Columns past the range's end hold leftovers: not part of the sum.
+        ptx::tmem_st8(dbase + u * 16, pk[u]);
+        if (u == kFirst - 1 || u == kCh - 1) {
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before_sync();
+          ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[u == kCh - 1]));
+        }
+      }
+      // Off the tensor pipe's path: what the roundings add up to.  Columns
+      // past the range's end hold leftovers and do not count.
+#pragma unroll
+      for (int u = 0; u < kCh; ++u) {
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float w0 = __uint_as_float(pk[u][e] << 16), w1 = __uint_as_float(pk[u][e] & 0xFFFF0000u);
+          ptx::add_f32x2(w0, w1, -pr[u][2 * e], -pr[u][2 * e + 1]);
+          ptx::add_f32x2(a0, a1, w0, w1);
+        }
         e0 += u < nch ? a0 : 0.f;
         e1 += u < nch ? a1 : 0.f;
-        ptx::tmem_st8(dbase + u * 16, pk);
       }
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before_sync();
-      ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[g]));
     }
     red[g][trow] = e0 + e1;
     ok = ok && wait(bars.acc_full, 0);
@@ -462,17 +517,17 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
       for (int u = 0; u < kOut; ++u) {
         const int c0 = (g * kOut + u) * 16;
-        uint32_t o[16], pk[8];
+        uint32_t o[16], w[8];
         ptx::tmem_ld16(tmem + lane_base + L::kAcc + c0, o);
         ptx::tmem_ld_wait(o);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          pk[e] = ptx::pack_bf16x2(fmaf(-extra, centre[c0 + 2 * e], __uint_as_float(o[2 * e])) * p.scale,
-                                   fmaf(-extra, centre[c0 + 2 * e + 1], __uint_as_float(o[2 * e + 1])) * p.scale);
+          w[e] = ptx::pack_bf16x2(fmaf(-extra, centre[c0 + 2 * e], __uint_as_float(o[2 * e])) * p.scale,
+                                  fmaf(-extra, centre[c0 + 2 * e + 1], __uint_as_float(o[2 * e + 1])) * p.scale);
         if (valid) {
           uint4* d4 = reinterpret_cast<uint4*>(p.dq + at + c0);
-          d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
     }
@@ -495,15 +550,23 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // work on the same block, each on half of its columns.  Tensor order: dV(j),
 // S(j+1), dK(j), dP(j+1): P(j+1) is computed under dK(j) and dP(j+1), dS(j)
 // under dV(j) and S(j+1).
+//
+// The softmax statistics differ by column here.  They enter through the MMA:
+// one more K step of 16 whose A operand holds ones in three columns and whose
+// B operand holds -lse / s (for S^T) or -delta (for dP^T) split into three
+// bf16 values a query, so the accumulators come out as S^T - lse / s and dP^T
+// - delta.  (Read from shared memory as vectors per column, they took 30% of
+// its cycles, which the MMAs' operands need: 73% of the tensor rate.)
 template <int D, int BQ, bool kKT, bool kVT>
 struct KLayout {
   static constexpr uint32_t kDk = 0, kDv = D, kS = 2 * D, kDp = 2 * D + BQ, kK = 2 * D + 2 * BQ,
                             kV = kK + (kKT ? D / 2 : 0);
   static_assert(kV + (kVT ? D / 2 : 0) <= kTmemAll, "TMEM columns");
   static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = BQ * D * 2;
-  static constexpr int kFit = (int)((232448 - 1024 - 2 * kTile - 1024 - 2048) / (2 * kBlock + 2 * BQ * 4));
+  static constexpr uint32_t kStat = 2 * BQ * kStatBytes, kOnes = 2 * kRowsB * 16;  // ones (16 columns), a stage's statistics
+  static constexpr int kFit = (int)((232448 - 1024 - 512 - kOnes - 2 * kTile) / (2 * kBlock + kStat));
   static constexpr int kStages = kFit < kMaxStagesB ? kFit : kMaxStagesB;
-  static constexpr size_t kSmem = 1024 + 2 * kTile + 2 * kStages * kBlock + kStages * 2 * BQ * 4;
+  static constexpr size_t kSmem = 1024 + kOnes + 2 * kTile + kStages * (2 * kBlock + kStat);
 };
 
 template <int D, int BQ, bool kKT, bool kVT>
@@ -516,8 +579,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   __shared__ BarsB bars;
   const uint32_t k_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t v_s = k_s + L::kTile, q_s0 = v_s + L::kTile, do_s0 = q_s0 + L::kStages * L::kBlock;
-  const uint32_t stat_s0 = do_s0 + L::kStages * L::kBlock;
-  FAS_BWD_PROLOGUE(kSoftThreads);
+  const uint32_t stat_s0 = do_s0 + L::kStages * L::kBlock, ones_s = stat_s0 + L::kStages * L::kStat;
+  // The ones: 128 rows of {1, 1, 1, 0, 0, 0, 0, 0}, then 128 rows of zeros
+  // (columns 8 .. 15; the statistics' columns 8 .. 15 may then be anything
+  // finite, and alias columns 0 .. 7).
+  for (uint32_t i = threadIdx.x; i < L::kOnes / 16; i += kThreadsB)
+    *reinterpret_cast<uint4*>(smem_raw + (ones_s - ptx::smem_addr(smem_raw)) + i * 16) =
+        i < kRowsB ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();
+  FAS_BWD_PROLOGUE();
   const Blocks blk(p.table[f], BQ);
 
   if (warp == kWarpK || warp == kWarpV) {
@@ -525,12 +595,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (warp == kWarpK) {
         const uint32_t tb = ptx::smem_addr(&bars.tile_full);
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
-        load_tile<D>(k_s, &tm_k, tb, p, sp.x, f, h, tile);
-        load_tile<D>(v_s, &tm_v, tb, p, sp.x, f, h, tile);
-        produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
+        load_tile<D>(k_s, &tm_k, tb, sp.x + tile * kRowsB, h);
+        load_tile<D>(v_s, &tm_v, tb, sp.x + tile * kRowsB, h);
+        produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, 0, h, blk, p, stat_s0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, BQ, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
+        produce<D, BQ, false>(bars, 1, &tm_do, L::kStages, do_s0, 0, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -541,42 +611,55 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       const uint64_t kdesc = ptx::smem_desc_sw128(k_s, 16, 1024), vdesc = ptx::smem_desc_sw128(v_s, 16, 1024);
       const uint64_t qd = ptx::smem_desc_sw128(q_s0, 16, 1024), dod = ptx::smem_desc_sw128(do_s0, 16, 1024);
       const uint64_t qmn = ptx::smem_desc_sw128(q_s0, BQ * 128, 1024), domn = ptx::smem_desc_sw128(do_s0, BQ * 128, 1024);
-      constexpr uint64_t kStep = L::kBlock >> 4;
-      auto s_mma = [&](int j) {
-        const int st = j % L::kStages;
-        if (!wait(bars.full[0][st], j / L::kStages)) return false;
-        mma_rows<D, BQ, kKT>(tmem + L::kS, tmem + L::kK, kdesc, qd + st * kStep, blk.count(j));
-        ptx::mma_commit(ptx::smem_addr(&bars.s_full[0]));
+      const uint64_t ones = smem_desc_plain(ones_s, kRowsB * 16), stat = smem_desc_plain(stat_s0, 0);
+      constexpr uint64_t kStep = L::kBlock >> 4, kStatStep = L::kStat >> 4;
+      int qs = 0, qph = 0, ds = 0, dph = 0;  // ring positions of S's Q and dP's dO
+      auto s_mma = [&](int n) {
+        if (!wait(bars.full[0][qs], qph)) return false;
+        ptx::mma_ss(tmem + L::kS, ones, stat + qs * kStatStep, ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
+        mma_rows<D, BQ, kKT, true>(tmem + L::kS, tmem + L::kK, kdesc, qd + qs * kStep, n);
+        ptx::mma_commit(ptx::smem_addr(&bars.s_full));
         return true;
       };
-      auto dp_mma = [&](int j) {
-        const int st = j % L::kStages;
-        if (!wait(bars.full[1][st], j / L::kStages)) return false;
-        mma_rows<D, BQ, kVT>(tmem + L::kDp, tmem + L::kV, vdesc, dod + st * kStep, blk.count(j));
-        ptx::mma_commit(ptx::smem_addr(&bars.dp_full[0]));
+      auto dp_mma = [&](int n) {  // the same block as the last s_mma
+        if (!wait(bars.full[1][ds], dph)) return false;
+        ptx::mma_ss(tmem + L::kDp, ones, stat + qs * kStatStep + (BQ * kStatBytes >> 4),
+                    ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
+        mma_rows<D, BQ, kVT, true>(tmem + L::kDp, tmem + L::kV, vdesc, dod + ds * kStep, n);
+        ptx::mma_commit(ptx::smem_addr(&bars.dp_full));
         return true;
+      };
+      auto next = [](int& st, int& ph) {
+        if (++st == L::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
       };
       bool ok = wait(bars.tile_full, 0);
+      int n = blk.count(0);
       if (ok) {
         if (kKT) tile_to_tmem<D>(tmem + L::kK, kdesc);
         if (kVT) tile_to_tmem<D>(tmem + L::kV, vdesc);
-        ok = s_mma(0) && dp_mma(0);
+        ok = s_mma(n) && dp_mma(n);
       }
       for (int j = 0; ok && j < blk.nb; ++j) {
-        const int st = j % L::kStages, n = blk.count(j);
         const bool more = j + 1 < blk.nb;
+        const int n1 = more ? blk.count(j + 1) : 0, st = qs;  // st: block j's stage in both rings
         ok = wait(bars.p_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        mma_acc<D, BQ, 2>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
-        if (more) ok = s_mma(j + 1);
+        next(qs, qph);
+        next(ds, dph);
+        if (more) ok = s_mma(n1);
         ok = ok && wait(bars.ds_full[0], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
+        mma_acc<D, BQ, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][st]));
-        if (more) ok = dp_mma(j + 1);
+        if (more) ok = dp_mma(n1);
+        n = n1;
       }
       ptx::mma_commit(ptx::smem_addr(&bars.acc_full));
       ptx::mma_commit(ptx::smem_addr(&bars.drain));
@@ -592,18 +675,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                                              p.limit_ns);
       return (bool)__all_sync(0xffffffffu, got);
     };
-    const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB);
+    const float c = p.scale * kLog2eB;
     constexpr int kCh = BQ / 32;  // chunks of 16 columns per group
-    const float* const stat0 =
-        reinterpret_cast<const float*>(smem_raw + (stat_s0 - ptx::smem_addr(smem_raw))) + g * (BQ / 2);
     const uint32_t sbase = tmem + lane_base + L::kS + g * (BQ / 2), dbase = tmem + lane_base + L::kDp + g * (BQ / 2);
     bool ok = true;
     for (int j = 0; ok && j < blk.nb; ++j) {
-      const int st = j % L::kStages;
-      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(stat0 + st * (2 * BQ));
-      const float4* nd = reinterpret_cast<const float4*>(stat0 + st * (2 * BQ) + BQ);
-      // The block's statistics came with its Q block (complete before S).
-      ok = wait(bars.full[0][st], j / L::kStages) && wait(bars.s_full[0], j);
+      ok = wait(bars.s_full, j);
       if (!ok) break;
       ptx::tc_fence_after_sync();
       uint32_t r[kCh][16];
@@ -613,24 +690,19 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       for (int u = 0; u < kCh; ++u) {
         uint32_t pk[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const ulonglong2 l = nl[u * 4 + e];
-          float x0, x1, x2, x3;
-          ptx::fma_f32x2(x0, x1, __uint_as_float(r[u][4 * e]), __uint_as_float(r[u][4 * e + 1]), c2, l.x);
-          ptx::fma_f32x2(x2, x3, __uint_as_float(r[u][4 * e + 2]), __uint_as_float(r[u][4 * e + 3]), c2, l.y);
-          pr[u][4 * e] = ptx::ex2(x0);
-          pr[u][4 * e + 1] = ptx::ex2(x1);
-          pr[u][4 * e + 2] = ptx::ex2(x2);
-          pr[u][4 * e + 3] = ptx::ex2(x3);
-          pk[2 * e] = ptx::pack_bf16x2(pr[u][4 * e], pr[u][4 * e + 1]);
-          pk[2 * e + 1] = ptx::pack_bf16x2(pr[u][4 * e + 2], pr[u][4 * e + 3]);
+        for (int e = 0; e < 8; ++e) {
+          float x0, x1;
+          mul_f32x2(x0, x1, __uint_as_float(r[u][2 * e]), __uint_as_float(r[u][2 * e + 1]), c, c);
+          pr[u][2 * e] = ptx::ex2(x0);
+          pr[u][2 * e + 1] = ptx::ex2(x1);
+          pk[e] = ptx::pack_bf16x2(pr[u][2 * e], pr[u][2 * e + 1]);
         }
         ptx::tmem_st8(sbase + u * 16, pk);
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before_sync();
       ptx::mbar_arrive(ptx::smem_addr(&bars.p_full));
-      ok = wait(bars.dp_full[0], j);
+      ok = wait(bars.dp_full, j);
       if (!ok) break;
       ptx::tc_fence_after_sync();
       core::load_chunks<0, kCh>(dbase, r);
@@ -638,23 +710,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       for (int u = 0; u < kCh; ++u) {
         uint32_t pk[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 d = nd[u * 4 + e];
-          float x0 = __uint_as_float(r[u][4 * e]), x1 = __uint_as_float(r[u][4 * e + 1]);
-          float x2 = __uint_as_float(r[u][4 * e + 2]), x3 = __uint_as_float(r[u][4 * e + 3]);
-          ptx::add_f32x2(x0, x1, d.x, d.y);
-          ptx::add_f32x2(x2, x3, d.z, d.w);
-          mul_f32x2(x0, x1, x0, x1, pr[u][4 * e], pr[u][4 * e + 1]);
-          mul_f32x2(x2, x3, x2, x3, pr[u][4 * e + 2], pr[u][4 * e + 3]);
-          pk[2 * e] = ptx::pack_bf16x2(x0, x1);
-          pk[2 * e + 1] = ptx::pack_bf16x2(x2, x3);
+        for (int e = 0; e < 8; ++e) {
+          float x0, x1;
+          mul_f32x2(x0, x1, __uint_as_float(r[u][2 * e]), __uint_as_float(r[u][2 * e + 1]), pr[u][2 * e],
+                    pr[u][2 * e + 1]);
+          pk[e] = ptx::pack_bf16x2(x0, x1);
         }
         ptx::tmem_st8(dbase + u * 16, pk);
       }
       ptx::tmem_st_wait();
-      // The statistics' stage goes back to the producer behind dK(j): these
-      // reads come before its next copy.
-      ptx::fence_proxy_async_smem();
       ptx::tc_fence_before_sync();
       ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[0]));
     }
@@ -703,22 +767,8 @@ struct KConfig<64> {
   static constexpr bool kKT = true, kVT = true;
 };
 
-// Tensor maps: 128-row tiles ({d, T, Nf, H} by frame or {d, N, H} by token)
-// and blocks of `box` tokens.
-int tile_map(CUtensorMap* m, const void* base, int d, const BwdParams& p) {
-  const cuuint64_t D = (cuuint64_t)d, rs = (cuuint64_t)p.row_stride * 2, hs = (cuuint64_t)p.head_stride * 2;
-  if (p.by_frame) {
-    const cuuint64_t dims[4] = {D, (cuuint64_t)p.T, (cuuint64_t)p.Nf, (cuuint64_t)p.H};
-    const cuuint64_t strides[3] = {rs, (cuuint64_t)p.T * rs, hs};
-    const cuuint32_t box[4] = {64, (cuuint32_t)kRowsB, 1, 1};
-    return bf16_tensor_map(m, base, 4, dims, strides, box);
-  }
-  const cuuint64_t dims[3] = {D, (cuuint64_t)p.N, (cuuint64_t)p.H};
-  const cuuint64_t strides[2] = {rs, hs};
-  const cuuint32_t box[3] = {64, (cuuint32_t)kRowsB, 1};
-  return bf16_tensor_map(m, base, 3, dims, strides, box);
-}
-int block_map(CUtensorMap* m, const void* base, int d, int rows, const BwdParams& p) {
+// Tensor map {d, N, H} with boxes of `rows` tokens.
+int token_map(CUtensorMap* m, const void* base, int d, int rows, const BwdParams& p) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.N, (cuuint64_t)p.H};
   const cuuint64_t strides[2] = {(cuuint64_t)p.row_stride * 2, (cuuint64_t)p.head_stride * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
@@ -730,18 +780,22 @@ int launch(const BwdParams& p, int grid, cudaStream_t st) {
   using C = KConfig<D>;
   using LQ = QLayout<D>;
   using LK = KLayout<D, C::kB, C::kKT, C::kVT>;
-  CUtensorMap tq, tdo, tk, tv, bq, bdo, bk, bv;
-  if (tile_map(&tq, p.q, D, p) != FAS_OK || tile_map(&tdo, p.dout, D, p) != FAS_OK ||
-      tile_map(&tk, p.k, D, p) != FAS_OK || tile_map(&tv, p.v, D, p) != FAS_OK ||
-      block_map(&bk, p.k, D, kBq, p) != FAS_OK || block_map(&bv, p.v, D, kBq, p) != FAS_OK ||
-      block_map(&bq, p.q, D, C::kB, p) != FAS_OK || block_map(&bdo, p.dout, D, C::kB, p) != FAS_OK)
+  static_assert(kBk == kRowsB, "tiles and the query pass's blocks share tensor maps");
+  CUtensorMap tq, tdo, tk, tv, bq, bdo;
+  if (token_map(&tq, p.q, D, kRowsB, p) != FAS_OK || token_map(&tdo, p.dout, D, kRowsB, p) != FAS_OK ||
+      token_map(&tk, p.k, D, kRowsB, p) != FAS_OK || token_map(&tv, p.v, D, kRowsB, p) != FAS_OK)
+    return -1;
+  bq = tq;
+  bdo = tdo;
+  if (C::kB != kRowsB &&
+      (token_map(&bq, p.q, D, C::kB, p) != FAS_OK || token_map(&bdo, p.dout, D, C::kB, p) != FAS_OK))
     return -1;
   auto kq = attention_bwd_q<D>;
   auto kk = attention_bwd_k<D, C::kB, C::kKT, C::kVT>;
   if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LQ::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LK::kSmem) != cudaSuccess)
     return -1;
-  kq<<<grid, kThreadsB, LQ::kSmem, st>>>(tq, tdo, bk, bv, p);
+  kq<<<grid, kThreadsB, LQ::kSmem, st>>>(tq, tdo, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   kk<<<grid, kThreadsB, LK::kSmem, st>>>(tk, tv, bq, bdo, p);
   return cudaGetLastError() == cudaSuccess ? 2 : -1;

@@ -163,15 +163,15 @@ struct BwdParams {
   const int4* work;        // [n_work] {head, frame, 128-row tile, -}
   const int4* table;       // [Nf] {start0, len0, start1, len1}
   const int2* spans;       // [Nf] {first token, tokens} of each frame
-  int by_frame;            // tiles are read by frame (uniform frames), else by token
   const uint16_t *q, *k, *v, *out, *dout;  // bf16, row (h, j) at + h * head_stride + j * row_stride
   uint16_t *dq, *dk, *dv;
   int64_t row_stride, head_stride;         // elements
   const float* lse;        // [H, N]
-  float* stats;            // [2, H, N]: -lse log2(e) and -delta, written by the query pass, read by the key pass
+  uint8_t* stats;          // [2, H, N] rows of 16 bytes: -lse / scale and -delta as sums of three bf16 values,
+                           // written by the query pass, read by the key pass
   unsigned int* err;       // device error word
   int64_t N;
-  int T, Nf, H;
+  int H;
   float scale;             // 1 / sqrt(d)
   uint64_t limit_ns;
 };

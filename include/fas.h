@@ -384,10 +384,10 @@ int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded,
  *   dq_i = s sum_j dS_ij k_j   dk_j = s sum_i dS_ij q_i   dv_j = sum_i P_ij dout_i
  * q, k, v, out, lse: fas_forward's inputs and outputs (any mode; the prepass
  * is not needed again); dout: the gradient of out.  dq, dk, dv: outputs.  All
- * bf16 in the current layout.  stats: device fp32 [2, H, N], a workspace
- * (it receives -lse log2(e) and -delta; the caller's memory, so that calls on
- * other streams, and captured graphs, share nothing but the plan's read-only
- * tables and the error word).  Sums are fp32; P and dS
+ * bf16 in the current layout.  workspace: device memory of
+ * FAS_BACKWARD_WORKSPACE(H, N) bytes, 16-byte aligned, the call's own until
+ * it has run (calls on other streams, and captured graphs, then share nothing
+ * but the plan's read-only tables and the error word).  Sums are fp32; P and dS
  * are rounded to bf16 for the products.  Every output row is written exactly
  * once, by one CTA in a fixed order: results are bit-reproducible.  Tokens a
  * row does not see are not read into it, whatever they hold.  Needs a plan
@@ -395,8 +395,9 @@ int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded,
  * returns FAS_ERR_ARG.  Asynchronous on cuda_stream; may be captured into a
  * graph.  (The page has no training; its section "Deleting the Mask" gives
  * the visibility.) */
+#define FAS_BACKWARD_WORKSPACE(H, N) (32 * (int64_t)(H) * (int64_t)(N))
 int fas_backward(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
-                 void* dq, void* dk, void* dv, float* stats, void* cuda_stream);
+                 void* dq, void* dk, void* dv, void* workspace, void* cuda_stream);
 
 /* The norms around a block, its gate and its residual, in one kernel.  For
  * token n of frame f, with the block's output y (bf16 [tokens, width]) and
