@@ -69,12 +69,13 @@ struct Blocks {
 };
 
 struct BarsB {
-  uint64_t tile_full, tile_free;   // the tiles have landed; they have been copied to TMEM
+  uint64_t tile_full;
   uint64_t full[2][kMaxStagesB];   // [ring][stage]
   uint64_t empty[2][kMaxStagesB];
   uint64_t s_full, dp_full;
-  uint64_t s_free;                 // query pass: S read into registers
-  uint64_t p_full, ds_full[2];
+  uint64_t s_free, dp_free;        // query pass: S, dP read into registers
+  uint64_t p_full, ds_full;        // P, dS stored as bf16
+  uint64_t acc_done;               // query pass: dQ(j) has read dS(j)
   uint64_t acc_full, drain;
   uint32_t tmem_base;
   int abort, skip;
@@ -83,18 +84,19 @@ struct BarsB {
 __device__ __forceinline__ void init_bars(BarsB& b) {
   auto one = [](uint64_t& x, int n) { ptx::mbar_init(ptx::smem_addr(&x), n); };
   one(b.tile_full, 1);
-  one(b.tile_free, 1);
   for (int i = 0; i < 2; ++i) {
     for (int s = 0; s < kMaxStagesB; ++s) {
       one(b.full[i][s], 1);
       one(b.empty[i][s], 1);
     }
-    one(b.ds_full[i], kSoftThreads);
   }
   one(b.s_full, 1);
   one(b.dp_full, 1);
   one(b.s_free, kSoftThreads);
+  one(b.dp_free, kSoftThreads);
   one(b.p_full, kSoftThreads);
+  one(b.ds_full, kSoftThreads);
+  one(b.acc_done, 1);
   one(b.acc_full, 1);
   one(b.drain, 1);
   b.abort = 0;
@@ -136,24 +138,28 @@ __device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// Loads a 128-row tile.  Rows past the frame's end are the next frame's (or
-// zeros past the last token): every row of a tile is computed by itself, and
-// those are never stored.
-template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int first, int h) {
+// Loads `kRows` tokens of a head from token `first` as a K-major tile of 64-
+// column halves, in boxes of kBox tokens (one tensor map serves tiles and
+// blocks of every size).  A tile's rows past the frame's end are the next
+// frame's (or zeros past the last token): every row of a tile is computed by
+// itself, and those are never stored.
+constexpr int kBox = 32;
+template <int D, int kRows>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int first, int h) {
+  static_assert(kRows % kBox == 0, "");
 #pragma unroll
-  for (int half = 0; half < D / 64; ++half) ptx::tma_load_3d(dst + half * (kRowsB * 128), tm, bar, half * 64, first, h);
+  for (int half = 0; half < D / 64; ++half)
+#pragma unroll
+    for (int r = 0; r < kRows; r += kBox)
+      ptx::tma_load_3d(dst + half * (kRows * 128) + r * 128, tm, bar, half * 64, first + r, h);
 }
 
-// One ring's producer: block j into stage j % depth.  Stage depth - 1 is at
-// `last` (a tile's slot, once the tile is in TMEM) when last is not zero.
-// kStats: the tokens' softmax statistics (kStatBytes each, two arrays) travel
-// with the block.
+// One ring's producer: block j into stage j % depth.  kStats: the tokens'
+// softmax statistics (kStatBytes each, two arrays) travel with the block.
 constexpr uint32_t kStatBytes = 16;
 template <int D, int B, bool kStats>
-__device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap* tm, int depth, uint32_t s0,
-                                        uint32_t last, int h, const Blocks& blk, const BwdParams& p,
-                                        uint32_t stat_s0) {
+__device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap* tm, int depth, uint32_t s0, int h,
+                                        const Blocks& blk, const BwdParams& p, uint32_t stat_s0) {
   constexpr uint32_t kBytes = B * D * 2;
   volatile int* abort_flag = &bars.abort;
   int j = 0;
@@ -163,16 +169,11 @@ __device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap
     if (u >= 1)
       ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.empty[ring][st]), (u - 1) & 1, abort_flag, p.err,
                                 kErrWaitProducer, p.limit_ns);
-    else if (last && st == depth - 1)
-      ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.tile_free), 0, abort_flag, p.err, kErrWaitProducer, p.limit_ns);
     if (!ok) break;
     const uint32_t fb = ptx::smem_addr(&bars.full[ring][st]);
-    const uint32_t dst = last && st == depth - 1 ? last : s0 + st * kBytes;
     const uint32_t nb = kStats ? (uint32_t)blk.count(j) * kStatBytes : 0;
     ptx::mbar_arrive_expect_tx(fb, kBytes + 2 * nb);
-#pragma unroll
-    for (int half = 0; half < D / 64; ++half)
-      ptx::tma_load_3d(dst + half * (B * 128), tm, fb, half * 64, blk.start(j), h);
+    load_rows<D, B>(s0 + st * kBytes, tm, fb, blk.start(j), h);
     if (kStats) {
       const uint8_t* src = p.stats + ((int64_t)h * p.N + blk.start(j)) * kStatBytes;
       bulk_load(stat_s0 + st * (2 * B * kStatBytes), src, nb, fb);
@@ -199,20 +200,15 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint64_t a
   }
 }
 
-// D[128 x D] += A[128 x n] . B[n x D]: A's bf16 chunks of 16 columns in TMEM
-// (each in the first 8 columns of its 16), B a block read along its rows.
-// kPart 0, 1: the first or second half of the chunks of each half of a full
-// block (the warpgroups release them in that order); 2: all.
-template <int D, int kB, int kPart>
+// D[128 x D] += A[128 x n] . B[n x D]: A's bf16 chunks of 16 columns in TMEM,
+// kStride columns apart (8 each), B a block read along its rows.
+template <int D, int kB, int kStride>
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t b_desc, int n, bool first) {
   constexpr uint32_t idesc = ptx::idesc_bf16_f32(kRowsB, D, true);
-  constexpr int kCh = kB / 16, kHalf = kCh / 2, kFirst = (kHalf + 1) / 2;
 #pragma unroll
-  for (int kk = 0; kk < kCh; ++kk) {
-    const bool mine = kPart == 2 || (kk % kHalf < kFirst) == (kPart == 0);
-    if (mine && (n == kB || kk * 16 < n))
-      ptx::mma_ts(d, a + kk * 16, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
-  }
+  for (int kk = 0; kk < kB / 16; ++kk)
+    if (n == kB || kk * 16 < n)
+      ptx::mma_ts(d, a + kk * kStride, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
 }
 
 // A 128-row K-major tile into TMEM as an A operand.
@@ -265,25 +261,26 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 
 // ------------------------------------------------------------- query pass
 //
-// Q and dO of the tile sit in TMEM as A operands; K and V blocks of 128 keys
-// stream through two rings (whose last stages are the tiles' own slots, free
-// once the tiles are in TMEM).  Both warpgroups work on the same block, each
-// on half of its columns.  Tensor order: S(j+1), dQ(j), dP(j+1): S(j+1) only
-// needs S(j) to have been read into registers, so dS(j) is computed under it
-// and P(j+1) under dQ(j) and dP(j+1).  dS is released in two halves, so that
-// dQ(j) starts on the first.  (Blocks of 64 keys in two S and two dP buffers,
-// the warpgroups alternating, left the tensor pipe half idle: an MMA of N =
-// 64 takes 32 clocks, less than the issue of the next.)
-constexpr int kBk = 128;  // keys per block
+// Q and dO of the tile sit in TMEM as A operands; K and V blocks of 96 keys
+// stream through two rings.  Both warpgroups work on the same block, each on
+// half of its columns, and dS has its own place in TMEM, so S(j+1) only needs
+// S(j) to have been read into registers, dP(j+1) the same of dP(j), and the
+// tensor pipe runs S(j+1), dP(j+1) while block j is exponentiated.  Tensor
+// order: S(j+1), dP(j+1), dQ(j).
+//
+// 96 keys: S, dP (fp32) and dS (bf16) take 240 columns beside dq, Q and dO.
+// Blocks of 128 with dS in dP's columns chain dS(j), dQ(j), dP(j+1) and left
+// the pipe 57% busy; blocks of 64 in two buffers, 52% (an MMA of N = 64 takes
+// 32 clocks, less than the issue of the next).
+constexpr int kBk = 96;  // keys per block
 
 template <int D>
 struct QLayout {
-  static constexpr uint32_t kAcc = 0, kS = D, kDp = D + kBk, kQ = D + 2 * kBk, kDo = kQ + D / 2;
+  static constexpr uint32_t kAcc = 0, kS = D, kDp = kS + kBk, kDs = kDp + kBk, kQ = kDs + kBk / 2, kDo = kQ + D / 2;
   static_assert(kDo + D / 2 <= kTmemAll, "TMEM columns");
   static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBk * D * 2;
-  static_assert(kTile == kBlock, "a block reuses a tile's slot");
-  static constexpr int kStages = 3;  // per ring, the tile's slot among them
-  static constexpr size_t kSmem = 1024 + 2 * kStages * kBlock;
+  static constexpr int kStages = 3;  // per ring
+  static constexpr size_t kSmem = 1024 + 2 * kTile + 2 * kStages * kBlock;
 };
 
 template <int D>
@@ -297,8 +294,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   __shared__ BarsB bars;
   __shared__ float red[4][128];  // partial sums: delta halves, then the keys' mean, then the rows' roundings
   __shared__ float centre[D];
-  const uint32_t k_s0 = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, q_s = k_s0 + (S - 1) * L::kBlock;
-  const uint32_t v_s0 = q_s + L::kTile, do_s = v_s0 + (S - 1) * L::kBlock;
+  const uint32_t q_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, do_s = q_s + L::kTile;
+  const uint32_t k_s0 = do_s + L::kTile, v_s0 = k_s0 + S * L::kBlock;
   FAS_BWD_PROLOGUE();
   const Blocks blk(p.table[f], kBk);
 
@@ -307,12 +304,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (warp == kWarpK) {
         const uint32_t tb = ptx::smem_addr(&bars.tile_full);
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
-        load_tile<D>(q_s, &tm_q, tb, sp.x + tile * kRowsB, h);
-        load_tile<D>(do_s, &tm_do, tb, sp.x + tile * kRowsB, h);
-        produce<D, kBk, false>(bars, 0, &tm_k, S, k_s0, q_s, h, blk, p, 0);
+        load_rows<D, kRowsB>(q_s, &tm_q, tb, sp.x + tile * kRowsB, h);
+        load_rows<D, kRowsB>(do_s, &tm_do, tb, sp.x + tile * kRowsB, h);
+        produce<D, kBk, false>(bars, 0, &tm_k, S, k_s0, h, blk, p, 0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, kBk, false>(bars, 1, &tm_v, S, v_s0, do_s, h, blk, p, 0);
+        produce<D, kBk, false>(bars, 1, &tm_v, S, v_s0, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -320,8 +317,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       auto wait = [&](uint64_t& b, int parity) {
         return ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitMma, p.limit_ns);
       };
-      // Stage st of either ring is at its base + st * block (the tile's slot
-      // follows the dedicated stages).
       const uint64_t kd = ptx::smem_desc_sw128(k_s0, 16, 1024), vd = ptx::smem_desc_sw128(v_s0, 16, 1024);
       const uint64_t kmn = ptx::smem_desc_sw128(k_s0, kBk * 128, 1024);
       constexpr uint64_t kStep = L::kBlock >> 4;
@@ -352,7 +347,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (ok) {
         tile_to_tmem<D>(tmem + L::kQ, ptx::smem_desc_sw128(q_s, 16, 1024));
         tile_to_tmem<D>(tmem + L::kDo, ptx::smem_desc_sw128(do_s, 16, 1024));
-        ptx::mma_commit(ptx::smem_addr(&bars.tile_free));
         ok = s_mma(n) && dp_mma(n);
       }
       for (int j = 0; ok && j < blk.nb; ++j) {
@@ -361,19 +355,17 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (more) {
           ok = wait(bars.s_free, j);
           ptx::tc_fence_after_sync();
-          ok = ok && s_mma(n1);
+          ok = ok && s_mma(n1) && wait(bars.dp_free, j);
+          ptx::tc_fence_after_sync();
+          ok = ok && dp_mma(n1);
         }
-        ok = ok && wait(bars.ds_full[0], j);
+        ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBk, 0>(tmem + L::kAcc, tmem + L::kDp, kmn + os * kStep, n, j == 0);
-        ok = wait(bars.ds_full[1], j);
-        if (!ok) break;
-        ptx::tc_fence_after_sync();
-        mma_acc<D, kBk, 1>(tmem + L::kAcc, tmem + L::kDp, kmn + os * kStep, n, false);
+        mma_acc<D, kBk, 8>(tmem + L::kAcc, tmem + L::kDs, kmn + os * kStep, n, j == 0);
+        ptx::mma_commit(ptx::smem_addr(&bars.acc_done));
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][os]));
         if (++os == S) os = 0;
-        if (more) ok = dp_mma(n1);
         n = n1;
       }
       ptx::mma_commit(ptx::smem_addr(&bars.acc_full));
@@ -393,6 +385,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                                              p.limit_ns);
       return (bool)__all_sync(0xffffffffu, got);
     };
+    const float lse = valid ? p.lse[(int64_t)h * p.N + token] : INFINITY;
     // delta: each group takes half of the row's columns.
     float delta = 0.f;
     if (valid) {
@@ -413,7 +406,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     ptx::named_barrier_sync(1, kSoftThreads);
     delta = red[0][trow] + red[1][trow];
     // A row past the frame's end gets P = 0 and is never stored.
-    const float lse = valid ? p.lse[(int64_t)h * p.N + token] : INFINITY;
     const float nl = -lse * kLog2eB;
     if (valid) {  // group 0: -lse / s, group 1: -delta, as the key pass's MMA takes them
       uint8_t* st = p.stats + ((int64_t)g * p.H * p.N + (int64_t)h * p.N + token) * kStatBytes;
@@ -448,10 +440,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       ptx::named_barrier_sync(1, kSoftThreads);
     }
     const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB), nl2 = ptx::f32x2(nl, nl);
+    const uint64_t minus1 = ptx::f32x2(-1.f, -1.f);
     const float nd = -delta;
     float e0 = 0.f, e1 = 0.f;  // what rounding dS to bf16 added to the row
-    constexpr int kCh = kBk / 32, kFirst = (kCh + 1) / 2;  // chunks of 16 columns per group
+    constexpr int kCh = kBk / 32;  // chunks of 16 columns per group
     const uint32_t sbase = tmem + lane_base + L::kS + g * (kBk / 2), dbase = tmem + lane_base + L::kDp + g * (kBk / 2);
+    const uint32_t dst = tmem + lane_base + L::kDs + g * (kBk / 4);
     for (int j = 0; ok && j < blk.nb; ++j) {
       const int nch = blk.count(j) / 16 - g * kCh;  // this half's chunks that hold keys
       ok = wait(bars.s_full, j);
@@ -475,6 +469,13 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (!ok) break;
       ptx::tc_fence_after_sync();
       core::load_chunks<0, kCh>(dbase, r);
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(ptx::smem_addr(&bars.dp_free));
+      if (j > 0) {  // dS(j-1) has been read (long ago, as a rule)
+        ok = wait(bars.acc_done, j - 1);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+      }
       uint32_t pk[kCh][8];
 #pragma unroll
       for (int u = 0; u < kCh; ++u) {
@@ -485,13 +486,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           mul_f32x2(pr[u][2 * e], pr[u][2 * e + 1], x0, x1, pr[u][2 * e], pr[u][2 * e + 1]);  // dS
           pk[u][e] = ptx::pack_bf16x2(pr[u][2 * e], pr[u][2 * e + 1]);
         }
-        ptx::tmem_st8(dbase + u * 16, pk[u]);
-        if (u == kFirst - 1 || u == kCh - 1) {
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before_sync();
-          ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[u == kCh - 1]));
-        }
+        ptx::tmem_st8(dst + u * 8, pk[u]);
       }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full));
       // Off the tensor pipe's path: what the roundings add up to.  Columns
       // past the range's end hold leftovers and do not count.
 #pragma unroll
@@ -499,8 +498,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float w0 = __uint_as_float(pk[u][e] << 16), w1 = __uint_as_float(pk[u][e] & 0xFFFF0000u);
-          ptx::add_f32x2(w0, w1, -pr[u][2 * e], -pr[u][2 * e + 1]);
+          float w0, w1;
+          ptx::fma_f32x2(w0, w1, pr[u][2 * e], pr[u][2 * e + 1], minus1, ptx::f32x2(__uint_as_float(pk[u][e] << 16), __uint_as_float(pk[u][e] & 0xFFFF0000u)));
           ptx::add_f32x2(a0, a1, w0, w1);
         }
         e0 += u < nch ? a0 : 0.f;
@@ -595,12 +594,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (warp == kWarpK) {
         const uint32_t tb = ptx::smem_addr(&bars.tile_full);
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
-        load_tile<D>(k_s, &tm_k, tb, sp.x + tile * kRowsB, h);
-        load_tile<D>(v_s, &tm_v, tb, sp.x + tile * kRowsB, h);
-        produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, 0, h, blk, p, stat_s0);
+        load_rows<D, kRowsB>(k_s, &tm_k, tb, sp.x + tile * kRowsB, h);
+        load_rows<D, kRowsB>(v_s, &tm_v, tb, sp.x + tile * kRowsB, h);
+        produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, BQ, false>(bars, 1, &tm_do, L::kStages, do_s0, 0, h, blk, p, 0);
+        produce<D, BQ, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -648,15 +647,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = wait(bars.p_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 2>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        mma_acc<D, BQ, 16>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
         next(qs, qph);
         next(ds, dph);
         if (more) ok = s_mma(n1);
-        ok = ok && wait(bars.ds_full[0], j);
+        ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
+        mma_acc<D, BQ, 16>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][st]));
         if (more) ok = dp_mma(n1);
         n = n1;
@@ -720,7 +719,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before_sync();
-      ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full[0]));
+      ptx::mbar_arrive(ptx::smem_addr(&bars.ds_full));
     }
     ok = ok && wait(bars.acc_full, 0);
     if (ok && !bars.abort) {
@@ -767,11 +766,11 @@ struct KConfig<64> {
   static constexpr bool kKT = true, kVT = true;
 };
 
-// Tensor map {d, N, H} with boxes of `rows` tokens.
-int token_map(CUtensorMap* m, const void* base, int d, int rows, const BwdParams& p) {
+// Tensor map {d, N, H} with boxes of kBox tokens.
+int token_map(CUtensorMap* m, const void* base, int d, const BwdParams& p) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.N, (cuuint64_t)p.H};
   const cuuint64_t strides[2] = {(cuuint64_t)p.row_stride * 2, (cuuint64_t)p.head_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kBox, 1};
   return bf16_tensor_map(m, base, 3, dims, strides, box);
 }
 
@@ -780,15 +779,9 @@ int launch(const BwdParams& p, int grid, cudaStream_t st) {
   using C = KConfig<D>;
   using LQ = QLayout<D>;
   using LK = KLayout<D, C::kB, C::kKT, C::kVT>;
-  static_assert(kBk == kRowsB, "tiles and the query pass's blocks share tensor maps");
-  CUtensorMap tq, tdo, tk, tv, bq, bdo;
-  if (token_map(&tq, p.q, D, kRowsB, p) != FAS_OK || token_map(&tdo, p.dout, D, kRowsB, p) != FAS_OK ||
-      token_map(&tk, p.k, D, kRowsB, p) != FAS_OK || token_map(&tv, p.v, D, kRowsB, p) != FAS_OK)
-    return -1;
-  bq = tq;
-  bdo = tdo;
-  if (C::kB != kRowsB &&
-      (token_map(&bq, p.q, D, C::kB, p) != FAS_OK || token_map(&bdo, p.dout, D, C::kB, p) != FAS_OK))
+  CUtensorMap tq, tdo, tk, tv;
+  if (token_map(&tq, p.q, D, p) != FAS_OK || token_map(&tdo, p.dout, D, p) != FAS_OK ||
+      token_map(&tk, p.k, D, p) != FAS_OK || token_map(&tv, p.v, D, p) != FAS_OK)
     return -1;
   auto kq = attention_bwd_q<D>;
   auto kk = attention_bwd_k<D, C::kB, C::kKT, C::kVT>;
@@ -797,7 +790,7 @@ int launch(const BwdParams& p, int grid, cudaStream_t st) {
     return -1;
   kq<<<grid, kThreadsB, LQ::kSmem, st>>>(tq, tdo, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  kk<<<grid, kThreadsB, LK::kSmem, st>>>(tk, tv, bq, bdo, p);
+  kk<<<grid, kThreadsB, LK::kSmem, st>>>(tk, tv, tq, tdo, p);
   return cudaGetLastError() == cudaSuccess ? 2 : -1;
 }
 
