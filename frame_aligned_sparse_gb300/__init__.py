@@ -149,10 +149,8 @@ def _check(call: str, rc: int) -> None:
 
 
 def _stream_handle(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        # The raw handle: building the Stream object costs more than a launch.
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_device_stream()[1]
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -405,13 +403,34 @@ def _prologue(x, w_folded, cos, sin, heads, head_dim, layout, groups, ranks, q, 
     return (*outs, key_sums)
 
 
-def _check_device(*tensors):
-    """All tensors on the current device (the kernels launch there)."""
+def _check_here(name, t, shape, dtype, device: int) -> int:
+    """_check_tensor, and that the tensor is on the current device (the
+    kernels launch there).  Returns its address."""
     import torch
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        _check_tensor(name, t, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def _current(name, t) -> Tuple[int, int]:
+    """The current device and its current stream's handle, for a call on t."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _current_device_stream()
+
+
+def _current_device_stream() -> Tuple[int, int]:
+    import torch
+    device = torch.cuda.current_device()
+    # The raw handle: building the Stream object costs more than a launch.
+    return device, torch._C._cuda_getCurrentRawStream(device)
+
+
+def _on(stream, current: int) -> int:
+    return current if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _own_until_run(stream, *temps):
@@ -432,24 +451,20 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
     out, lse as fas_forward took and returned them, dout the gradient of out
     (bf16, the plan's layout).  Returns (dq, dk, dv)."""
     import torch
-    shape = _qkv_shape()
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)):
-        _check_tensor(name, t, shape, torch.bfloat16)
-    _check_tensor("lse", lse, _lse_shape(), torch.float32)
-    grads = []
-    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        _check_tensor(name, t, shape, torch.bfloat16)
-        grads.append(t)
-    _check_device(q, k, v, out, lse, dout, *grads)
-    workspace = torch.empty((32, *_lse_shape()), dtype=torch.uint8, device=q.device)  # FAS_BACKWARD_WORKSPACE
-    rc = load().fas_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                             dout.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
-                             workspace.data_ptr(), _stream_handle(stream))
+    shape, lse_shape, bf16 = _qkv_shape(), _lse_shape(), torch.bfloat16
+    device, current = _current("q", q)
+    ptrs = [_check_here("q", q, shape, bf16, device), _check_here("k", k, shape, bf16, device),
+            _check_here("v", v, shape, bf16, device), _check_here("out", out, shape, bf16, device),
+            _check_here("lse", lse, lse_shape, torch.float32, device),
+            _check_here("dout", dout, shape, bf16, device)]
+    dq, dk, dv = (torch.empty_like(q) if t is None else t for t in (dq, dk, dv))
+    ptrs += [_check_here("dq", dq, shape, bf16, device), _check_here("dk", dk, shape, bf16, device),
+             _check_here("dv", dv, shape, bf16, device)]
+    workspace = torch.empty((32, *lse_shape), dtype=torch.uint8, device=q.device)  # FAS_BACKWARD_WORKSPACE
+    rc = load().fas_backward(*ptrs, workspace.data_ptr(), _on(stream, current))
     _check("fas_backward", rc)
-    _own_until_run(stream, workspace, *grads)
-    return tuple(grads)
+    _own_until_run(stream, workspace, dq, dk, dv)
+    return dq, dk, dv
 
 
 class Checkpoint(NamedTuple):
@@ -477,7 +492,8 @@ def _checkpoint_empty(shape, device):
                       torch.empty((*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), dtype=torch.uint8, device=device))
 
 
-def _check_checkpoint(name, c, shape=None):
+def _check_checkpoint(name, c, device: int, shape=None):
+    """The checkpoint and the addresses of its codes and scales."""
     import torch
     if not isinstance(c, tuple) or len(c) != 2:
         raise TypeError(f"{name} must be a Checkpoint (codes, scales)")
@@ -485,21 +501,20 @@ def _check_checkpoint(name, c, shape=None):
     shape = tuple(c.codes.shape) if shape is None else tuple(shape)
     if not shape or shape[-1] % CHECKPOINT_BLOCK:
         raise ValueError(f"{name}: the last axis must be a multiple of {CHECKPOINT_BLOCK}, got {shape}")
-    _check_tensor(f"{name}.codes", c.codes, shape, torch.float8_e4m3fn)
-    _check_tensor(f"{name}.scales", c.scales, (*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), torch.uint8)
-    return c
+    return c, [_check_here(f"{name}.codes", c.codes, shape, torch.float8_e4m3fn, device),
+               _check_here(f"{name}.scales", c.scales, (*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), torch.uint8,
+                           device)]
 
 
 def fas_checkpoint_pack(x, out: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
     """Holds x (bf16 or fp32, contiguous, last axis a multiple of 32) in 8
     bits: see ``fas_checkpoint_pack`` in fas.h."""
     dtype = _dtype_code("x", x)
-    _check_tensor("x", x, x.shape, x.dtype)
-    c = _checkpoint_empty(tuple(x.shape), x.device) if out is None else _check_checkpoint("out", out, x.shape)
-    _check_device(x, *c)
-    _check("fas_checkpoint_pack",
-           load().fas_checkpoint_pack(x.data_ptr(), dtype, c.codes.data_ptr(), c.scales.data_ptr(), x.numel(),
-                                      _stream_handle(stream)))
+    device, current = _current("x", x)
+    ptr = _check_here("x", x, x.shape, x.dtype, device)
+    c = _checkpoint_empty(tuple(x.shape), x.device) if out is None else out
+    c, ptrs = _check_checkpoint("out", c, device, x.shape)
+    _check("fas_checkpoint_pack", load().fas_checkpoint_pack(ptr, dtype, *ptrs, x.numel(), _on(stream, current)))
     _own_until_run(stream, *c)
     return c
 
@@ -507,39 +522,41 @@ def fas_checkpoint_pack(x, out: Optional[Checkpoint] = None, stream=None) -> Che
 def fas_checkpoint_unpack(c: Checkpoint, dtype=None, out=None, stream=None):
     """The tensor a checkpoint stands for, as bf16 (the default) or fp32."""
     import torch
-    c = _check_checkpoint("c", c)
+    if not isinstance(c, tuple) or len(c) != 2:
+        raise TypeError("c must be a Checkpoint (codes, scales)")
+    device, current = _current("c.codes", c[0])
+    c, ptrs = _check_checkpoint("c", c, device)
+    shape = c.codes.shape
     if out is None:
-        out = torch.empty(c.codes.shape, dtype=dtype or torch.bfloat16, device=c.codes.device)
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=c.codes.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out must be {dtype}, got {out.dtype}")
     code = _dtype_code("out", out)
-    _check_tensor("out", out, c.codes.shape, out.dtype)
-    _check_device(out, *c)
+    ptr = _check_here("out", out, shape, out.dtype, device)
     _check("fas_checkpoint_unpack",
-           load().fas_checkpoint_unpack(c.codes.data_ptr(), c.scales.data_ptr(), out.data_ptr(), code, out.numel(),
-                                        _stream_handle(stream)))
+           load().fas_checkpoint_unpack(*ptrs, ptr, code, out.numel(), _on(stream, current)))
     _own_until_run(stream, out)
     return out
 
 
-def _norm_frames(tokens: int, width: int, gate, frame_tokens):
-    """(gate pointer, host spans or None, number of frames)."""
+def _norm_frames(tokens: int, width: int, gate, frame_tokens, device: int):
+    """(gate's address, host spans or None, number of frames)."""
     import torch
     if gate is None:
         return None, None, 1
     if gate.ndim != 2:
         raise ValueError(f"gate must be [frames, width], got {tuple(gate.shape)}")
     n = gate.shape[0]
-    _check_tensor("gate", gate, (n, width), torch.float32)
+    ptr = _check_here("gate", gate, (n, width), torch.float32, device)
     if frame_tokens is None or isinstance(frame_tokens, int) or np.ndim(frame_tokens) == 0:
         span = tokens // n if frame_tokens is None and n else frame_tokens
         if n * int(span or 0) != tokens:
             raise ValueError(f"gate has {n} frames of {span} tokens; x has {tokens} tokens")
-        return gate.data_ptr(), None, n
+        return ptr, None, n
     spans = np.ascontiguousarray(frame_tokens, dtype=np.int32)
     if spans.ndim != 1 or len(spans) != n or int(spans.sum(dtype=np.int64)) != tokens:
         raise ValueError(f"frame_tokens must hold {n} spans (one per row of gate) that add up to {tokens} tokens")
-    return gate.data_ptr(), spans, n
+    return ptr, spans, n
 
 
 @functools.lru_cache(maxsize=256)
@@ -549,14 +566,6 @@ def _norm_workspace(tokens: int, width: int, spans: Optional[bytes], frames: int
     _check("fas_residual_norm_backward",
            load().fas_residual_norm_backward_workspace(tokens, width, spans, frames, ctypes.byref(need)))
     return need.value
-
-
-def _empty_or(name, t, shape, dtype, device):
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check_tensor(name, t, shape, dtype)
-    return t
 
 
 def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None, alpha: float = 1.0,
@@ -573,23 +582,24 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
     residual = _dtype_code("x", x)
     if x.ndim != 2:
         raise ValueError(f"x must be [tokens, width], got {tuple(x.shape)}")
-    N, C = x.shape
-    _check_tensor("x", x, (N, C), x.dtype)
-    _check_tensor("y", y, (N, C), torch.bfloat16)
-    _check_tensor("gamma_post", gamma_post, (C,), torch.float32)
-    _check_tensor("gamma_pre", gamma_pre, (C,), torch.float32)
-    gate_ptr, spans, frames = _norm_frames(N, C, gate, frame_tokens)
-    x_out = _empty_or("x_out", x_out, (N, C), x.dtype, x.device)
-    h = _empty_or("h", h, (N, C), torch.bfloat16, x.device)
-    rstd = torch.empty((2, N), dtype=torch.float32, device=x.device)
+    shape = N, C = x.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    device, current = _current("x", x)
+    py, px = _check_here("y", y, shape, bf16, device), _check_here("x", x, shape, x.dtype, device)
+    ppost = _check_here("gamma_post", gamma_post, (C,), f32, device)
+    ppre = _check_here("gamma_pre", gamma_pre, (C,), f32, device)
+    pgate, spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
+    if x_out is None:
+        x_out = torch.empty_like(x)
+    if h is None:
+        h = torch.empty_like(y)
+    px_out, ph = _check_here("x_out", x_out, shape, x.dtype, device), _check_here("h", h, shape, bf16, device)
+    rstd = torch.empty((2, N), dtype=f32, device=x.device)
     held = (_checkpoint_empty((N, C), x.device), _checkpoint_empty((N, C), x.device)) if checkpoint else ()
     parts = [t for c in held for t in c]
-    _check_device(y, x, gamma_post, gamma_pre, gate, x_out, h)
-    rc = load().fas_residual_norm(y.data_ptr(), x.data_ptr(), residual, gate_ptr, gamma_post.data_ptr(),
-                                  gamma_pre.data_ptr(), float(alpha), float(eps), N, C,
-                                  None if spans is None else spans.ctypes.data, frames, x_out.data_ptr(),
-                                  h.data_ptr(), rstd.data_ptr(), *([t.data_ptr() for t in parts] or [None] * 4),
-                                  _stream_handle(stream))
+    rc = load().fas_residual_norm(py, px, residual, pgate, ppost, ppre, alpha, eps, N, C,
+                                  None if spans is None else spans.ctypes.data, frames, px_out, ph, rstd.data_ptr(),
+                                  *([t.data_ptr() for t in parts] or (None,) * 4), _on(stream, current))
     _check("fas_residual_norm", rc)
     _own_until_run(stream, x_out, h, rstd, *parts)
     return (x_out, h, rstd, *held)
@@ -606,39 +616,37 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
     residual = _dtype_code("dx_out", dx_out)
     if dx_out.ndim != 2:
         raise ValueError(f"dx_out must be [tokens, width], got {tuple(dx_out.shape)}")
-    N, C = dx_out.shape
-    _check_tensor("dx_out", dx_out, (N, C), dx_out.dtype)
-    _check_tensor("dh", dh, (N, C), torch.bfloat16)
+    shape = N, C = dx_out.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    device, current = _current("dx_out", dx_out)
+    args = [_check_here("dx_out", dx_out, shape, dx_out.dtype, device), _check_here("dh", dh, shape, bf16, device)]
     if isinstance(y, torch.Tensor) != isinstance(x_out, torch.Tensor):
         raise TypeError("y and x_out must both be tensors or both be Checkpoints")
     if isinstance(y, torch.Tensor):
-        _check_tensor("y", y, (N, C), torch.bfloat16)
-        _check_tensor("x_out", x_out, (N, C), dx_out.dtype)
-        saved = [y, x_out]
-        ptrs = [y.data_ptr(), x_out.data_ptr(), residual] + [None] * 4
+        args += [_check_here("y", y, shape, bf16, device), _check_here("x_out", x_out, shape, dx_out.dtype, device),
+                 residual, None, None, None, None]
     else:
-        saved = [*_check_checkpoint("y", y, (N, C)), *_check_checkpoint("x_out", x_out, (N, C))]
-        ptrs = [None, None, residual] + [t.data_ptr() for t in saved]
-    _check_tensor("rstd", rstd, (2, N), torch.float32)
-    _check_tensor("gamma_post", gamma_post, (C,), torch.float32)
-    _check_tensor("gamma_pre", gamma_pre, (C,), torch.float32)
-    gate_ptr, spans, frames = _norm_frames(N, C, gate, frame_tokens)
-    dx = _empty_or("dx", dx, (N, C), dx_out.dtype, dx_out.device)
-    dy = _empty_or("dy", dy, (N, C), torch.bfloat16, dx_out.device)
-    _check_device(dx_out, dh, *saved, rstd, gamma_post, gamma_pre, gate, dx, dy)
-    lib = load()
-    spans_ptr = None if spans is None else spans.ctypes.data
-    need = _norm_workspace(N, C, None if spans is None else spans.tobytes(), frames, dx_out.get_device())
+        args += [None, None, residual, *_check_checkpoint("y", y, device, shape)[1],
+                 *_check_checkpoint("x_out", x_out, device, shape)[1]]
+    args += [_check_here("rstd", rstd, (2, N), f32, device), None,
+             _check_here("gamma_post", gamma_post, (C,), f32, device),
+             _check_here("gamma_pre", gamma_pre, (C,), f32, device)]
+    args[-3], spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
+    if dx is None:
+        dx = torch.empty_like(dx_out)
+    if dy is None:
+        dy = torch.empty_like(dh)
+    need = _norm_workspace(N, C, None if spans is None else spans.tobytes(), frames, device)
     workspace = torch.empty(need, dtype=torch.uint8, device=dx_out.device)
-    dpost, dpre = torch.empty((2, C), dtype=torch.float32, device=dx_out.device).unbind()  # C is a multiple of 8
+    dpost, dpre = torch.empty_like(gamma_post), torch.empty_like(gamma_pre)
     dgate = None if gate is None else torch.empty_like(gate)
-    rc = lib.fas_residual_norm_backward(
-        dx_out.data_ptr(), dh.data_ptr(), *ptrs, rstd.data_ptr(), gate_ptr, gamma_post.data_ptr(),
-        gamma_pre.data_ptr(), float(alpha), N, C, spans_ptr, frames, dx.data_ptr(), dy.data_ptr(),
-        None if dgate is None else dgate.data_ptr(), dpost.data_ptr(), dpre.data_ptr(),
-        workspace.data_ptr(), need, _stream_handle(stream))
+    rc = load().fas_residual_norm_backward(
+        *args, alpha, N, C, None if spans is None else spans.ctypes.data, frames,
+        _check_here("dx", dx, shape, dx_out.dtype, device), _check_here("dy", dy, shape, bf16, device),
+        None if dgate is None else dgate.data_ptr(), dpost.data_ptr(), dpre.data_ptr(), workspace.data_ptr(), need,
+        _on(stream, current))
     _check("fas_residual_norm_backward", rc)
-    _own_until_run(stream, workspace, dpost, dx, dy, *([] if dgate is None else [dgate]))
+    _own_until_run(stream, workspace, dpost, dpre, dx, dy, *([] if dgate is None else [dgate]))
     return dx, dy, dpost, dpre, dgate
 
 

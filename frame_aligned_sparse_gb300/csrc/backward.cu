@@ -25,7 +25,7 @@
 // dS_ij = 0 up to out's rounding, a common component c of the keys cancels in
 // dq, but the roundings of dS times c do not: the query pass sums what
 // rounding added to each row and takes it out along c (the mean of the first
-// block's keys), which leaves the roundings times k - c.  (Keys with a common
+// 64 keys), which leaves the roundings times k - c.  (Keys with a common
 // component three times their spread, as the prepass's mean-centring is for,
 // tripled dq's error without it.)
 
@@ -46,9 +46,14 @@ namespace {
 using core::drain_wait;
 
 constexpr int kRowsB = kQTile;  // rows of a work item (MMA M)
-constexpr int kSoftThreads = 256;
-constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10;
-constexpr int kThreadsB = 32 * 11;
+// Softmax warpgroups: all work on the same block, each on a third of its
+// columns.  (Two, each on a half, run their exponentials in lockstep and leave
+// the special-function unit idle under everything else: the mid geometry's
+// query pass took 698 us instead of 652, the key pass 788 instead of 773.)
+constexpr int kSoftGroups = 3;
+constexpr int kSoftThreads = 128 * kSoftGroups;
+constexpr int kWarpK = 4 * kSoftGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2, kWarpMean = kWarpK + 3;
+constexpr int kThreadsB = 32 * (kWarpMean + 1);
 constexpr int kMaxStagesB = 6;
 constexpr uint32_t kTmemAll = 512;
 constexpr float kLog2eB = 1.4426950408889634f;
@@ -74,7 +79,7 @@ struct BarsB {
   uint64_t empty[2][kMaxStagesB];
   uint64_t s_full, dp_full;
   uint64_t s_free, dp_free;        // query pass: S, dP read into registers
-  uint64_t p_full, ds_full;        // P, dS stored as bf16
+  uint64_t p_full[2], ds_full;     // P (in two parts) and dS stored as bf16
   uint64_t acc_done;               // query pass: dQ(j) has read dS(j)
   uint64_t acc_full, drain;
   uint32_t tmem_base;
@@ -94,7 +99,8 @@ __device__ __forceinline__ void init_bars(BarsB& b) {
   one(b.dp_full, 1);
   one(b.s_free, kSoftThreads);
   one(b.dp_free, kSoftThreads);
-  one(b.p_full, kSoftThreads);
+  one(b.p_full[0], kSoftThreads);
+  one(b.p_full[1], kSoftThreads);
   one(b.ds_full, kSoftThreads);
   one(b.acc_done, 1);
   one(b.acc_full, 1);
@@ -202,12 +208,16 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_tmem, uint64_t a
 
 // D[128 x D] += A[128 x n] . B[n x D]: A's bf16 chunks of 16 columns in TMEM,
 // kStride columns apart (8 each), B a block read along its rows.
-template <int D, int kB, int kStride>
+// kPart 0, 1: the first or the last chunks of each warpgroup's share of the
+// block (released in that order); 2: all.
+template <int kB>
+constexpr int kFirstChunks = (kB / 16 / kSoftGroups + 1) / 2;
+template <int D, int kB, int kStride, int kPart>
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t b_desc, int n, bool first) {
   constexpr uint32_t idesc = ptx::idesc_bf16_f32(kRowsB, D, true);
 #pragma unroll
   for (int kk = 0; kk < kB / 16; ++kk)
-    if (n == kB || kk * 16 < n)
+    if ((kPart == 2 || (kk % (kB / 16 / kSoftGroups) < kFirstChunks<kB>) == (kPart == 0)) && (n == kB || kk * 16 < n))
       ptx::mma_ts(d, a + kk * kStride, b_desc + ((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
 }
 
@@ -219,23 +229,18 @@ __device__ __forceinline__ void tile_to_tmem(uint32_t col, uint64_t desc) {
     ptx::tmem_cp_128x256b(col + kk * 8, desc + (((kk >> 2) * (kRowsB * 128) + (kk & 3) * 32) >> 4));
 }
 
-// Writes 16 * N columns of an fp32 accumulator row, scaled, as bf16.
-template <int N>
+// Writes 16 columns of an fp32 accumulator row, scaled, as bf16.
 __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float scale, bool valid) {
+  uint32_t o[16], pk[8];
+  ptx::tmem_ld16(taddr, o);
+  ptx::tmem_ld_wait(o);
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    uint32_t o[16];
-    ptx::tmem_ld16(taddr + u * 16, o);
-    ptx::tmem_ld_wait(o);
-    uint32_t pk[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      pk[e] = ptx::pack_bf16x2(__uint_as_float(o[2 * e]) * scale, __uint_as_float(o[2 * e + 1]) * scale);
-    if (valid) {
-      uint4* d4 = reinterpret_cast<uint4*>(dst + u * 16);
-      d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-    }
+  for (int e = 0; e < 8; ++e)
+    pk[e] = ptx::pack_bf16x2(__uint_as_float(o[2 * e]) * scale, __uint_as_float(o[2 * e + 1]) * scale);
+  if (valid) {
+    uint4* d4 = reinterpret_cast<uint4*>(dst);
+    d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
   }
 }
 
@@ -262,8 +267,8 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 // ------------------------------------------------------------- query pass
 //
 // Q and dO of the tile sit in TMEM as A operands; K and V blocks of 96 keys
-// stream through two rings.  Both warpgroups work on the same block, each on
-// half of its columns, and dS has its own place in TMEM, so S(j+1) only needs
+// stream through two rings.  The warpgroups work on the same block, and
+// dS has its own place in TMEM, so S(j+1) only needs
 // S(j) to have been read into registers, dP(j+1) the same of dP(j), and the
 // tensor pipe runs S(j+1), dP(j+1) while block j is exponentiated.  Tensor
 // order: S(j+1), dP(j+1), dQ(j).
@@ -292,8 +297,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   constexpr int S = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ BarsB bars;
-  __shared__ float red[4][128];  // partial sums: delta halves, then the keys' mean, then the rows' roundings
-  __shared__ float centre[D];
+  __shared__ float red[kSoftGroups][kRowsB];  // delta, then what rounding added to the rows by group
+  __shared__ __align__(16) float centre[D];
   const uint32_t q_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, do_s = q_s + L::kTile;
   const uint32_t k_s0 = do_s + L::kTile, v_s0 = k_s0 + S * L::kBlock;
   FAS_BWD_PROLOGUE();
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBk, 8>(tmem + L::kAcc, tmem + L::kDs, kmn + os * kStep, n, j == 0);
+        mma_acc<D, kBk, 8, 2>(tmem + L::kAcc, tmem + L::kDs, kmn + os * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.acc_done));
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][os]));
         if (++os == S) os = 0;
@@ -374,8 +379,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (!ok) bars.abort = 1;
     }
     __syncwarp();
+  } else if (warp == kWarpMean) {
+    // The mean of the first keys the rows see (64 at most): the lane's D / 32
+    // columns.  Needed by the epilogue alone.
+    constexpr int E = D / 32;
+    const int n = min(blk.r.y, 64);
+    const uint16_t* src = p.k + (int64_t)h * p.head_stride + (int64_t)blk.r.x * p.row_stride + lane * E;
+    float c[E] = {};
+#pragma unroll 16
+    for (int r = 0; r < n; ++r)  // n is a multiple of 16
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(src + r * p.row_stride)[e];
+        c[2 * e] += __uint_as_float(w << 16);
+        c[2 * e + 1] += __uint_as_float(w & 0xFFFF0000u);
+      }
+#pragma unroll
+    for (int e = 0; e < E; ++e) centre[lane * E + e] = c[e] / (float)n;
+    ptx::named_barrier_arrive(2, kSoftThreads + 32);
   } else {
-    const int g = warp / 4, trow = (warp % 4) * 32 + lane, tid = threadIdx.x;
+    const int g = warp / 4, trow = (warp % 4) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const int row = tile * kRowsB + trow;
     const bool valid = row < sp.y;
@@ -386,68 +409,54 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       return (bool)__all_sync(0xffffffffu, got);
     };
     const float lse = valid ? p.lse[(int64_t)h * p.N + token] : INFINITY;
-    // delta: each group takes half of the row's columns.
-    float delta = 0.f;
-    if (valid) {
-      const uint4* o4 = reinterpret_cast<const uint4*>(p.out + at + g * (D / 2));
-      const uint4* d4 = reinterpret_cast<const uint4*>(p.dout + at + g * (D / 2));
+    // delta: D / 8 lanes read a row of out and of dout, each of 8 warps 16 rows.
+    if (warp < 8) {
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+      const int sub = lane / kLanes, c = lane % kLanes;
+      uint4 a[16 / kPer], b[16 / kPer];
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 a = o4[c], b = d4[c];
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          delta = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(bw[e] << 16), delta);
-          delta = fmaf(__uint_as_float(aw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), delta);
+      for (int i = 0; i < 16 / kPer; ++i) {
+        const int r = tile * kRowsB + warp * 16 + i * kPer + sub;
+        a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < sp.y) {
+          const int64_t o = (int64_t)h * p.head_stride + ((int64_t)sp.x + r) * p.row_stride + c * 8;
+          a[i] = *reinterpret_cast<const uint4*>(p.out + o);
+          b[i] = *reinterpret_cast<const uint4*>(p.dout + o);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 16 / kPer; ++i) {
+        const uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        float d = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          d = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(bw[e] << 16), d);
+          d = fmaf(__uint_as_float(aw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), d);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (c == 0) red[0][warp * 16 + i * kPer + sub] = d;
+      }
     }
-    red[g][trow] = delta;
     ptx::named_barrier_sync(1, kSoftThreads);
-    delta = red[0][trow] + red[1][trow];
+    const float delta = red[0][trow];
     // A row past the frame's end gets P = 0 and is never stored.
     const float nl = -lse * kLog2eB;
-    if (valid) {  // group 0: -lse / s, group 1: -delta, as the key pass's MMA takes them
+    if (valid && g < 2) {  // group 0: -lse / s, group 1: -delta, as the key pass's MMA takes them
       uint8_t* st = p.stats + ((int64_t)g * p.H * p.N + (int64_t)h * p.N + token) * kStatBytes;
       *reinterpret_cast<uint4*>(st) = split3(g == 0 ? -lse / p.scale : -delta);
     }
-    ptx::named_barrier_sync(1, kSoftThreads);
-    // The mean of the first block's keys (64 of them at most), from its
-    // shared-memory stage (the 128-byte swizzle permutes the 16-byte pieces
-    // of a row by row % 8).
-    bool ok = wait(bars.full[0][0], 0);
-    {
-      constexpr int kParts = kSoftThreads / (D / 2);
-      const int cp = tid % (D / 2), part = tid / (D / 2), n = min(blk.count(0), 64);
-      float c0 = 0.f, c1 = 0.f;
-      if (ok)
-        for (int r = part; r < n; r += kParts) {
-          const uint32_t off = (cp / 32) * (kBk * 128) + r * 128 + ((((cp % 32) / 4) ^ (r & 7)) * 16) + (cp % 4) * 4;
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(smem_raw + (k_s0 - ptx::smem_addr(smem_raw)) + off);
-          c0 += __uint_as_float(w << 16);
-          c1 += __uint_as_float(w & 0xFFFF0000u);
-        }
-      red[0][part * D + 2 * cp] = c0;
-      red[0][part * D + 2 * cp + 1] = c1;
-      ptx::consume(c0, c1);
-      ptx::fence_proxy_async_smem();
-      ptx::named_barrier_sync(1, kSoftThreads);
-      if (tid < D) {
-        float c = 0.f;
-        for (int i = 0; i < kParts; ++i) c += red[0][i * D + tid];
-        centre[tid] = c / (float)n;
-      }
-      ptx::named_barrier_sync(1, kSoftThreads);
-    }
+    ptx::named_barrier_sync(1, kSoftThreads);  // red is written again
+    bool ok = true;
     const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB), nl2 = ptx::f32x2(nl, nl);
-    const uint64_t minus1 = ptx::f32x2(-1.f, -1.f);
     const float nd = -delta;
+    const uint64_t minus1 = ptx::f32x2(-1.f, -1.f);
     float e0 = 0.f, e1 = 0.f;  // what rounding dS to bf16 added to the row
-    constexpr int kCh = kBk / 32;  // chunks of 16 columns per group
-    const uint32_t sbase = tmem + lane_base + L::kS + g * (kBk / 2), dbase = tmem + lane_base + L::kDp + g * (kBk / 2);
-    const uint32_t dst = tmem + lane_base + L::kDs + g * (kBk / 4);
+    constexpr int kCh = kBk / 16 / kSoftGroups;  // chunks of 16 columns per group
+    const uint32_t sbase = tmem + lane_base + L::kS + g * kCh * 16, dbase = tmem + lane_base + L::kDp + g * kCh * 16;
+    const uint32_t dst = tmem + lane_base + L::kDs + g * kCh * 8;
     for (int j = 0; ok && j < blk.nb; ++j) {
-      const int nch = blk.count(j) / 16 - g * kCh;  // this half's chunks that hold keys
+      const int nch = blk.count(j) / 16 - g * kCh;  // this group's chunks that hold keys
       ok = wait(bars.s_full, j);
       if (!ok) break;
       ptx::tc_fence_after_sync();
@@ -499,7 +508,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float w0, w1;
-          ptx::fma_f32x2(w0, w1, pr[u][2 * e], pr[u][2 * e + 1], minus1, ptx::f32x2(__uint_as_float(pk[u][e] << 16), __uint_as_float(pk[u][e] & 0xFFFF0000u)));
+          ptx::fma_f32x2(w0, w1, pr[u][2 * e], pr[u][2 * e + 1], minus1,
+                         ptx::f32x2(__uint_as_float(pk[u][e] << 16), __uint_as_float(pk[u][e] & 0xFFFF0000u)));
           ptx::add_f32x2(a0, a1, w0, w1);
         }
         e0 += u < nch ? a0 : 0.f;
@@ -508,14 +518,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
     red[g][trow] = e0 + e1;
     ok = ok && wait(bars.acc_full, 0);
-    ptx::named_barrier_sync(1, kSoftThreads);
+    ptx::named_barrier_sync(2, kSoftThreads + 32);  // and the mean
     if (ok && !bars.abort) {
       ptx::tc_fence_after_sync();
-      const float extra = red[0][trow] + red[1][trow];
-      constexpr int kOut = D / 32;  // chunks of 16 columns per group
+      float extra = 0.f;
 #pragma unroll
-      for (int u = 0; u < kOut; ++u) {
-        const int c0 = (g * kOut + u) * 16;
+      for (int i = 0; i < kSoftGroups; ++i) extra += red[i][trow];
+#pragma unroll 1
+      for (int c0 = g * 16; c0 < D; c0 += kSoftGroups * 16) {
         uint32_t o[16], w[8];
         ptx::tmem_ld16(tmem + lane_base + L::kAcc + c0, o);
         ptx::tmem_ld_wait(o);
@@ -545,8 +555,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // V.dO^T with the tile's K and V as A operands and blocks of Q and dO as B;
 // P^T and dS^T then are the A operands of dv += P^T.dO and dk += dS^T.Q, whose
 // B operands are the same Q and dO blocks read along their rows.  The two
-// accumulators and one S^T and dP^T buffer each fill TMEM; both warpgroups
-// work on the same block, each on half of its columns.  Tensor order: dV(j),
+// accumulators and one S^T and dP^T buffer each fill TMEM; the
+// warpgroups work on the same block.  Tensor order: dV(j),
 // S(j+1), dK(j), dP(j+1): P(j+1) is computed under dK(j) and dP(j+1), dS(j)
 // under dV(j) and S(j+1).
 //
@@ -554,7 +564,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // one more K step of 16 whose A operand holds ones in three columns and whose
 // B operand holds -lse / s (for S^T) or -delta (for dP^T) split into three
 // bf16 values a query, so the accumulators come out as S^T - lse / s and dP^T
-// - delta.  (Read from shared memory as vectors per column, they took 30% of
+// - delta.  P is released in two parts, so that dV(j) starts on the first.
+// (Read from shared memory as vectors per column, they took 30% of
 // its cycles, which the MMAs' operands need: 73% of the tensor rate.)
 template <int D, int BQ, bool kKT, bool kVT>
 struct KLayout {
@@ -644,10 +655,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       for (int j = 0; ok && j < blk.nb; ++j) {
         const bool more = j + 1 < blk.nb;
         const int n1 = more ? blk.count(j + 1) : 0, st = qs;  // st: block j's stage in both rings
-        ok = wait(bars.p_full, j);
+        ok = wait(bars.p_full[0], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 16>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        mma_acc<D, BQ, 16, 0>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        ok = wait(bars.p_full[1], j);
+        if (!ok) break;
+        ptx::tc_fence_after_sync();
+        mma_acc<D, BQ, 16, 1>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, false);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
         next(qs, qph);
         next(ds, dph);
@@ -655,7 +670,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 16>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
+        mma_acc<D, BQ, 16, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][st]));
         if (more) ok = dp_mma(n1);
         n = n1;
@@ -666,7 +681,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (!ok) bars.abort = 1;
     }
     __syncwarp();
-  } else {
+  } else if (warp < kWarpK) {
     const int g = warp / 4, trow = (warp % 4) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     auto wait = [&](uint64_t& b, int parity) {
@@ -675,8 +690,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       return (bool)__all_sync(0xffffffffu, got);
     };
     const float c = p.scale * kLog2eB;
-    constexpr int kCh = BQ / 32;  // chunks of 16 columns per group
-    const uint32_t sbase = tmem + lane_base + L::kS + g * (BQ / 2), dbase = tmem + lane_base + L::kDp + g * (BQ / 2);
+    static_assert(BQ % (16 * kSoftGroups) == 0, "");
+    constexpr int kCh = BQ / 16 / kSoftGroups;  // chunks of 16 columns per group
+    const uint32_t sbase = tmem + lane_base + L::kS + g * kCh * 16, dbase = tmem + lane_base + L::kDp + g * kCh * 16;
     bool ok = true;
     for (int j = 0; ok && j < blk.nb; ++j) {
       ok = wait(bars.s_full, j);
@@ -697,10 +713,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           pk[e] = ptx::pack_bf16x2(pr[u][2 * e], pr[u][2 * e + 1]);
         }
         ptx::tmem_st8(sbase + u * 16, pk);
+        if (u == kFirstChunks<BQ> - 1 || u == kCh - 1) {
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before_sync();
+          ptx::mbar_arrive(ptx::smem_addr(&bars.p_full[u == kCh - 1]));
+        }
       }
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before_sync();
-      ptx::mbar_arrive(ptx::smem_addr(&bars.p_full));
       ok = wait(bars.dp_full, j);
       if (!ok) break;
       ptx::tc_fence_after_sync();
@@ -726,10 +744,13 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       ptx::tc_fence_after_sync();
       const int row = tile * kRowsB + trow;
       const int64_t at = (int64_t)h * p.head_stride + ((int64_t)sp.x + row) * p.row_stride;
-      if (g == 0)
-        store_acc<D / 16>(tmem + lane_base + L::kDk, p.dk + at, p.scale, row < sp.y);
-      else
-        store_acc<D / 16>(tmem + lane_base + L::kDv, p.dv + at, 1.f, row < sp.y);
+#pragma unroll 1
+      for (int u = g; u < D / 8; u += kSoftGroups) {  // dk's chunks of 16 columns, then dv's
+        const bool k = u < D / 16;
+        const int c0 = (k ? u : u - D / 16) * 16;
+        store_acc(tmem + lane_base + (k ? L::kDk : L::kDv) + c0, (k ? p.dk : p.dv) + at + c0, k ? p.scale : 1.f,
+                  row < sp.y);
+      }
     }
   }
   ptx::tc_fence_before_sync();
@@ -762,7 +783,7 @@ struct KConfig<128> {
 };
 template <>
 struct KConfig<64> {
-  static constexpr int kB = 128;
+  static constexpr int kB = 96;
   static constexpr bool kKT = true, kVT = true;
 };
 

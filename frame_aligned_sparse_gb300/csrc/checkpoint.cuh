@@ -23,7 +23,7 @@ namespace ckpt {
 
 constexpr int kBlock = FAS_CHECKPOINT_BLOCK;
 
-__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+constexpr uint32_t kInfBits = 0x7F800000u;
 
 // The scale byte for a block whose largest finite magnitude is amax = m 2^E
 // (1 <= m < 2): 448 = 1.75 * 2^8, so the power is E - 8, or E - 7 for m > 1.75.
@@ -46,25 +46,42 @@ __device__ __forceinline__ uint32_t encode2(float x0, float x1) {
 
 // This lane's eight elements of a block as codes (first element in the low
 // byte) and the block's scale byte.  All lanes of the warp take part; the
-// block is the four lanes 4i .. 4i + 3.
+// block is the four lanes 4i .. 4i + 3.  Magnitudes are compared as integers,
+// which orders finite ones below infinity and NaN, so a warp learns from the
+// maximum whether it holds any that are not finite.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
 __device__ __forceinline__ uint2 encode8(const vec::P2 (&p)[4], uint32_t& byte) {
-  float x[8];
+  vec::P2 x[4];
+  uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    x[2 * e] = vec::lo(p[e]);
-    x[2 * e + 1] = vec::hi(p[e]);
+    x[e] = p[e];
+    m = max(m, max((uint32_t)x[e].v & 0x7FFFFFFFu, (uint32_t)(x[e].v >> 32) & 0x7FFFFFFFu));
   }
-  float amax = 0.f;
+  uint32_t amax = block_max(m);
+  if (__any_sync(0xffffffffu, amax >= kInfBits)) {
+    m = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite(x[e]) ? fabsf(x[e]) : 0.f);
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  byte = scale_byte(amax);
-  const float inv = inv_scale_of(byte);
-  float y[8];
+    for (int e = 0; e < 4; ++e) {
+      uint32_t lo = (uint32_t)x[e].v, hi = (uint32_t)(x[e].v >> 32);
+      if ((lo & 0x7FFFFFFFu) >= kInfBits) lo = 0x7FC00000u; else m = max(m, lo & 0x7FFFFFFFu);
+      if ((hi & 0x7FFFFFFFu) >= kInfBits) hi = 0x7FC00000u; else m = max(m, hi & 0x7FFFFFFFu);
+      x[e] = vec::pair(__uint_as_float(lo), __uint_as_float(hi));
+    }
+    amax = block_max(m);
+  }
+  byte = scale_byte(__uint_as_float(amax));
+  const vec::P2 inv = vec::both(inv_scale_of(byte));
+  uint32_t c[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = finite(x[e]) ? x[e] * inv : __uint_as_float(0x7FC00000u);
-  return make_uint2(encode2(y[0], y[1]) | encode2(y[2], y[3]) << 16, encode2(y[4], y[5]) | encode2(y[6], y[7]) << 16);
+  for (int e = 0; e < 4; ++e) {
+    const vec::P2 y = vec::mul2(x[e], inv);
+    c[e] = encode2(vec::lo(y), vec::hi(y));
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // The eight values that codes c under the scale byte stand for (exact).

@@ -202,7 +202,7 @@ struct NormArgs {
   void* dy = nullptr;
   float *dgate = nullptr, *dgamma_post = nullptr, *dgamma_pre = nullptr;
   float *z_part = nullptr, *d_part = nullptr;    // [items, width] partial column sums
-  int64_t rows = 0, items = 0, chunk = 0;
+  int64_t rows = 0, items = 0;
   int width = 0;
   int warps = 1, groups = 1;      // warps per row, rows per CTA (set by the launcher)
   bool f32 = false;               // residual type

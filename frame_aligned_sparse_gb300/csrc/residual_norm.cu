@@ -34,32 +34,19 @@
 #include "kernels.h"
 #include "vec8.cuh"
 
+#ifndef FAS_NORM_FWD
+#define FAS_NORM_FWD 4
+#endif
+#ifndef FAS_NORM_BWD
+#define FAS_NORM_BWD 3
+#endif
+
 namespace fas {
 namespace {
 
-constexpr int kMaxGroups = 8;   // row groups per CTA (named barriers 1 .. 8)
+constexpr int kMaxGroups = 4;   // row groups per CTA (named barriers 1 .. 4), and warps of a CTA unless a row needs more
 constexpr int kMaxWarps = 16;   // warps per row
-
-// Frame of a row and first row of a frame: uniform spans, or a table passed
-// with the launch's arguments (no device copy to keep alive).
-struct Uniform {
-  int64_t span;
-  __device__ __forceinline__ int frame(int64_t row) const { return (int)(row / span); }
-  __device__ __forceinline__ int64_t end(int f) const { return (f + 1) * span; }
-};
-struct Ragged {
-  int n;
-  int32_t start[kNormMaxFrames + 1];
-  __device__ __forceinline__ int frame(int64_t row) const {
-    int lo = 0, hi = n - 1;  // the last frame that starts at or before row
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (start[mid] <= row) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  }
-  __device__ __forceinline__ int64_t end(int f) const { return start[f + 1]; }
-};
+constexpr int kFwdPerSm = FAS_NORM_FWD, kBwdPerSm = FAS_NORM_BWD;  // CTAs per SM
 
 // Sums over the W warps of the row group.  `slot` alternates, so that one
 // barrier a call is enough (a slot is written again two calls later).
@@ -67,6 +54,17 @@ template <int N>
 struct Exchange {
   float v[2][N][kMaxWarps];
 };
+// A barrier of one row group.  The numbers are constants: with one in a
+// register the kernel would claim all sixteen barriers, and an SM holds
+// sixty-four.
+__device__ __forceinline__ void group_sync(int group, int threads) {
+  switch (group) {
+    case 0: asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); break;
+    case 1: asm volatile("bar.sync 2, %0;" ::"r"(threads) : "memory"); break;
+    case 2: asm volatile("bar.sync 3, %0;" ::"r"(threads) : "memory"); break;
+    default: asm volatile("bar.sync 4, %0;" ::"r"(threads) : "memory"); break;
+  }
+}
 template <int N>
 __device__ __forceinline__ void group_sums(float (&v)[N], Exchange<N>& ex, int slot, int warps, int w, int lane,
                                            int group) {
@@ -78,7 +76,7 @@ __device__ __forceinline__ void group_sums(float (&v)[N], Exchange<N>& ex, int s
   if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) ex.v[slot][i][w] = v[i];
-  ptx::named_barrier_sync(1 + group, warps * 32);
+  group_sync(group, warps * 32);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
   for (int k = 0; k < warps; k += 4)  // the row's tail is zero
@@ -95,10 +93,14 @@ __device__ __forceinline__ void clear_exchange(Exchange<N> (&ex)[kMaxGroups]) {
   __syncthreads();
 }
 
-// Stages of a row ring: as many as keep the widest row's ring in shared
-// memory (V = 4: 16,384 columns, 192 KB a stage in the fp32 backward).
-template <int V>
-constexpr int kRing = V == 1 ? 4 : V == 2 ? 2 : 1;
+// Stages of a row ring.  Rows of at most four warps: two (forward) or three
+// (backward) cover HBM's latency with the CTAs that fit; wider rows: what
+// shared memory holds (V = 4: 16,384 columns, 192 KB a stage in the fp32
+// backward).
+template <int V, bool kWide>
+constexpr int kRingFwd = V == 4 ? 1 : 2;
+template <class R, int V, bool kWide>
+constexpr int kRingBwd = !kWide ? (sizeof(R) == 16 ? 3 : 2) : V == 2 && sizeof(R) == 16 ? 2 : 1;
 
 // Asynchronous copies of this thread's bytes into its own shared memory.
 template <int kBytes>
@@ -154,10 +156,43 @@ __device__ __forceinline__ void load_param(const float* p, vec::P2 (&x)[4]) {
   v.get(x);
 }
 
-// kWide: rows of more than eight warps (512 threads a CTA); else 256.
-template <class R, int V, bool kCkpt, bool kWide, class Frames>
-__global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : kCkpt ? 3 : 4)
-    residual_norm_fwd(const NormArgs a, const __grid_constant__ Frames frames) {
+// Work items: each frame's rows are dealt out to its items in turn (item k of
+// n takes rows k, k + n, ...), so that the items of a frame read and write
+// neighbouring rows at any time.  (Consecutive rows per item spread the
+// accesses over as many far places as there are items, @@)
+// Frames of equal spans, or a table passed with the launch's arguments (no
+// device copy to keep alive).
+struct UniformItems {
+  int64_t span;
+  int per_frame;
+  __device__ __forceinline__ int frame(int64_t item) const { return (int)(item / per_frame); }
+  __device__ __forceinline__ int64_t first(int f) const { return (int64_t)f * per_frame; }
+  __device__ __forceinline__ int count(int) const { return per_frame; }
+  __device__ __forceinline__ int64_t start(int f) const { return f * span; }
+  __device__ __forceinline__ int64_t rows(int) const { return span; }
+};
+struct RaggedItems {
+  int n;
+  int32_t row[kNormMaxFrames + 1], item[kNormMaxFrames + 1];
+  __device__ __forceinline__ int frame(int64_t i) const {
+    int lo = 0, hi = n - 1;  // the last frame whose items start at or before i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (item[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ int64_t first(int f) const { return item[f]; }
+  __device__ __forceinline__ int count(int f) const { return item[f + 1] - item[f]; }
+  __device__ __forceinline__ int64_t start(int f) const { return row[f]; }
+  __device__ __forceinline__ int64_t rows(int f) const { return row[f + 1] - row[f]; }
+};
+
+// kWide: rows of more than four warps (up to 512 threads a CTA); else 128
+// threads, so that few registers are left over at any count.
+template <class R, int V, bool kCkpt, bool kWide, class Items>
+__global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
+    residual_norm_fwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
   __shared__ __align__(16) Exchange<1> ex[kMaxGroups];
   clear_exchange(ex);
@@ -165,12 +200,15 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : kCkpt ? 3 : 4)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp / W, w = warp % W;
   const int C = a.width;
-  const int64_t ngroups = (int64_t)gridDim.x * G, gi = (int64_t)blockIdx.x * G + group;
-  const int64_t r0 = a.rows * gi / ngroups;
-  const int n = (int)(a.rows * (gi + 1) / ngroups - r0);
+  const int64_t item = (int64_t)blockIdx.x * G + group;
+  if (item >= a.items) return;  // whole groups: the group's barrier is its own
+  const int f = items.frame(item), stride = items.count(f), first = (int)(item - items.first(f));
+  const int64_t r0 = items.start(f) + first;
+  const int n = (int)((items.rows(f) - first + stride - 1) / stride);
+  const int64_t row_step = (int64_t)stride * C;  // elements between the item's rows
   const float inv_c = 1.0f / (float)C;
   extern __shared__ uint4 ring[];
-  constexpr int S = kRing<V>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
+  constexpr int S = kRingFwd<V, kWide>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   bool in[V];
   int col[V];
@@ -196,36 +234,29 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : kCkpt ? 3 : 4)
           ring_load<Bf16>(dst, step, py + v * vstep * 2);
           ring_load<R>(dst + step, step, px + v * vstep * kElem);
         }
-      py += C * 2;
-      px += (int64_t)C * kElem;
+      py += row_step * 2;
+      px += row_step * kElem;
       ld.next();
     }
     copy_commit();
   };
   for (int i = 0; i < S; ++i) load();
-  P2 gpre[V][4], coef[V][4];
-  const P2 alpha = both(a.alpha), zero = both(0.f);
+  P2 gpre[V][4], coef[V][4];  // coef: alpha gate gamma_post
+  const P2 zero = both(0.f);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) gpre[v][e] = coef[v][e] = zero;
-    if (in[v]) load_param(a.gamma_pre + col[v], gpre[v]);
-  }
-  int frame_end = 0;  // row of this group at which the frame ends
-  for (int i = 0; i < n; ++i) {
-    if (i >= frame_end) {  // a new frame: alpha gate gamma_post
-      const int f = a.gate ? frames.frame(r0 + i) : 0;
-      frame_end = a.gate ? (int)min(frames.end(f) - r0, (int64_t)n) : n;
+    if (in[v]) {
+      load_param(a.gamma_pre + col[v], gpre[v]);
+      load_param(a.gamma_post + col[v], coef[v]);
+      P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
+      if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (in[v]) {
-          load_param(a.gamma_post + col[v], coef[v]);
-          P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
-          if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], alpha), gt[e]);
-        }
+      for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], both(a.alpha)), gt[e]);
     }
+  }
+  for (int i = 0; i < n; ++i) {
     copy_wait<S - 1>();
     P2 y[V][4], x[V][4], acc = zero;
 #pragma unroll
@@ -278,7 +309,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : kCkpt ? 3 : 4)
         uint32_t by, bx;
         const uint2 cy = ckpt::encode8(y[v], by), cx = ckpt::encode8(x[v], bx);
         if (in[v]) {
-          const int64_t at = (r0 + i) * C + col[v];
+          const int64_t at = (r0 + (int64_t)i * stride) * C + col[v];
           *reinterpret_cast<uint2*>(a.y8 + at) = cy;
           *reinterpret_cast<uint2*>(a.x8 + at) = cx;
           if ((lane & 3) == 0) {
@@ -288,39 +319,14 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : kCkpt ? 3 : 4)
         }
       }
     }
-    ph += C * 2;
-    po += (int64_t)C * kElem;
+    ph += row_step * 2;
+    po += row_step * kElem;
     if (w == 0 && lane == 0) {
-      a.rstd[r0 + i] = ry;
-      a.rstd[a.rows + r0 + i] = rx;
+      a.rstd[r0 + (int64_t)i * stride] = ry;
+      a.rstd[a.rows + r0 + (int64_t)i * stride] = rx;
     }
   }
 }
-
-// Backward items: item i covers `chunk` rows (fewer at the end) of one frame.
-struct UniformItems {
-  int64_t span;
-  int per_frame;
-  __device__ __forceinline__ int frame(int64_t item) const { return (int)(item / per_frame); }
-  __device__ __forceinline__ int64_t first(int f) const { return (int64_t)f * per_frame; }
-  __device__ __forceinline__ int64_t start(int f) const { return f * span; }
-  __device__ __forceinline__ int64_t end(int f) const { return (f + 1) * span; }
-};
-struct RaggedItems {
-  int n;
-  int32_t row[kNormMaxFrames + 1], item[kNormMaxFrames + 1];
-  __device__ __forceinline__ int frame(int64_t i) const {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (item[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  }
-  __device__ __forceinline__ int64_t first(int f) const { return item[f]; }
-  __device__ __forceinline__ int64_t start(int f) const { return row[f]; }
-  __device__ __forceinline__ int64_t end(int f) const { return row[f + 1]; }
-};
 
 // y and x' of one thread's eight columns, 16 bits (or fp32 x') or 8 bits.
 template <class R, bool k8>
@@ -334,9 +340,9 @@ struct Held<R, false> {
     ring_load<vec::Bf16>(dst, step, y + cols * 2);
     ring_load<R>(dst + step, step, x + cols * kElem);
   }
-  __device__ __forceinline__ void next(int c) {
+  __device__ __forceinline__ void next(int64_t c) {
     y += c * 2;
-    x += (int64_t)c * kElem;
+    x += c * kElem;
   }
   static __device__ __forceinline__ void get(uint32_t src, uint32_t step, uint32_t, uint32_t, vec::P2 (&yf)[4],
                                              vec::P2 (&xf)[4]) {
@@ -353,7 +359,7 @@ struct Held<R, true> {
     copy_async<8>(dst, y + cols);
     copy_async<8>(dst + 8, x + cols);
   }
-  __device__ __forceinline__ void next(int c) {
+  __device__ __forceinline__ void next(int64_t c) {
     y += c;
     x += c;
   }
@@ -365,11 +371,58 @@ struct Held<R, true> {
   }
 };
 
+// alpha gate gamma_post and gamma_pre of a thread's columns: in registers, or
+// (V = 2, where the two column sums take 64 registers) in shared memory, four
+// 16-byte pieces a vector that only this thread reads.  Kept in registers
+// there, they left 8 warps an SM, or spilled.
+template <int V>
+struct Params {
+  static constexpr int kPieces = V == 2 ? 4 : 0;
+  vec::P2 coef_[V == 2 ? 1 : V][4], gpre_[V == 2 ? 1 : V][4];
+  uint32_t at, step;
+  __device__ __forceinline__ void set(int v, const vec::P2 (&c)[4], const vec::P2 (&g)[4]) {
+    if constexpr (V == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const vec::P2 *x = (i < 2 ? c : g) + (i & 1) * 2;
+        asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(at + (v * 4 + i) * step), "l"(x[0].v), "l"(x[1].v) : "memory");
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        coef_[v][e] = c[e];
+        gpre_[v][e] = g[e];
+      }
+    }
+  }
+  __device__ __forceinline__ void piece(int v, int i, vec::P2 (&x)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x[2 * k].v), "=l"(x[2 * k + 1].v) : "r"(at + (v * 4 + i + k) * step));
+  }
+  __device__ __forceinline__ void coef(int v, vec::P2 (&x)[4]) const {
+    if constexpr (V == 2) {
+      piece(v, 0, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = coef_[v][e];
+    }
+  }
+  __device__ __forceinline__ void gpre(int v, vec::P2 (&x)[4]) const {
+    if constexpr (V == 2) {
+      piece(v, 2, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = gpre_[v][e];
+    }
+  }
+};
+
 // Both row means come from one exchange: with t = dx' + r_x a (g = t - r_x xh
 // m1), sum(b yh) = sum(coef yh t) - r_x m1 sum(coef yh xh), coef = alpha gate
 // gamma_post, so the three sums of a xh, coef yh t and coef yh xh give both.
 template <class R, int V, bool k8, bool kWide, class Items>
-__global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
+__global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
     residual_norm_bwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
   __shared__ __align__(16) Exchange<3> ex[kMaxGroups];
@@ -382,12 +435,13 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
   ptx::grid_launch_next();
   const int64_t item = (int64_t)blockIdx.x * G + group;
   if (item >= a.items) return;  // whole groups: the group's barrier is its own
-  const int f = items.frame(item);
-  const int64_t r0 = items.start(f) + (item - items.first(f)) * a.chunk;
-  const int n = (int)(min(r0 + a.chunk, items.end(f)) - r0);
+  const int f = items.frame(item), stride = items.count(f), first = (int)(item - items.first(f));
+  const int64_t r0 = items.start(f) + first;
+  const int n = (int)((items.rows(f) - first + stride - 1) / stride);
+  const int64_t row_step = (int64_t)stride * C;  // elements between the item's rows
   extern __shared__ uint4 ring[];
   using H = Held<R, k8>;
-  constexpr int S = kRing<V>, kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
+  constexpr int S = kRingBwd<R, V, kWide>, kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   int col[V];
   bool in[V];
@@ -414,9 +468,9 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
           ring_load<Bf16>(dst + kG * step, step, ph + v * vstep * 2);
           held.load(dst + (kG + 1) * step, step, v * vstep);
         }
-      pg += (int64_t)C * kElem;
-      ph += C * 2;
-      held.next(C);
+      pg += row_step * kElem;
+      ph += row_step * 2;
+      held.next(row_step);
       ld.next();
     }
     copy_commit();
@@ -436,14 +490,14 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
   }
   auto load_small = [&](int i, Small& s) {
     if (i < n) {
-      s.ry = pr[i];
-      s.rx = pr[i + a.rows];
+      s.ry = pr[(int64_t)i * stride];
+      s.rx = pr[(int64_t)i * stride + a.rows];
       if (k8)
 #pragma unroll
         for (int v = 0; v < V; ++v)
           if (in[v]) {
-            s.by[v] = sy[(int64_t)i * (C / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
-            s.bx[v] = sx[(int64_t)i * (C / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
+            s.by[v] = sy[i * (row_step / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
+            s.bx[v] = sx[i * (row_step / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
           }
     }
   };
@@ -451,19 +505,24 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
   load_small(0, small[0]);
   load_small(1, small[1]);
   const P2 zero = both(0.f);
-  P2 coef[V][4], gpre[V][4], z[V][4], dg[V][4];
+  P2 z[V][4], dg[V][4];
+  Params<V> params;
+  params.at = base + S * V * kVec * step;
+  params.step = step;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
+    P2 c[4] = {zero, zero, zero, zero}, g[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) coef[v][e] = gpre[v][e] = z[v][e] = dg[v][e] = zero;
+    for (int e = 0; e < 4; ++e) z[v][e] = dg[v][e] = zero;
     if (in[v]) {
-      load_param(a.gamma_post + col[v], coef[v]);
-      load_param(a.gamma_pre + col[v], gpre[v]);
+      load_param(a.gamma_post + col[v], c);
+      load_param(a.gamma_pre + col[v], g);
       P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
       if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], both(a.alpha)), gt[e]);
+      for (int e = 0; e < 4; ++e) c[e] = mul2(mul2(c[e], both(a.alpha)), gt[e]);
     }
+    params.set(v, c, g);
   }
   auto row = [&](int i, Small& sm, int slot) {
     P2 y[V][4], x[V][4], t[V][4];
@@ -482,15 +541,18 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
         ring_read<Bf16>(src + kG * step, step).get(h);
         H::get(src + (kG + 1) * step, step, sm.by[v], sm.bx[v], y[v], x[v]);
       }
+      P2 coef[4], gpre[4];
+      params.coef(v, coef);
+      params.gpre(v, gpre);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         y[v][e] = mul2(y[v][e], ry2);
         x[v][e] = mul2(x[v][e], rx2);
         dg[v][e] = fma2(h[e], x[v][e], dg[v][e]);
-        const P2 ah = mul2(h[e], gpre[v][e]);
+        const P2 ah = mul2(h[e], gpre[e]);
         sa = fma2(ah, x[v][e], sa);
         t[v][e] = fma2(rx2, ah, t[v][e]);
-        const P2 cy = mul2(coef[v][e], y[v][e]);
+        const P2 cy = mul2(coef[e], y[v][e]);
         sb = fma2(cy, t[v][e], sb);
         sc = fma2(cy, x[v][e], sc);
       }
@@ -504,12 +566,13 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
     const P2 nrm1 = both(-rm1), nm2 = both(-m2);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      P2 d[4];
+      P2 d[4], coef[4];
+      params.coef(v, coef);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         t[v][e] = fma2(nrm1, x[v][e], t[v][e]);  // g
         z[v][e] = fma2(y[v][e], t[v][e], z[v][e]);
-        d[e] = mul2(ry2, fma2(nm2, y[v][e], mul2(coef[v][e], t[v][e])));
+        d[e] = mul2(ry2, fma2(nm2, y[v][e], mul2(coef[e], t[v][e])));
       }
       Bf16 dv;
       R ov;
@@ -520,8 +583,8 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
         ov.store(pdx + v * vstep * kElem, 0);
       }
     }
-    pdx += (int64_t)C * kElem;
-    pdy += C * 2;
+    pdx += row_step * kElem;
+    pdy += row_step * 2;
   };
   for (int i = 0; i < n; i += 2) {
     row(i, small[0], 0);
@@ -538,31 +601,34 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 2)
     }
 }
 
-// Adds the partials: a CTA per 32 columns, 128 lanes of four-column loads.
+// Adds the partials: a CTA per 16 columns, 128 lanes of four-column loads.
 // A frame's items are split over `sub` lanes, so that each lane has few loads
 // and all are in flight at once; then the frame's lanes are added, and the
 // frames, each in a fixed order.
-constexpr int kSumCols = 32, kSumLanes = 128, kSumThreads = kSumCols / 4 * kSumLanes;
+constexpr int kSumCols = 16, kSumLanes = 128, kSumThreads = kSumCols / 4 * kSumLanes, kSumRows = kSumThreads / kSumCols;
 
 template <class Items>
 __global__ void __launch_bounds__(kSumThreads)
     residual_norm_sums(const NormArgs a, const __grid_constant__ Items items, int n_frames) {
   __shared__ __align__(16) float zr[kSumLanes][kSumCols], dr[kSumLanes][kSumCols];
+  __shared__ float last[2][kSumCols][kSumRows + 1];
   const int tx = threadIdx.x % (kSumCols / 4), lane = threadIdx.x / (kSumCols / 4);
   const int C = a.width, c0 = blockIdx.x * kSumCols;
   const bool in = c0 + tx * 4 < C;  // C is a multiple of 8
   const int sub = n_frames >= kSumLanes ? 1 : kSumLanes / n_frames, par = kSumLanes / sub;
-  const int ct = threadIdx.x % kSumCols, wt = threadIdx.x / kSumCols;  // one column a thread, 32 warps
+  const int ct = threadIdx.x % kSumCols, wt = threadIdx.x / kSumCols;  // one column a thread
   const bool ct_in = c0 + ct < C;
+  // What the first kernel does not write is read before it ends.
   const float post = ct_in ? a.gamma_post[c0 + ct] * a.alpha : 0.f;
+  float gate = a.gate && ct_in && wt < n_frames ? a.gate[(int64_t)wt * C + c0 + ct] : 1.f;
   ptx::grid_wait_previous();
   float4 d = {0.f, 0.f, 0.f, 0.f};
-  float zs = 0.f;  // warp 0: dgamma_post
+  float zs = 0.f;
   for (int f0 = 0; f0 < n_frames; f0 += par) {
     const int f = f0 + lane / sub, s = lane % sub;
     float4 z = {0.f, 0.f, 0.f, 0.f};
     if (in && lane / sub < par && f < n_frames) {
-      const int64_t i1 = f + 1 < n_frames ? items.first(f + 1) : a.items;
+      const int64_t i1 = items.first(f) + items.count(f);
 #pragma unroll 4
       for (int64_t i = items.first(f) + s; i < i1; i += sub) {
         const float4 p = *reinterpret_cast<const float4*>(a.z_part + i * C + c0 + tx * 4);
@@ -574,34 +640,38 @@ __global__ void __launch_bounds__(kSumThreads)
     *reinterpret_cast<float4*>(&zr[lane][tx * 4]) = z;
     __syncthreads();
     const int nf = n_frames - f0 < par ? n_frames - f0 : par;
-    for (int k = wt; k < nf; k += kSumThreads / kSumCols) {
+    for (int k = wt; k < nf; k += kSumRows) {
       float v = 0.f;
       for (int l = 0; l < sub; ++l) v += zr[k * sub + l][ct];
       if (a.gate && ct_in) {
         const int64_t at = (int64_t)(f0 + k) * C + c0 + ct;
+        if (f0 + k != wt) gate = a.gate[at];
         a.dgate[at] = post * v;
-        v *= a.gate[at];
       }
-      zr[k * sub][ct] = v;
+      zs = fmaf(gate, v, zs);
     }
-    __syncthreads();
-    if (wt == 0)
-      for (int k = 0; k < nf; ++k) zs += zr[k * sub][ct];
     __syncthreads();
   }
   *reinterpret_cast<float4*>(&dr[lane][tx * 4]) = d;
   __syncthreads();
-  constexpr int kPer = kSumLanes / (kSumThreads / kSumCols);  // lanes a warp adds first
-  float v = 0.f;
+  float ds = 0.f;
 #pragma unroll
-  for (int l = 0; l < kPer; ++l) v += dr[wt * kPer + l][ct];
-  zr[wt][ct] = v;
+  for (int l = 0; l < kSumLanes / kSumRows; ++l) ds += dr[wt * (kSumLanes / kSumRows) + l][ct];
+  last[0][ct][wt] = zs;
+  last[1][ct][wt] = ds;
   __syncthreads();
-  if (wt == 0 && ct_in) {
-    float ds = 0.f;
-    for (int l = 0; l < kSumThreads / kSumCols; ++l) ds += zr[l][ct];
-    a.dgamma_post[c0 + ct] = a.alpha * zs;
-    a.dgamma_pre[c0 + ct] = ds;
+  // A warp per column adds its 32 shares.
+  static_assert(kSumRows == 32 && kSumThreads == 32 * kSumCols, "");
+  const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+  float v0 = last[0][w][l], v1 = last[1][w][l];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v0 += __shfl_xor_sync(0xffffffffu, v0, o);
+    v1 += __shfl_xor_sync(0xffffffffu, v1, o);
+  }
+  if (l == 0 && c0 + w < C) {
+    a.dgamma_post[c0 + w] = a.alpha * v0;
+    a.dgamma_pre[c0 + w] = v1;
   }
 }
 
@@ -611,62 +681,51 @@ struct Shape {
 };
 Shape shape_of(int width) {
   const int vecs = width / 8;
-  const int V = vecs <= 32 * kMaxWarps ? 1 : vecs <= 64 * kMaxWarps ? 2 : 4;
+  const int V = vecs <= 32 * kMaxGroups ? 1 : vecs <= 64 * kMaxWarps ? 2 : 4;
   const int W = (vecs + 32 * V - 1) / (32 * V);
   return {V, W, std::max(1, kMaxGroups / W)};
 }
 
-// Row groups that run at once for a kernel of `threads` a CTA on the device.
-template <class K>
-int64_t resident_groups(K kern, const Shape& s, size_t smem, int sms) {
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * s.W * s.G, smem) != cudaSuccess || per_sm < 1)
-    return 0;
-  return (int64_t)per_sm * sms * s.G;
-}
-
-// Opt-in shared memory of a kernel's ring (per launch: it belongs to the
-// device's context; up to 48 KB with the static part goes without).
+// A kernel's ring: its opt-in shared memory, and the SM's whole share for it
+// (by itself the driver leaves room for fewer CTAs than fit).  Set on every
+// launch: it belongs to the device's context.
 template <class K>
 cudaError_t allow_ring(K kern, size_t smem) {
-  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                          : cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
-template <class R, int V, bool kCkpt, bool kWide, class Frames>
-cudaError_t fwd(NormArgs a, const Frames& fr, const Shape& s, int sms, cudaStream_t st) {
-  auto kern = residual_norm_fwd<R, V, kCkpt, kWide, Frames>;
-  const size_t smem = (size_t)32 * s.W * s.G * kRing<V> * V * (16 + sizeof(R));
+template <class R, int V, bool kCkpt, bool kWide, class Items>
+cudaError_t fwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
+  auto kern = residual_norm_fwd<R, V, kCkpt, kWide, Items>;
+  const size_t smem = (size_t)32 * s.W * s.G * kRingFwd<V, kWide> * V * (16 + sizeof(R));
   const cudaError_t e = allow_ring(kern, smem);
   if (e != cudaSuccess) return e;
-  int64_t groups = a.rows;
-  if (groups > s.G * sms) {  // more rows than groups that surely fit
-    const int64_t res = resident_groups(kern, s, smem, sms);
-    if (res == 0) return cudaErrorInvalidConfiguration;
-    groups = std::min(groups, res);
-  }
-  kern<<<(unsigned)((groups + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, fr);
+  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
   return cudaGetLastError();
 }
 
-template <class R, int V, class Frames>
-cudaError_t fwd_c(const NormArgs& a, const Frames& fr, const Shape& s, int sms, cudaStream_t st) {
-  if (s.W > kMaxGroups) return a.y8 ? fwd<R, V, true, true>(a, fr, s, sms, st) : fwd<R, V, false, true>(a, fr, s, sms, st);
-  if constexpr (V == 1)
-    return a.y8 ? fwd<R, V, true, false>(a, fr, s, sms, st) : fwd<R, V, false, false>(a, fr, s, sms, st);
-  return cudaErrorInvalidValue;  // V > 1 only for rows of more than eight warps
+template <class R, int V, class Items>
+cudaError_t fwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
+  if constexpr (V >= 2)
+    if (s.W > kMaxGroups) return a.y8 ? fwd<R, V, true, true>(a, it, s, st) : fwd<R, V, false, true>(a, it, s, st);
+  if constexpr (V <= 2)
+    return a.y8 ? fwd<R, V, true, false>(a, it, s, st) : fwd<R, V, false, false>(a, it, s, st);
+  return cudaErrorInvalidValue;  // V = 4 has more warps
 }
-template <class Frames>
-cudaError_t fwd_all(const NormArgs& a, const Frames& fr, const Shape& s, int sms, cudaStream_t st) {
-  if (s.V == 1) return a.f32 ? fwd_c<vec::F32, 1>(a, fr, s, sms, st) : fwd_c<vec::Bf16, 1>(a, fr, s, sms, st);
-  if (s.V == 2) return a.f32 ? fwd_c<vec::F32, 2>(a, fr, s, sms, st) : fwd_c<vec::Bf16, 2>(a, fr, s, sms, st);
-  return a.f32 ? fwd_c<vec::F32, 4>(a, fr, s, sms, st) : fwd_c<vec::Bf16, 4>(a, fr, s, sms, st);
+template <class Items>
+cudaError_t fwd_all(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
+  if (s.V == 1) return a.f32 ? fwd_c<vec::F32, 1>(a, it, s, st) : fwd_c<vec::Bf16, 1>(a, it, s, st);
+  if (s.V == 2) return a.f32 ? fwd_c<vec::F32, 2>(a, it, s, st) : fwd_c<vec::Bf16, 2>(a, it, s, st);
+  return a.f32 ? fwd_c<vec::F32, 4>(a, it, s, st) : fwd_c<vec::Bf16, 4>(a, it, s, st);
 }
 
 template <class R, int V, bool k8, bool kWide, class Items>
 cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
   auto kern = residual_norm_bwd<R, V, k8, kWide, Items>;
-  const size_t smem = (size_t)32 * s.W * s.G * kRing<V> * V * (sizeof(R) + 16 + 16 * Held<R, k8>::kPieces);
+  const size_t smem = (size_t)32 * s.W * s.G * V * 16 *
+                      (kRingBwd<R, V, kWide> * (sizeof(R) / 16 + 1 + Held<R, k8>::kPieces) + Params<V>::kPieces);
   const cudaError_t e = allow_ring(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
@@ -674,9 +733,10 @@ cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t
 }
 template <class R, int V, class Items>
 cudaError_t bwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true>(a, it, s, st) : bwd<R, V, false, true>(a, it, s, st);
-  if constexpr (V == 1) return a.y8 ? bwd<R, V, true, false>(a, it, s, st) : bwd<R, V, false, false>(a, it, s, st);
-  return cudaErrorInvalidValue;  // V > 1 only for rows of more than eight warps
+  if constexpr (V >= 2)
+    if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true>(a, it, s, st) : bwd<R, V, false, true>(a, it, s, st);
+  if constexpr (V <= 2) return a.y8 ? bwd<R, V, true, false>(a, it, s, st) : bwd<R, V, false, false>(a, it, s, st);
+  return cudaErrorInvalidValue;  // V = 4 has more warps
 }
 template <class Items>
 cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shape& s, cudaStream_t st) {
@@ -702,35 +762,17 @@ cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shap
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-}  // namespace
-
-cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
-                                 cudaStream_t st) {
-  const Shape s = shape_of(a.width);
-  a.warps = s.W;
-  a.groups = s.G;
-  if (!spans) return fwd_all(a, Uniform{span}, s, sms, st);
-  Ragged fr;
-  fr.n = n_frames;
-  fr.start[0] = 0;
-  for (int f = 0; f < n_frames; ++f) fr.start[f + 1] = fr.start[f] + spans[f];
-  return fwd_all(a, fr, s, sms, st);
-}
-
-// Rows per item: about one item per group that runs at once (kItemGroups a
-// SM), and never across frames.  Depends on the shape and the device alone.
-constexpr int kItemGroupsPerSm = 2;
-
-NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms) {
-  const Shape s = shape_of(width);
-  const int64_t want = std::max<int64_t>(n_frames, (int64_t)kItemGroupsPerSm * sms * s.G);
+// Splits the rows: about one item per row group of `per_sm` CTAs on every SM,
+// none across frames.  Depends on the shape and the device alone.
+NormItems split(int64_t rows, const Shape& s, const int32_t* spans, int n_frames, int64_t span, int sms, int per_sm) {
+  const int64_t want = std::max<int64_t>(n_frames, (int64_t)per_sm * sms * s.G);
   auto count = [&](int64_t chunk) {
     if (!spans) return (int64_t)n_frames * ((span + chunk - 1) / chunk);
     int64_t n = 0;
     for (int f = 0; f < n_frames; ++f) n += (spans[f] + chunk - 1) / chunk;
     return n;
   };
-  int64_t lo = 1, hi = rows;  // the smallest chunk with at most `want` items
+  int64_t lo = 1, hi = rows;  // the fewest rows an item with at most `want` items
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
     if (count(mid) <= want) hi = mid; else lo = mid + 1;
@@ -738,6 +780,37 @@ NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int
   NormItems r;
   r.chunk = lo;
   r.items = count(lo);
+  return r;
+}
+
+// Calls fn with the frames' item table.
+template <class Fn>
+cudaError_t with_items(const NormItems& n, const int32_t* spans, int n_frames, int64_t span, Fn fn) {
+  if (!spans) return fn(UniformItems{span, (int)((span + n.chunk - 1) / n.chunk)});
+  RaggedItems it;
+  it.n = n_frames;
+  it.row[0] = it.item[0] = 0;
+  for (int f = 0; f < n_frames; ++f) {
+    it.row[f + 1] = it.row[f] + spans[f];
+    it.item[f + 1] = it.item[f] + (int32_t)((spans[f] + n.chunk - 1) / n.chunk);
+  }
+  return fn(it);
+}
+
+}  // namespace
+
+cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
+                                 cudaStream_t st) {
+  const Shape s = shape_of(a.width);
+  const NormItems n = split(a.rows, s, spans, n_frames, span, sms, kFwdPerSm);
+  a.warps = s.W;
+  a.groups = s.G;
+  a.items = n.items;
+  return with_items(n, spans, n_frames, span, [&](const auto& it) { return fwd_all(a, it, s, st); });
+}
+
+NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms) {
+  NormItems r = split(rows, shape_of(width), spans, n_frames, span, sms, kBwdPerSm);
   r.bytes = 2 * align256(r.items * width * 4);
   return r;
 }
@@ -748,20 +821,9 @@ cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const 
   a.warps = s.W;
   a.groups = s.G;
   a.items = n.items;
-  a.chunk = n.chunk;
-  const int64_t part = align256(n.items * a.width * 4);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.z_part = reinterpret_cast<float*>(ws);
-  a.d_part = reinterpret_cast<float*>(ws + part);
-  if (!spans) return bwd_all(a, UniformItems{span, (int)((span + n.chunk - 1) / n.chunk)}, n_frames, s, st);
-  RaggedItems it;
-  it.n = n_frames;
-  it.row[0] = it.item[0] = 0;
-  for (int f = 0; f < n_frames; ++f) {
-    it.row[f + 1] = it.row[f] + spans[f];
-    it.item[f + 1] = it.item[f] + (int32_t)((spans[f] + n.chunk - 1) / n.chunk);
-  }
-  return bwd_all(a, it, n_frames, s, st);
+  a.z_part = static_cast<float*>(workspace);
+  a.d_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(n.items * a.width * 4));
+  return with_items(n, spans, n_frames, span, [&](const auto& it) { return bwd_all(a, it, n_frames, s, st); });
 }
 
 }  // namespace fas
