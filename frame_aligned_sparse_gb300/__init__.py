@@ -429,6 +429,15 @@ def _current_device_stream() -> Tuple[int, int]:
     return device, torch._C._cuda_getCurrentRawStream(device)
 
 
+def _output(name, t, like, device: int):
+    """An output with like's type and shape, and its address."""
+    import torch
+    if t is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr()
+    return t, _check_here(name, t, like.shape, like.dtype, device)
+
+
 def _on(stream, current: int) -> int:
     return current if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -437,8 +446,6 @@ def _own_until_run(stream, *temps):
     """Keeps the memory of tensors the binding allocated for a call on
     another stream than the current one until that stream has used it."""
     import torch
-    if stream is None:
-        return
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream != torch.cuda.current_stream():
@@ -457,13 +464,17 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
             _check_here("v", v, shape, bf16, device), _check_here("out", out, shape, bf16, device),
             _check_here("lse", lse, lse_shape, torch.float32, device),
             _check_here("dout", dout, shape, bf16, device)]
-    dq, dk, dv = (torch.empty_like(q) if t is None else t for t in (dq, dk, dv))
-    ptrs += [_check_here("dq", dq, shape, bf16, device), _check_here("dk", dk, shape, bf16, device),
-             _check_here("dv", dv, shape, bf16, device)]
+    dq, p = _output("dq", dq, q, device)
+    ptrs.append(p)
+    dk, p = _output("dk", dk, q, device)
+    ptrs.append(p)
+    dv, p = _output("dv", dv, q, device)
+    ptrs.append(p)
     workspace = torch.empty((32, *lse_shape), dtype=torch.uint8, device=q.device)  # FAS_BACKWARD_WORKSPACE
     rc = load().fas_backward(*ptrs, workspace.data_ptr(), _on(stream, current))
     _check("fas_backward", rc)
-    _own_until_run(stream, workspace, dq, dk, dv)
+    if stream is not None:
+        _own_until_run(stream, workspace, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -475,12 +486,14 @@ class Checkpoint(NamedTuple):
     scales: "torch.Tensor"
 
 
-def _dtype_code(name, t):
+def _dtype_code(name, t) -> int:
     import torch
-    codes = {torch.bfloat16: 0, torch.float32: 1}
-    if not isinstance(t, torch.Tensor) or t.dtype not in codes:
-        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
-    return codes[t.dtype]
+    if isinstance(t, torch.Tensor):
+        if t.dtype is torch.bfloat16:
+            return 0
+        if t.dtype is torch.float32:
+            return 1
+    raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
 
 
 def _checkpoint_empty(shape, device):
@@ -515,7 +528,8 @@ def fas_checkpoint_pack(x, out: Optional[Checkpoint] = None, stream=None) -> Che
     c = _checkpoint_empty(tuple(x.shape), x.device) if out is None else out
     c, ptrs = _check_checkpoint("out", c, device, x.shape)
     _check("fas_checkpoint_pack", load().fas_checkpoint_pack(ptr, dtype, *ptrs, x.numel(), _on(stream, current)))
-    _own_until_run(stream, *c)
+    if stream is not None:
+        _own_until_run(stream, *c)
     return c
 
 
@@ -535,7 +549,8 @@ def fas_checkpoint_unpack(c: Checkpoint, dtype=None, out=None, stream=None):
     ptr = _check_here("out", out, shape, out.dtype, device)
     _check("fas_checkpoint_unpack",
            load().fas_checkpoint_unpack(*ptrs, ptr, code, out.numel(), _on(stream, current)))
-    _own_until_run(stream, out)
+    if stream is not None:
+        _own_until_run(stream, out)
     return out
 
 
@@ -589,11 +604,8 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
     ppost = _check_here("gamma_post", gamma_post, (C,), f32, device)
     ppre = _check_here("gamma_pre", gamma_pre, (C,), f32, device)
     pgate, spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
-    if x_out is None:
-        x_out = torch.empty_like(x)
-    if h is None:
-        h = torch.empty_like(y)
-    px_out, ph = _check_here("x_out", x_out, shape, x.dtype, device), _check_here("h", h, shape, bf16, device)
+    x_out, px_out = _output("x_out", x_out, x, device)
+    h, ph = _output("h", h, y, device)
     rstd = torch.empty((2, N), dtype=f32, device=x.device)
     held = (_checkpoint_empty((N, C), x.device), _checkpoint_empty((N, C), x.device)) if checkpoint else ()
     parts = [t for c in held for t in c]
@@ -601,7 +613,8 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
                                   None if spans is None else spans.ctypes.data, frames, px_out, ph, rstd.data_ptr(),
                                   *([t.data_ptr() for t in parts] or (None,) * 4), _on(stream, current))
     _check("fas_residual_norm", rc)
-    _own_until_run(stream, x_out, h, rstd, *parts)
+    if stream is not None:
+        _own_until_run(stream, x_out, h, rstd, *parts)
     return (x_out, h, rstd, *held)
 
 
@@ -632,21 +645,20 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
              _check_here("gamma_post", gamma_post, (C,), f32, device),
              _check_here("gamma_pre", gamma_pre, (C,), f32, device)]
     args[-3], spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
-    if dx is None:
-        dx = torch.empty_like(dx_out)
-    if dy is None:
-        dy = torch.empty_like(dh)
+    dx, pdx = _output("dx", dx, dx_out, device)
+    dy, pdy = _output("dy", dy, dh, device)
     need = _norm_workspace(N, C, None if spans is None else spans.tobytes(), frames, device)
     workspace = torch.empty(need, dtype=torch.uint8, device=dx_out.device)
     dpost, dpre = torch.empty_like(gamma_post), torch.empty_like(gamma_pre)
     dgate = None if gate is None else torch.empty_like(gate)
     rc = load().fas_residual_norm_backward(
         *args, alpha, N, C, None if spans is None else spans.ctypes.data, frames,
-        _check_here("dx", dx, shape, dx_out.dtype, device), _check_here("dy", dy, shape, bf16, device),
+        pdx, pdy,
         None if dgate is None else dgate.data_ptr(), dpost.data_ptr(), dpre.data_ptr(), workspace.data_ptr(), need,
         _on(stream, current))
     _check("fas_residual_norm_backward", rc)
-    _own_until_run(stream, workspace, dpost, dpre, dx, dy, *([] if dgate is None else [dgate]))
+    if stream is not None:
+        _own_until_run(stream, workspace, dpost, dpre, dx, dy, *([] if dgate is None else [dgate]))
     return dx, dy, dpost, dpre, dgate
 
 

@@ -1054,7 +1054,7 @@ int fas_residual_norm_backward(const void* dx_out, const void* dh, const void* y
   a.width = width;
   a.f32 = residual == FAS_DTYPE_F32;
   a.alpha = alpha;
-  const cudaError_t e = fas::launch_residual_norm_backward(a, items, frame_tokens, n_frames, span, workspace,
+  const cudaError_t e = fas::launch_residual_norm_backward(a, items, frame_tokens, n_frames, span, sms, workspace,
                                                            static_cast<cudaStream_t>(cuda_stream));
   g_state.last_launches = e == cudaSuccess ? 2 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;

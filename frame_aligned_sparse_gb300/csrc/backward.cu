@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   __shared__ __align__(16) float centre[D];
   const uint32_t q_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, do_s = q_s + L::kTile;
   const uint32_t k_s0 = do_s + L::kTile, v_s0 = k_s0 + S * L::kBlock;
+  ptx::grid_launch_next();
   FAS_BWD_PROLOGUE();
   const Blocks blk(p.table[f], kBk);
 
@@ -607,6 +608,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
         load_rows<D, kRowsB>(k_s, &tm_k, tb, sp.x + tile * kRowsB, h);
         load_rows<D, kRowsB>(v_s, &tm_v, tb, sp.x + tile * kRowsB, h);
+        // Everything this CTA writes hangs on the statistics, so nothing of
+        // it happens before the query pass has ended.
+        ptx::grid_wait_previous();
         produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
@@ -811,8 +815,19 @@ int launch(const BwdParams& p, int grid, cudaStream_t st) {
     return -1;
   kq<<<grid, kThreadsB, LQ::kSmem, st>>>(tq, tdo, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  kk<<<grid, kThreadsB, LK::kSmem, st>>>(tk, tv, tq, tdo, p);
-  return cudaGetLastError() == cudaSuccess ? 2 : -1;
+  // The key pass starts in the query pass's tail and waits there for its
+  // statistics.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreadsB);
+  cfg.dynamicSmemBytes = LK::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kk, tk, tv, tq, tdo, p) == cudaSuccess ? 2 : -1;
 }
 
 }  // namespace

@@ -205,6 +205,7 @@ struct NormArgs {
   int64_t rows = 0, items = 0;
   int width = 0;
   int warps = 1, groups = 1;      // warps per row, rows per CTA (set by the launcher)
+  int sms = 1;                    // SMs of the device (set by the launcher)
   bool f32 = false;               // residual type
   float alpha = 1.f, eps = 0.f;
 };
@@ -219,7 +220,7 @@ NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int
 cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
                                  cudaStream_t stream);
 cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
-                                          int64_t span, void* workspace, cudaStream_t stream);
+                                          int64_t span, int sms, void* workspace, cudaStream_t stream);
 
 // n elements (a multiple of 32) to and from 8-bit checkpoints.
 cudaError_t launch_checkpoint_pack(const void* x, bool f32, uint8_t* codes, uint8_t* scales, int64_t n,

@@ -46,7 +46,7 @@ namespace {
 
 constexpr int kMaxGroups = 4;   // row groups per CTA (named barriers 1 .. 4), and warps of a CTA unless a row needs more
 constexpr int kMaxWarps = 16;   // warps per row
-constexpr int kFwdPerSm = FAS_NORM_FWD, kBwdPerSm = FAS_NORM_BWD;  // CTAs per SM
+constexpr int kFwdPerSm = FAS_NORM_FWD, kBwdPerSm = FAS_NORM_BWD;  // CTAs of four warps per SM
 
 // Sums over the W warps of the row group.  `slot` alternates, so that one
 // barrier a call is enough (a slot is written again two calls later).
@@ -686,21 +686,24 @@ Shape shape_of(int width) {
   return {V, W, std::max(1, kMaxGroups / W)};
 }
 
-// A kernel's ring: its opt-in shared memory, and the SM's whole share for it
-// (by itself the driver leaves room for fewer CTAs than fit).  Set on every
-// launch: it belongs to the device's context.
+// A kernel's ring: its opt-in shared memory, and, for more CTAs than SMs, the
+// SM's whole share for it (by itself the driver leaves room for fewer CTAs
+// than fit).  Set on every launch: it belongs to the device's context.
 template <class K>
-cudaError_t allow_ring(K kern, size_t smem) {
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+cudaError_t allow_ring(K kern, size_t smem, bool many) {
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024)  // up to 48 KB with the static part goes without
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && many)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  return e;
 }
 
 template <class R, int V, bool kCkpt, bool kWide, class Items>
 cudaError_t fwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
   auto kern = residual_norm_fwd<R, V, kCkpt, kWide, Items>;
   const size_t smem = (size_t)32 * s.W * s.G * kRingFwd<V, kWide> * V * (16 + sizeof(R));
-  const cudaError_t e = allow_ring(kern, smem);
+  const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
   return cudaGetLastError();
@@ -726,7 +729,7 @@ cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t
   auto kern = residual_norm_bwd<R, V, k8, kWide, Items>;
   const size_t smem = (size_t)32 * s.W * s.G * V * 16 *
                       (kRingBwd<R, V, kWide> * (sizeof(R) / 16 + 1 + Held<R, k8>::kPieces) + Params<V>::kPieces);
-  const cudaError_t e = allow_ring(kern, smem);
+  const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
   return cudaGetLastError();
@@ -762,10 +765,12 @@ cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shap
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Splits the rows: about one item per row group of `per_sm` CTAs on every SM,
-// none across frames.  Depends on the shape and the device alone.
+// Splits the rows: about one item per row group that runs at once, none
+// across frames.  Depends on the shape and the device alone.
 NormItems split(int64_t rows, const Shape& s, const int32_t* spans, int n_frames, int64_t span, int sms, int per_sm) {
-  const int64_t want = std::max<int64_t>(n_frames, (int64_t)per_sm * sms * s.G);
+  // per_sm is in CTAs of four warps (which fix the registers a thread).
+  const int ctas = std::max(1, per_sm * kMaxGroups / (s.W * s.G));
+  const int64_t want = std::max<int64_t>(n_frames, (int64_t)ctas * sms * s.G);
   auto count = [&](int64_t chunk) {
     if (!spans) return (int64_t)n_frames * ((span + chunk - 1) / chunk);
     int64_t n = 0;
@@ -806,6 +811,7 @@ cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames,
   a.warps = s.W;
   a.groups = s.G;
   a.items = n.items;
+  a.sms = sms;
   return with_items(n, spans, n_frames, span, [&](const auto& it) { return fwd_all(a, it, s, st); });
 }
 
@@ -816,8 +822,9 @@ NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int
 }
 
 cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
-                                          int64_t span, void* workspace, cudaStream_t st) {
+                                          int64_t span, int sms, void* workspace, cudaStream_t st) {
   const Shape s = shape_of(a.width);
+  a.sms = sms;
   a.warps = s.W;
   a.groups = s.G;
   a.items = n.items;
