@@ -948,7 +948,7 @@ int fas_residual_norm(const void* y, const void* x, int residual, const float* g
                       const float* gamma_pre, float alpha, float eps, int64_t tokens, int width,
                       const int32_t* frame_tokens, int n_frames, void* x_out, void* h, float* rstd, uint8_t* y_codes,
                       uint8_t* y_scales, uint8_t* x_codes, uint8_t* x_scales, void* cuda_stream) {
-  if (!y || !x || !gamma_post || !gamma_pre || !x_out || !h || !rstd) return FAS_ERR_ARG;
+  if (!y || !x || !gamma_post || !gamma_pre || !x_out || !h || !rstd || x_out == h) return FAS_ERR_ARG;
   int rc = norm_shape(tokens, width, residual);
   if (rc != FAS_OK) return rc;
   const int held = (y_codes != nullptr) + (y_scales != nullptr) + (x_codes != nullptr) + (x_scales != nullptr);
@@ -1012,7 +1012,7 @@ int fas_residual_norm_backward(const void* dx_out, const void* dh, const void* y
                                void* cuda_stream) {
   if (!dx_out || !dh || !rstd || !gamma_post || !gamma_pre || !dx || !dy || !dgamma_post || !dgamma_pre || !workspace)
     return FAS_ERR_ARG;
-  if ((gate == nullptr) != (dgate == nullptr)) return FAS_ERR_ARG;
+  if ((gate == nullptr) != (dgate == nullptr) || dx == dy) return FAS_ERR_ARG;
   const int plain = (y != nullptr) + (x_out != nullptr);
   const int held = (y_codes != nullptr) + (y_scales != nullptr) + (x_codes != nullptr) + (x_scales != nullptr);
   if (!((plain == 2 && held == 0) || (plain == 0 && held == 4))) return FAS_ERR_ARG;

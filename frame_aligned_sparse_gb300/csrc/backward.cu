@@ -14,7 +14,16 @@
 // over the queries that see them.  Together they compute S and dP twice (7
 // products for the 5 that the gradients need), but every gradient stays in
 // TMEM until its one store: no fp32 gradient goes through memory, no atomics,
-// bit-reproducible results.
+// bit-reproducible results.  (One kernel for all five would stage dS in
+// shared memory for two more operands, 208 KB a block of 64 queries, over
+// 1660 clocks of its bandwidth for 1280 of the tensor pipe, and add 64 KB of
+// fp32 reductions to L2 a pair of tiles.)
+//
+// Bound by the tensor pipe and, on long runs, by power: the 720p geometry
+// with 6 heads takes 11.9 ms, 1.18 PFLOP/s of the five products and 1.65 of
+// the seven executed, 0.97 of the rate that the library's bf16 product
+// sustains (1.70); at d = 64 the exponentials and their conversions bound it
+// (0.73 PFLOP/s of five).
 //
 // A visible range is walked in blocks; its last block is shortened to the
 // tokens it has (a multiple of 16) through the MMA's N or its K steps, so no
@@ -25,9 +34,9 @@
 // dS_ij = 0 up to out's rounding, a common component c of the keys cancels in
 // dq, but the roundings of dS times c do not: the query pass sums what
 // rounding added to each row and takes it out along c (the mean of the first
-// 64 keys), which leaves the roundings times k - c.  (Keys with a common
-// component three times their spread, as the prepass's mean-centring is for,
-// tripled dq's error without it.)
+// 64 keys), which leaves the roundings times k - c.  (On keys with a common
+// component of three times their spread, as the prepass's mean-centring is
+// for, dq's error against 64 bits is 2.4e-3, dk's and dv's; 5.5e-3 without.)
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -56,7 +65,6 @@ constexpr int kWarpK = 4 * kSoftGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK +
 constexpr int kThreadsB = 32 * (kWarpMean + 1);
 constexpr int kMaxStagesB = 6;
 constexpr uint32_t kTmemAll = 512;
-constexpr float kLog2eB = 1.4426950408889634f;
 
 // Blocks of one item's two visible ranges.
 struct Blocks {
@@ -118,9 +126,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // x as the sum of three bf16 values (24 bits: exact to fp32 rounding) in the
-// first three elements of a 16-byte row, the others zero.
+// first three elements of a 16-byte row, the others zero; infinities and NaN
+// in the first alone.
 __device__ __forceinline__ uint4 split3(float x) {
   const uint32_t a = ptx::pack_bf16x2(x, 0.f) & 0xFFFFu;
+  if ((a & 0x7F80u) == 0x7F80u) return make_uint4(a, 0u, 0u, 0u);
   const float r1 = x - __uint_as_float(a << 16);
   const uint32_t b = ptx::pack_bf16x2(r1, 0.f) & 0xFFFFu;
   const float r2 = r1 - __uint_as_float(b << 16);
@@ -442,14 +452,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     ptx::named_barrier_sync(1, kSoftThreads);
     const float delta = red[0][trow];
     // A row past the frame's end gets P = 0 and is never stored.
-    const float nl = -lse * kLog2eB;
+    const float nl = -lse * core::kLog2e;
     if (valid && g < 2) {  // group 0: -lse / s, group 1: -delta, as the key pass's MMA takes them
       uint8_t* st = p.stats + ((int64_t)g * p.H * p.N + (int64_t)h * p.N + token) * kStatBytes;
       *reinterpret_cast<uint4*>(st) = split3(g == 0 ? -lse / p.scale : -delta);
     }
     ptx::named_barrier_sync(1, kSoftThreads);  // red is written again
     bool ok = true;
-    const uint64_t c2 = ptx::f32x2(p.scale * kLog2eB, p.scale * kLog2eB), nl2 = ptx::f32x2(nl, nl);
+    const uint64_t c2 = ptx::f32x2(p.scale * core::kLog2e, p.scale * core::kLog2e), nl2 = ptx::f32x2(nl, nl);
     const float nd = -delta;
     const uint64_t minus1 = ptx::f32x2(-1.f, -1.f);
     float e0 = 0.f, e1 = 0.f;  // what rounding dS to bf16 added to the row
@@ -566,40 +576,43 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // B operand holds -lse / s (for S^T) or -delta (for dP^T) split into three
 // bf16 values a query, so the accumulators come out as S^T - lse / s and dP^T
 // - delta.  P is released in two parts, so that dV(j) starts on the first.
-// (Read from shared memory as vectors per column, they took 30% of
-// its cycles, which the MMAs' operands need: 73% of the tensor rate.)
-template <int D, int BQ, bool kKT, bool kVT>
+// (Read
+// from shared memory as vectors per column, they took 30% of its cycles, which
+// the MMAs' operands need.)
+constexpr int kBq = 96;  // queries per block
+
+template <int D>
 struct KLayout {
-  static constexpr uint32_t kDk = 0, kDv = D, kS = 2 * D, kDp = 2 * D + BQ, kK = 2 * D + 2 * BQ,
-                            kV = kK + (kKT ? D / 2 : 0);
-  static_assert(kV + (kVT ? D / 2 : 0) <= kTmemAll, "TMEM columns");
-  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = BQ * D * 2;
-  static constexpr uint32_t kStat = 2 * BQ * kStatBytes, kOnes = 2 * kRowsB * 16;  // ones (16 columns), a stage's statistics
+  // V's A operand is in TMEM; K's too where there is room (d = 64).
+  static constexpr bool kKT = D == 64;
+  static constexpr uint32_t kDk = 0, kDv = D, kS = 2 * D, kDp = kS + kBq, kV = kDp + kBq, kK = kV + D / 2;
+  static_assert(kK + (kKT ? D / 2 : 0) <= kTmemAll, "TMEM columns");
+  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBq * D * 2;
+  static constexpr uint32_t kStat = 2 * kBq * kStatBytes, kOnes = 2 * kRowsB * 16;  // ones (16 columns), a stage's statistics
   static constexpr int kFit = (int)((232448 - 1024 - 512 - kOnes - 2 * kTile) / (2 * kBlock + kStat));
   static constexpr int kStages = kFit < kMaxStagesB ? kFit : kMaxStagesB;
   static constexpr size_t kSmem = 1024 + kOnes + 2 * kTile + kStages * (2 * kBlock + kStat);
 };
 
-template <int D, int BQ, bool kKT, bool kVT>
+template <int D>
 __global__ void __launch_bounds__(kThreadsB, 1)
     attention_bwd_k(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const BwdParams p) {
-  using L = KLayout<D, BQ, kKT, kVT>;
+  using L = KLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ BarsB bars;
   const uint32_t k_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t v_s = k_s + L::kTile, q_s0 = v_s + L::kTile, do_s0 = q_s0 + L::kStages * L::kBlock;
   const uint32_t stat_s0 = do_s0 + L::kStages * L::kBlock, ones_s = stat_s0 + L::kStages * L::kStat;
-  // The ones: 128 rows of {1, 1, 1, 0, 0, 0, 0, 0}, then 128 rows of zeros
-  // (columns 8 .. 15; the statistics' columns 8 .. 15 may then be anything
-  // finite, and alias columns 0 .. 7).
+  // The ones: 128 rows of {1, 1, 1, 0, 0, 0, 0, 0}, then 128 rows of zeros,
+  // which are columns 8 .. 15 of both operands of the statistics' K step.
   for (uint32_t i = threadIdx.x; i < L::kOnes / 16; i += kThreadsB)
     *reinterpret_cast<uint4*>(smem_raw + (ones_s - ptx::smem_addr(smem_raw)) + i * 16) =
         i < kRowsB ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   ptx::fence_proxy_async_smem();
   FAS_BWD_PROLOGUE();
-  const Blocks blk(p.table[f], BQ);
+  const Blocks blk(p.table[f], kBq);
 
   if (warp == kWarpK || warp == kWarpV) {
     if (lane == 0) {
@@ -611,10 +624,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         // Everything this CTA writes hangs on the statistics, so nothing of
         // it happens before the query pass has ended.
         ptx::grid_wait_previous();
-        produce<D, BQ, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
+        produce<D, kBq, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, BQ, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
+        produce<D, kBq, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -624,22 +637,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       };
       const uint64_t kdesc = ptx::smem_desc_sw128(k_s, 16, 1024), vdesc = ptx::smem_desc_sw128(v_s, 16, 1024);
       const uint64_t qd = ptx::smem_desc_sw128(q_s0, 16, 1024), dod = ptx::smem_desc_sw128(do_s0, 16, 1024);
-      const uint64_t qmn = ptx::smem_desc_sw128(q_s0, BQ * 128, 1024), domn = ptx::smem_desc_sw128(do_s0, BQ * 128, 1024);
-      const uint64_t ones = smem_desc_plain(ones_s, kRowsB * 16), stat = smem_desc_plain(stat_s0, 0);
-      constexpr uint64_t kStep = L::kBlock >> 4, kStatStep = L::kStat >> 4;
+      const uint64_t qmn = ptx::smem_desc_sw128(q_s0, kBq * 128, 1024), domn = ptx::smem_desc_sw128(do_s0, kBq * 128, 1024);
+      constexpr uint32_t kZeros = kRowsB * 16;
+      const uint64_t ones = smem_desc_plain(ones_s, kZeros);
+      constexpr uint64_t kStep = L::kBlock >> 4;
+      auto stat = [&](int st, int which) {
+        const uint32_t at = stat_s0 + st * L::kStat + which * (kBq * kStatBytes);
+        return smem_desc_plain(at, ones_s + kZeros - at);
+      };
       int qs = 0, qph = 0, ds = 0, dph = 0;  // ring positions of S's Q and dP's dO
       auto s_mma = [&](int n) {
         if (!wait(bars.full[0][qs], qph)) return false;
-        ptx::mma_ss(tmem + L::kS, ones, stat + qs * kStatStep, ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
-        mma_rows<D, BQ, kKT, true>(tmem + L::kS, tmem + L::kK, kdesc, qd + qs * kStep, n);
+        ptx::mma_ss(tmem + L::kS, ones, stat(qs, 0), ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
+        mma_rows<D, kBq, L::kKT, true>(tmem + L::kS, tmem + L::kK, kdesc, qd + qs * kStep, n);
         ptx::mma_commit(ptx::smem_addr(&bars.s_full));
         return true;
       };
       auto dp_mma = [&](int n) {  // the same block as the last s_mma
         if (!wait(bars.full[1][ds], dph)) return false;
-        ptx::mma_ss(tmem + L::kDp, ones, stat + qs * kStatStep + (BQ * kStatBytes >> 4),
-                    ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
-        mma_rows<D, BQ, kVT, true>(tmem + L::kDp, tmem + L::kV, vdesc, dod + ds * kStep, n);
+        ptx::mma_ss(tmem + L::kDp, ones, stat(qs, 1), ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
+        mma_rows<D, kBq, true, true>(tmem + L::kDp, tmem + L::kV, 0, dod + ds * kStep, n);
         ptx::mma_commit(ptx::smem_addr(&bars.dp_full));
         return true;
       };
@@ -652,8 +669,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       bool ok = wait(bars.tile_full, 0);
       int n = blk.count(0);
       if (ok) {
-        if (kKT) tile_to_tmem<D>(tmem + L::kK, kdesc);
-        if (kVT) tile_to_tmem<D>(tmem + L::kV, vdesc);
+        tile_to_tmem<D>(tmem + L::kV, vdesc);
+        if (L::kKT) tile_to_tmem<D>(tmem + L::kK, kdesc);
         ok = s_mma(n) && dp_mma(n);
       }
       for (int j = 0; ok && j < blk.nb; ++j) {
@@ -662,11 +679,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = wait(bars.p_full[0], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 16, 0>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        mma_acc<D, kBq, 16, 0>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
         ok = wait(bars.p_full[1], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 16, 1>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, false);
+        mma_acc<D, kBq, 16, 1>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, false);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
         next(qs, qph);
         next(ds, dph);
@@ -674,7 +691,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, BQ, 16, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
+        mma_acc<D, kBq, 16, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][st]));
         if (more) ok = dp_mma(n1);
         n = n1;
@@ -693,9 +710,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                                              p.limit_ns);
       return (bool)__all_sync(0xffffffffu, got);
     };
-    const float c = p.scale * kLog2eB;
-    static_assert(BQ % (16 * kSoftGroups) == 0, "");
-    constexpr int kCh = BQ / 16 / kSoftGroups;  // chunks of 16 columns per group
+    const float c = p.scale * core::kLog2e;
+    static_assert(kBq % (16 * kSoftGroups) == 0, "");
+    constexpr int kCh = kBq / 16 / kSoftGroups;  // chunks of 16 columns per group
     const uint32_t sbase = tmem + lane_base + L::kS + g * kCh * 16, dbase = tmem + lane_base + L::kDp + g * kCh * 16;
     bool ok = true;
     for (int j = 0; ok && j < blk.nb; ++j) {
@@ -717,7 +734,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           pk[e] = ptx::pack_bf16x2(pr[u][2 * e], pr[u][2 * e + 1]);
         }
         ptx::tmem_st8(sbase + u * 16, pk);
-        if (u == kFirstChunks<BQ> - 1 || u == kCh - 1) {
+        if (u == kFirstChunks<kBq> - 1 || u == kCh - 1) {
           ptx::tmem_st_wait();
           ptx::tc_fence_before_sync();
           ptx::mbar_arrive(ptx::smem_addr(&bars.p_full[u == kCh - 1]));
@@ -767,30 +784,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 
 #undef FAS_BWD_PROLOGUE
 
-#ifndef FAS_BWD_BQ
-#define FAS_BWD_BQ 96
-#endif
-#ifndef FAS_BWD_KT
-#define FAS_BWD_KT false
-#endif
-#ifndef FAS_BWD_VT
-#define FAS_BWD_VT true
-#endif
-
-// Queries per block of the key pass, and which operand tiles go to TMEM.
-template <int D>
-struct KConfig;
-template <>
-struct KConfig<128> {
-  static constexpr int kB = FAS_BWD_BQ;
-  static constexpr bool kKT = FAS_BWD_KT, kVT = FAS_BWD_VT;
-};
-template <>
-struct KConfig<64> {
-  static constexpr int kB = 96;
-  static constexpr bool kKT = true, kVT = true;
-};
-
 // Tensor map {d, N, H} with boxes of kBox tokens.
 int token_map(CUtensorMap* m, const void* base, int d, const BwdParams& p) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.N, (cuuint64_t)p.H};
@@ -801,15 +794,14 @@ int token_map(CUtensorMap* m, const void* base, int d, const BwdParams& p) {
 
 template <int D>
 int launch(const BwdParams& p, int grid, cudaStream_t st) {
-  using C = KConfig<D>;
   using LQ = QLayout<D>;
-  using LK = KLayout<D, C::kB, C::kKT, C::kVT>;
+  using LK = KLayout<D>;
   CUtensorMap tq, tdo, tk, tv;
   if (token_map(&tq, p.q, D, p) != FAS_OK || token_map(&tdo, p.dout, D, p) != FAS_OK ||
       token_map(&tk, p.k, D, p) != FAS_OK || token_map(&tv, p.v, D, p) != FAS_OK)
     return -1;
   auto kq = attention_bwd_q<D>;
-  auto kk = attention_bwd_k<D, C::kB, C::kKT, C::kVT>;
+  auto kk = attention_bwd_k<D>;
   if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LQ::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LK::kSmem) != cudaSuccess)
     return -1;

@@ -11,14 +11,22 @@
 //   Z_f = sum_{n in f} yh g               dgate_f    = alpha gamma_post Z_f
 //   dgamma_pre = sum_n dh xh              dgamma_post = sum_f alpha gate_f Z_f
 // so both gradients through the post norm need only the frames' sums Z_f.
+// Everything is fp32 but the stored results, which are rounded once.
 //
-// A row belongs to a group of W warps, eight columns (V times) a thread, so
-// a row's values stay in registers from its load to its stores, and the two
-// row sums are warp shuffles and one exchange through shared memory each.
-// Both kernels are bound by HBM.  Groups are persistent over consecutive
-// rows: gamma and gate stay in registers, and the next rows are on their way
+// A row belongs to a group of W warps, eight columns a vector and two vectors
+// a thread (one up to 1024 columns, four above 8192), so a row's values stay
+// in registers from its arrival to its stores, and a row sum is a warp
+// shuffle and one exchange through shared memory.  A group works through its
+// item's rows; gamma and gate stay with it, and the next rows are on their way
 // into a ring in shared memory.  Each thread copies just the bytes it will
-// read itself (cp.async), so the ring needs no barrier.
+// read itself (cp.async), so the ring needs no barrier.  (One vector a thread
+// and rows prefetched into registers: twice the instructions a row, 57 us
+// forward and 80 backward at 14,960 x 2048.)
+//
+// Bound by HBM: forward 41.5 us at 14,960 x 2048 bf16 (5.9 TB/s, 0.87 of the
+// measured copy rate), backward 59 us (6.2 TB/s, 0.91) and 7 for its sums;
+// 292 us (0.82) from 8-bit checkpoints at 79,200 x 2048, where decoding takes
+// issue slots; device time of captured calls.
 //
 // Backward: a group's rows never cross frames, so it adds its columns of Z
 // and of dgamma_pre in registers and writes one partial row of each at its
@@ -34,19 +42,15 @@
 #include "kernels.h"
 #include "vec8.cuh"
 
-#ifndef FAS_NORM_FWD
-#define FAS_NORM_FWD 4
-#endif
-#ifndef FAS_NORM_BWD
-#define FAS_NORM_BWD 3
-#endif
-
 namespace fas {
 namespace {
 
 constexpr int kMaxGroups = 4;   // row groups per CTA (named barriers 1 .. 4), and warps of a CTA unless a row needs more
 constexpr int kMaxWarps = 16;   // warps per row
-constexpr int kFwdPerSm = FAS_NORM_FWD, kBwdPerSm = FAS_NORM_BWD;  // CTAs of four warps per SM
+// CTAs of four warps per SM: what the registers allow without spilling (16
+// warps of 128, 12 of 168).  On 14,960 x 2048: forward 41.5 us with 4, 43 with
+// 3, 44 with 5; backward 66 with 3, 74 with 2, 173 with 4, which spills.
+constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
 
 // Sums over the W warps of the row group.  `slot` alternates, so that one
 // barrier a call is enough (a slot is written again two calls later).
@@ -157,11 +161,9 @@ __device__ __forceinline__ void load_param(const float* p, vec::P2 (&x)[4]) {
 }
 
 // Work items: each frame's rows are dealt out to its items in turn (item k of
-// n takes rows k, k + n, ...), so that the items of a frame read and write
-// neighbouring rows at any time.  (Consecutive rows per item spread the
-// accesses over as many far places as there are items, @@)
-// Frames of equal spans, or a table passed with the launch's arguments (no
-// device copy to keep alive).
+// n takes rows k, k + n, ...), so that the items of a frame work on
+// neighbouring rows at any time.  Frames of equal spans, or a table passed
+// with the launch's arguments (no device copy to keep alive).
 struct UniformItems {
   int64_t span;
   int per_frame;

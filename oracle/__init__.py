@@ -51,3 +51,4 @@ from .prologue import (  # noqa: F401
     qkv_prologue,
     prologue_flops,
 )
+from .training import attention_backward  # noqa: F401

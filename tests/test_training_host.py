@@ -59,6 +59,24 @@ def test_residual_norm_backward_reference_matches_differences(gated):
         assert abs((grad * u).sum() - diff) <= 1e-6 * (grad * u).abs().sum(), name
 
 
+@pytest.mark.parametrize("geo", [(48, 2, 1, 1), (16, 4, 0, 0), (32, 3, 2, 1)], ids=str)
+def test_oracle_attention_backward_matches_the_reference(geo):
+    """The oracle's row-by-row backward (NumPy, bf16 bits) against this
+    directory's batched one: the same numbers to 64-bit rounding."""
+    import oracle
+    T, F, R0, r = geo
+    g = torch.Generator().manual_seed(2)
+    h, n, d = 2, (F + R0) * T, 64
+    q, k, v, dout = (torch.randn(h, n, d, generator=g).bfloat16() for _ in range(4))
+    out, lse = ref.attention(q, k, v, [T] * (F + R0), R0, r)
+    out = out.bfloat16()
+    bits = lambda t: t.view(torch.int16).numpy().view(np.uint16)
+    got = oracle.attention_backward(bits(q), bits(k), bits(v), bits(out), lse.numpy(), bits(dout), T, R0, r)
+    want = ref.attention_backward(q, k, v, out, lse, dout, [T] * (F + R0), R0, r)
+    for name in ("dq", "dk", "dv"):
+        assert np.allclose(got[name], want[name][0].numpy(), rtol=1e-11, atol=1e-12), name
+
+
 def test_checkpoint_reference_is_nearest():
     """The search-based packing reference against torch's e4m3 conversion on
     scaled values, and its error bound: half a step, 2^-4 of the value or
@@ -96,7 +114,7 @@ def norm_call(**kw):
     (dict(tokens=0), fas.FAS_ERR_ARG), (dict(width=0), fas.FAS_ERR_ARG), (dict(width=12), fas.FAS_ERR_ARG),
     (dict(width=16392), fas.FAS_ERR_UNSUPPORTED), (dict(residual=2), fas.FAS_ERR_ARG), (dict(eps=-1.0), fas.FAS_ERR_ARG),
     (dict(eps=float("nan")), fas.FAS_ERR_ARG), (dict(y=None), fas.FAS_ERR_ARG), (dict(rstd=None), fas.FAS_ERR_ARG),
-    (dict(x=2 * A + 8), fas.FAS_ERR_ALIGN), (dict(yc=A), fas.FAS_ERR_ARG),
+    (dict(x=2 * A + 8), fas.FAS_ERR_ALIGN), (dict(yc=A), fas.FAS_ERR_ARG), (dict(h=5 * A), fas.FAS_ERR_ARG),
     (dict(yc=A, ys=A, xc=A, xs=A, width=72), fas.FAS_ERR_ARG),
     (dict(gate=A, frames=0), fas.FAS_ERR_ARG), (dict(gate=A, frames=3), fas.FAS_ERR_ARG),
     (dict(gate=A, frames=2, spans=[1, 2]), fas.FAS_ERR_ARG), (dict(gate=A, frames=2, spans=[4, 0]), fas.FAS_ERR_ARG),
@@ -120,7 +138,7 @@ def norm_bwd_call(**kw):
     (dict(gate=A), fas.FAS_ERR_ARG), (dict(dgate=A), fas.FAS_ERR_ARG), (dict(y=None), fas.FAS_ERR_ARG),
     (dict(yc=A, ys=A, xc=A, xs=A), fas.FAS_ERR_ARG), (dict(y=None, x_out=None, yc=A, ys=A, xc=A), fas.FAS_ERR_ARG),
     (dict(y=None, x_out=None, yc=A, ys=A, xc=A, xs=A, width=72), fas.FAS_ERR_ARG),
-    (dict(ws=None), fas.FAS_ERR_ARG), (dict(ws=12 * A + 8), fas.FAS_ERR_ALIGN), (dict(dgp=None), fas.FAS_ERR_ARG),
+    (dict(ws=None), fas.FAS_ERR_ARG), (dict(dy=8 * A), fas.FAS_ERR_ARG), (dict(ws=12 * A + 8), fas.FAS_ERR_ALIGN), (dict(dgp=None), fas.FAS_ERR_ARG),
 ])
 def test_residual_norm_backward_refuses(kw, code):
     assert norm_bwd_call(**kw) == code
