@@ -403,21 +403,25 @@ def _prologue(x, w_folded, cos, sin, heads, head_dim, layout, groups, ranks, q, 
     return (*outs, key_sums)
 
 
+# A small call's time is the host's: the checks below read each property once,
+# and the current stream's raw handle replaces its Stream object, which costs
+# more than a launch to build.
+
 def _check_here(name, t, shape, dtype, device: int) -> int:
     """_check_tensor, and that the tensor is on the current device (the
     kernels launch there).  Returns its address."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        _check_tensor(name, t, shape, dtype)
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor: told below
+    _check_tensor(name, t, shape, dtype)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
 def _current(name, t) -> Tuple[int, int]:
     """The current device and its current stream's handle, for a call on t."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     return _current_device_stream()
 
@@ -425,14 +429,13 @@ def _current(name, t) -> Tuple[int, int]:
 def _current_device_stream() -> Tuple[int, int]:
     import torch
     device = torch.cuda.current_device()
-    # The raw handle: building the Stream object costs more than a launch.
     return device, torch._C._cuda_getCurrentRawStream(device)
 
 
 def _output(name, t, like, device: int):
     """An output with like's type and shape, and its address."""
-    import torch
     if t is None:
+        import torch
         t = torch.empty_like(like)
         return t, t.data_ptr()
     return t, _check_here(name, t, like.shape, like.dtype, device)
@@ -559,14 +562,15 @@ def _norm_frames(tokens: int, width: int, gate, frame_tokens, device: int):
     import torch
     if gate is None:
         return None, None, 1
-    if gate.ndim != 2:
-        raise ValueError(f"gate must be [frames, width], got {tuple(gate.shape)}")
-    n = gate.shape[0]
+    n = gate.shape[0] if gate.ndim == 2 else 0
     ptr = _check_here("gate", gate, (n, width), torch.float32, device)
-    if frame_tokens is None or isinstance(frame_tokens, int) or np.ndim(frame_tokens) == 0:
-        span = tokens // n if frame_tokens is None and n else frame_tokens
-        if n * int(span or 0) != tokens:
-            raise ValueError(f"gate has {n} frames of {span} tokens; x has {tokens} tokens")
+    if frame_tokens is None:
+        if n == 0 or tokens % n:
+            raise ValueError(f"{tokens} tokens are not {n} equal frames (one per row of gate)")
+        return ptr, None, n
+    if isinstance(frame_tokens, int) or np.ndim(frame_tokens) == 0:
+        if n * int(frame_tokens) != tokens:
+            raise ValueError(f"gate has {n} frames of {frame_tokens} tokens; x has {tokens} tokens")
         return ptr, None, n
     spans = np.ascontiguousarray(frame_tokens, dtype=np.int32)
     if spans.ndim != 1 or len(spans) != n or int(spans.sum(dtype=np.int64)) != tokens:
@@ -607,12 +611,16 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
     x_out, px_out = _output("x_out", x_out, x, device)
     h, ph = _output("h", h, y, device)
     rstd = torch.empty((2, N), dtype=f32, device=x.device)
-    held = (_checkpoint_empty((N, C), x.device), _checkpoint_empty((N, C), x.device)) if checkpoint else ()
-    parts = [t for c in held for t in c]
+    held, parts, ptrs = (), (), (None, None, None, None)
+    if checkpoint:
+        held = _checkpoint_empty((N, C), x.device), _checkpoint_empty((N, C), x.device)
+        parts = (*held[0], *held[1])
+        ptrs = [t.data_ptr() for t in parts]
     rc = load().fas_residual_norm(py, px, residual, pgate, ppost, ppre, alpha, eps, N, C,
                                   None if spans is None else spans.ctypes.data, frames, px_out, ph, rstd.data_ptr(),
-                                  *([t.data_ptr() for t in parts] or (None,) * 4), _on(stream, current))
-    _check("fas_residual_norm", rc)
+                                  *ptrs, _on(stream, current))
+    if rc:
+        _check("fas_residual_norm", rc)
     if stream is not None:
         _own_until_run(stream, x_out, h, rstd, *parts)
     return (x_out, h, rstd, *held)
