@@ -562,7 +562,7 @@ def _norm_frames(tokens: int, width: int, gate, frame_tokens, device: int):
     import torch
     if gate is None:
         return None, None, 1
-    n = gate.shape[0] if gate.ndim == 2 else 0
+    n = gate.shape[0] if getattr(gate, "ndim", 0) == 2 else 0
     ptr = _check_here("gate", gate, (n, width), torch.float32, device)
     if frame_tokens is None:
         if n == 0 or tokens % n:

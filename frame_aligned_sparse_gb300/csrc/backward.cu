@@ -182,6 +182,7 @@ __device__ __forceinline__ void produce(BarsB& bars, int ring, const CUtensorMap
   bool ok = true;
   for (; j < blk.nb; ++j) {
     const int st = j % depth, u = j / depth;
+    if (j == depth) ptx::grid_wait_previous();  // a bounded wait must not count the previous kernel's time
     if (u >= 1)
       ok = ptx::mbar_wait<true>(ptx::smem_addr(&bars.empty[ring][st]), (u - 1) & 1, abort_flag, p.err,
                                 kErrWaitProducer, p.limit_ns);
@@ -258,7 +259,10 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 #define FAS_BWD_PROLOGUE()                                                                          \
   if (threadIdx.x == 0) bars.skip = *reinterpret_cast<volatile unsigned int*>(p.err) != 0u;          \
   __syncthreads();                                                                                   \
-  if (bars.skip) return;                                                                             \
+  if (bars.skip) {                                                                                   \
+    ptx::grid_wait_previous(); /* what follows this kernel must also follow the one before */       \
+    return;                                                                                          \
+  }                                                                                                  \
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;                                        \
   const int4 item = p.work[blockIdx.x];                                                              \
   const int h = item.x, f = item.y, tile = item.z;                                                   \
@@ -621,8 +625,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
         load_rows<D, kRowsB>(k_s, &tm_k, tb, sp.x + tile * kRowsB, h);
         load_rows<D, kRowsB>(v_s, &tm_v, tb, sp.x + tile * kRowsB, h);
-        // Everything this CTA writes hangs on the statistics, so nothing of
-        // it happens before the query pass has ended.
+        // The statistics, and so everything this CTA writes, come after the
+        // query pass.  (The other roles wait for its end too before their
+        // first bounded wait that hangs on it.)
         ptx::grid_wait_previous();
         produce<D, kBq, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
@@ -671,6 +676,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (ok) {
         tile_to_tmem<D>(tmem + L::kV, vdesc);
         if (L::kKT) tile_to_tmem<D>(tmem + L::kK, kdesc);
+        ptx::grid_wait_previous();
         ok = s_mma(n) && dp_mma(n);
       }
       for (int j = 0; ok && j < blk.nb; ++j) {
@@ -710,6 +716,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                                              p.limit_ns);
       return (bool)__all_sync(0xffffffffu, got);
     };
+    ptx::grid_wait_previous();
     const float c = p.scale * core::kLog2e;
     static_assert(kBq % (16 * kSoftGroups) == 0, "");
     constexpr int kCh = kBq / 16 / kSoftGroups;  // chunks of 16 columns per group

@@ -433,7 +433,8 @@ def test_residual_norm_zero_rows():
 def test_norm_binding_refuses():
     c = Norm([4, 4], 64, torch.bfloat16, True)
     call = lambda **kw: fas.fas_residual_norm(c.y, c.x, c.post, c.pre, **{**c.kw, **kw})
-    for kw, exc in ((dict(gate=c.gate[:, :32]), ValueError), (dict(gate=c.gate.half()), TypeError), (dict(frame_tokens=3), ValueError),
+    for kw, exc in ((dict(gate=c.gate[:, :32]), ValueError), (dict(gate=[1.0]), TypeError), (dict(gate=c.gate[0]), ValueError),
+                    (dict(gate=c.gate.cpu()), TypeError), (dict(gate=c.gate.half()), TypeError), (dict(frame_tokens=3), ValueError),
                     (dict(frame_tokens=[4, 3]), ValueError), (dict(frame_tokens=[8]), ValueError), (dict(x_out=c.x[:4]), ValueError),
                     (dict(h=c.x.float()), TypeError), (dict(frame_tokens=[8, 0]), fas.FasError), (dict(eps=-1.0), fas.FasError)):
         with pytest.raises(exc):
