@@ -23,7 +23,7 @@
 // with 6 heads takes 11.9 ms, 1.18 PFLOP/s of the five products and 1.65 of
 // the seven executed, 0.97 of the rate that the library's bf16 product
 // sustains (1.70); at d = 64 the exponentials and their conversions bound it
-// (0.73 PFLOP/s of five).
+// (0.80 PFLOP/s of five on the mid geometry, 0.89 on the 720p one).
 //
 // A visible range is walked in blocks; its last block is shortened to the
 // tokens it has (a multiple of 16) through the MMA's N or its K steps, so no
@@ -159,14 +159,15 @@ __device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float 
 // blocks of every size).  A tile's rows past the frame's end are the next
 // frame's (or zeros past the last token): every row of a tile is computed by
 // itself, and those are never stored.
-constexpr int kBox = 32;
+template <int D>
+constexpr int kBox = D == 64 ? 16 : 32;
 template <int D, int kRows>
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int first, int h) {
-  static_assert(kRows % kBox == 0, "");
+  static_assert(kRows % kBox<D> == 0, "");
 #pragma unroll
   for (int half = 0; half < D / 64; ++half)
 #pragma unroll
-    for (int r = 0; r < kRows; r += kBox)
+    for (int r = 0; r < kRows; r += kBox<D>)
       ptx::tma_load_3d(dst + half * (kRows * 128) + r * 128, tm, bar, half * 64, first + r, h);
 }
 
@@ -281,23 +282,26 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 // ------------------------------------------------------------- query pass
 //
 // Q and dO of the tile sit in TMEM as A operands; K and V blocks of 96 keys
-// stream through two rings.  The warpgroups work on the same block, and
+// (144 at d = 64) stream through two rings.  The warpgroups work on the same block, and
 // dS has its own place in TMEM, so S(j+1) only needs
 // S(j) to have been read into registers, dP(j+1) the same of dP(j), and the
 // tensor pipe runs S(j+1), dP(j+1) while block j is exponentiated.  Tensor
 // order: S(j+1), dP(j+1), dQ(j).
 //
-// 96 keys: S, dP (fp32) and dS (bf16) take 240 columns beside dq, Q and dO.
+// 96 keys: S, dP (fp32) and dS (bf16) take 240 columns beside dq, Q and dO; at
+// d = 64 there is room for 144, and the softmax warps, which bound it, pay
+// their waits less often (8.8 -> 8.0 ms on 6 heads x 22 x 3600, both passes).
 // Blocks of 128 with dS in dP's columns chain dS(j), dQ(j), dP(j+1) and left
 // the pipe 57% busy; blocks of 64 in two buffers, 52% (an MMA of N = 64 takes
 // 32 clocks, less than the issue of the next).
-constexpr int kBk = 96;  // keys per block
+template <int D>
+constexpr int kBk = D == 64 ? 144 : 96;  // keys per block
 
 template <int D>
 struct QLayout {
-  static constexpr uint32_t kAcc = 0, kS = D, kDp = kS + kBk, kDs = kDp + kBk, kQ = kDs + kBk / 2, kDo = kQ + D / 2;
+  static constexpr uint32_t kAcc = 0, kS = D, kDp = kS + kBk<D>, kDs = kDp + kBk<D>, kQ = kDs + kBk<D> / 2, kDo = kQ + D / 2;
   static_assert(kDo + D / 2 <= kTmemAll, "TMEM columns");
-  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBk * D * 2;
+  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBk<D> * D * 2;
   static constexpr int kStages = 3;  // per ring
   static constexpr size_t kSmem = 1024 + 2 * kTile + 2 * kStages * kBlock;
 };
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const uint32_t k_s0 = do_s + L::kTile, v_s0 = k_s0 + S * L::kBlock;
   ptx::grid_launch_next();
   FAS_BWD_PROLOGUE();
-  const Blocks blk(p.table[f], kBk);
+  const Blocks blk(p.table[f], kBk<D>);
 
   if (warp == kWarpK || warp == kWarpV) {
     if (lane == 0) {
@@ -326,10 +330,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ptx::mbar_arrive_expect_tx(tb, 2 * L::kTile);
         load_rows<D, kRowsB>(q_s, &tm_q, tb, sp.x + tile * kRowsB, h);
         load_rows<D, kRowsB>(do_s, &tm_do, tb, sp.x + tile * kRowsB, h);
-        produce<D, kBk, false>(bars, 0, &tm_k, S, k_s0, h, blk, p, 0);
+        produce<D, kBk<D>, false>(bars, 0, &tm_k, S, k_s0, h, blk, p, 0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, kBk, false>(bars, 1, &tm_v, S, v_s0, h, blk, p, 0);
+        produce<D, kBk<D>, false>(bars, 1, &tm_v, S, v_s0, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -338,12 +342,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         return ptx::mbar_wait<false>(ptx::smem_addr(&b), parity & 1, abort_flag, p.err, kErrWaitMma, p.limit_ns);
       };
       const uint64_t kd = ptx::smem_desc_sw128(k_s0, 16, 1024), vd = ptx::smem_desc_sw128(v_s0, 16, 1024);
-      const uint64_t kmn = ptx::smem_desc_sw128(k_s0, kBk * 128, 1024);
+      const uint64_t kmn = ptx::smem_desc_sw128(k_s0, kBk<D> * 128, 1024);
       constexpr uint64_t kStep = L::kBlock >> 4;
       int ks = 0, kph = 0, vs = 0, vph = 0, os = 0;  // ring positions: S's K, dP's V, dQ's K
       auto s_mma = [&](int n) {
         if (!wait(bars.full[0][ks], kph)) return false;
-        mma_rows<D, kBk, true>(tmem + L::kS, tmem + L::kQ, 0, kd + ks * kStep, n);
+        mma_rows<D, kBk<D>, true>(tmem + L::kS, tmem + L::kQ, 0, kd + ks * kStep, n);
         ptx::mma_commit(ptx::smem_addr(&bars.s_full));
         if (++ks == S) {
           ks = 0;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       };
       auto dp_mma = [&](int n) {
         if (!wait(bars.full[1][vs], vph)) return false;
-        mma_rows<D, kBk, true>(tmem + L::kDp, tmem + L::kDo, 0, vd + vs * kStep, n);
+        mma_rows<D, kBk<D>, true>(tmem + L::kDp, tmem + L::kDo, 0, vd + vs * kStep, n);
         ptx::mma_commit(ptx::smem_addr(&bars.dp_full));
         ptx::mma_commit(ptx::smem_addr(&bars.empty[1][vs]));
         if (++vs == S) {
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBk, 8, 2>(tmem + L::kAcc, tmem + L::kDs, kmn + os * kStep, n, j == 0);
+        mma_acc<D, kBk<D>, 8, 2>(tmem + L::kAcc, tmem + L::kDs, kmn + os * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.acc_done));
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][os]));
         if (++os == S) os = 0;
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const float nd = -delta;
     const uint64_t minus1 = ptx::f32x2(-1.f, -1.f);
     float e0 = 0.f, e1 = 0.f;  // what rounding dS to bf16 added to the row
-    constexpr int kCh = kBk / 16 / kSoftGroups;  // chunks of 16 columns per group
+    constexpr int kCh = kBk<D> / 16 / kSoftGroups;  // chunks of 16 columns per group
     const uint32_t sbase = tmem + lane_base + L::kS + g * kCh * 16, dbase = tmem + lane_base + L::kDp + g * kCh * 16;
     const uint32_t dst = tmem + lane_base + L::kDs + g * kCh * 8;
     for (int j = 0; ok && j < blk.nb; ++j) {
@@ -583,16 +587,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // (Read
 // from shared memory as vectors per column, they took 30% of its cycles, which
 // the MMAs' operands need.)
-constexpr int kBq = 96;  // queries per block
+template <int D>
+constexpr int kBq = D == 64 ? 144 : 96;  // queries per block
 
 template <int D>
 struct KLayout {
   // V's A operand is in TMEM; K's too where there is room (d = 64).
   static constexpr bool kKT = D == 64;
-  static constexpr uint32_t kDk = 0, kDv = D, kS = 2 * D, kDp = kS + kBq, kV = kDp + kBq, kK = kV + D / 2;
+  static constexpr uint32_t kDk = 0, kDv = D, kS = 2 * D, kDp = kS + kBq<D>, kV = kDp + kBq<D>, kK = kV + D / 2;
   static_assert(kK + (kKT ? D / 2 : 0) <= kTmemAll, "TMEM columns");
-  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBq * D * 2;
-  static constexpr uint32_t kStat = 2 * kBq * kStatBytes, kOnes = 2 * kRowsB * 16;  // ones (16 columns), a stage's statistics
+  static constexpr uint32_t kTile = kRowsB * D * 2, kBlock = kBq<D> * D * 2;
+  static constexpr uint32_t kStat = 2 * kBq<D> * kStatBytes;  // a stage's statistics
+  // Ones for A's rows, then zeros for the rows of A and of B (columns 8 .. 15).
+  static constexpr uint32_t kOneRows = kRowsB, kZeroRows = kBq<D> > kRowsB ? kBq<D> : kRowsB;
+  static constexpr uint32_t kOnes = (kOneRows + kZeroRows) * 16;
   static constexpr int kFit = (int)((232448 - 1024 - 512 - kOnes - 2 * kTile) / (2 * kBlock + kStat));
   static constexpr int kStages = kFit < kMaxStagesB ? kFit : kMaxStagesB;
   static constexpr size_t kSmem = 1024 + kOnes + 2 * kTile + kStages * (2 * kBlock + kStat);
@@ -609,14 +617,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const uint32_t k_s = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t v_s = k_s + L::kTile, q_s0 = v_s + L::kTile, do_s0 = q_s0 + L::kStages * L::kBlock;
   const uint32_t stat_s0 = do_s0 + L::kStages * L::kBlock, ones_s = stat_s0 + L::kStages * L::kStat;
-  // The ones: 128 rows of {1, 1, 1, 0, 0, 0, 0, 0}, then 128 rows of zeros,
-  // which are columns 8 .. 15 of both operands of the statistics' K step.
+  // The ones: rows of {1, 1, 1, 0, 0, 0, 0, 0}, then rows of zeros, which are
+  // columns 8 .. 15 of both operands of the statistics' K step.
   for (uint32_t i = threadIdx.x; i < L::kOnes / 16; i += kThreadsB)
     *reinterpret_cast<uint4*>(smem_raw + (ones_s - ptx::smem_addr(smem_raw)) + i * 16) =
-        i < kRowsB ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+        i < L::kOneRows ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   ptx::fence_proxy_async_smem();
   FAS_BWD_PROLOGUE();
-  const Blocks blk(p.table[f], kBq);
+  const Blocks blk(p.table[f], kBq<D>);
 
   if (warp == kWarpK || warp == kWarpV) {
     if (lane == 0) {
@@ -629,10 +637,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         // query pass.  (The other roles wait for its end too before their
         // first bounded wait that hangs on it.)
         ptx::grid_wait_previous();
-        produce<D, kBq, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
+        produce<D, kBq<D>, true>(bars, 0, &tm_q, L::kStages, q_s0, h, blk, p, stat_s0);
         if (bars.abort) drain_wait(tb, 0, p.err, p.limit_ns);
       } else {
-        produce<D, kBq, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
+        produce<D, kBq<D>, false>(bars, 1, &tm_do, L::kStages, do_s0, h, blk, p, 0);
       }
     }
   } else if (warp == kWarpMma) {
@@ -642,26 +650,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       };
       const uint64_t kdesc = ptx::smem_desc_sw128(k_s, 16, 1024), vdesc = ptx::smem_desc_sw128(v_s, 16, 1024);
       const uint64_t qd = ptx::smem_desc_sw128(q_s0, 16, 1024), dod = ptx::smem_desc_sw128(do_s0, 16, 1024);
-      const uint64_t qmn = ptx::smem_desc_sw128(q_s0, kBq * 128, 1024), domn = ptx::smem_desc_sw128(do_s0, kBq * 128, 1024);
-      constexpr uint32_t kZeros = kRowsB * 16;
+      const uint64_t qmn = ptx::smem_desc_sw128(q_s0, kBq<D> * 128, 1024), domn = ptx::smem_desc_sw128(do_s0, kBq<D> * 128, 1024);
+      constexpr uint32_t kZeros = L::kOneRows * 16;
       const uint64_t ones = smem_desc_plain(ones_s, kZeros);
       constexpr uint64_t kStep = L::kBlock >> 4;
       auto stat = [&](int st, int which) {
-        const uint32_t at = stat_s0 + st * L::kStat + which * (kBq * kStatBytes);
+        const uint32_t at = stat_s0 + st * L::kStat + which * (kBq<D> * kStatBytes);
         return smem_desc_plain(at, ones_s + kZeros - at);
       };
       int qs = 0, qph = 0, ds = 0, dph = 0;  // ring positions of S's Q and dP's dO
       auto s_mma = [&](int n) {
         if (!wait(bars.full[0][qs], qph)) return false;
         ptx::mma_ss(tmem + L::kS, ones, stat(qs, 0), ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
-        mma_rows<D, kBq, L::kKT, true>(tmem + L::kS, tmem + L::kK, kdesc, qd + qs * kStep, n);
+        mma_rows<D, kBq<D>, L::kKT, true>(tmem + L::kS, tmem + L::kK, kdesc, qd + qs * kStep, n);
         ptx::mma_commit(ptx::smem_addr(&bars.s_full));
         return true;
       };
       auto dp_mma = [&](int n) {  // the same block as the last s_mma
         if (!wait(bars.full[1][ds], dph)) return false;
         ptx::mma_ss(tmem + L::kDp, ones, stat(qs, 1), ptx::idesc_bf16_f32(kRowsB, (uint32_t)n, false), 0u);
-        mma_rows<D, kBq, true, true>(tmem + L::kDp, tmem + L::kV, 0, dod + ds * kStep, n);
+        mma_rows<D, kBq<D>, true, true>(tmem + L::kDp, tmem + L::kV, 0, dod + ds * kStep, n);
         ptx::mma_commit(ptx::smem_addr(&bars.dp_full));
         return true;
       };
@@ -685,11 +693,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = wait(bars.p_full[0], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBq, 16, 0>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
+        mma_acc<D, kBq<D>, 16, 0>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, j == 0);
         ok = wait(bars.p_full[1], j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBq, 16, 1>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, false);
+        mma_acc<D, kBq<D>, 16, 1>(tmem + L::kDv, tmem + L::kS, domn + st * kStep, n, false);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[1][st]));
         next(qs, qph);
         next(ds, dph);
@@ -697,7 +705,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         ok = ok && wait(bars.ds_full, j);
         if (!ok) break;
         ptx::tc_fence_after_sync();
-        mma_acc<D, kBq, 16, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
+        mma_acc<D, kBq<D>, 16, 2>(tmem + L::kDk, tmem + L::kDp, qmn + st * kStep, n, j == 0);
         ptx::mma_commit(ptx::smem_addr(&bars.empty[0][st]));
         if (more) ok = dp_mma(n1);
         n = n1;
@@ -718,8 +726,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     };
     ptx::grid_wait_previous();
     const float c = p.scale * core::kLog2e;
-    static_assert(kBq % (16 * kSoftGroups) == 0, "");
-    constexpr int kCh = kBq / 16 / kSoftGroups;  // chunks of 16 columns per group
+    static_assert(kBq<D> % (16 * kSoftGroups) == 0, "");
+    constexpr int kCh = kBq<D> / 16 / kSoftGroups;  // chunks of 16 columns per group
     const uint32_t sbase = tmem + lane_base + L::kS + g * kCh * 16, dbase = tmem + lane_base + L::kDp + g * kCh * 16;
     bool ok = true;
     for (int j = 0; ok && j < blk.nb; ++j) {
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           pk[e] = ptx::pack_bf16x2(pr[u][2 * e], pr[u][2 * e + 1]);
         }
         ptx::tmem_st8(sbase + u * 16, pk);
-        if (u == kFirstChunks<kBq> - 1 || u == kCh - 1) {
+        if (u == kFirstChunks<kBq<D>> - 1 || u == kCh - 1) {
           ptx::tmem_st_wait();
           ptx::tc_fence_before_sync();
           ptx::mbar_arrive(ptx::smem_addr(&bars.p_full[u == kCh - 1]));
@@ -795,7 +803,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 int token_map(CUtensorMap* m, const void* base, int d, const BwdParams& p) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.N, (cuuint64_t)p.H};
   const cuuint64_t strides[2] = {(cuuint64_t)p.row_stride * 2, (cuuint64_t)p.head_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)kBox, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(d == 64 ? kBox<64> : kBox<128>), 1};
   return bf16_tensor_map(m, base, 3, dims, strides, box);
 }
 
