@@ -282,11 +282,11 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, uint16_t* dst, float s
 // ------------------------------------------------------------- query pass
 //
 // Q and dO of the tile sit in TMEM as A operands; K and V blocks of 96 keys
-// (144 at d = 64) stream through two rings.  The warpgroups work on the same block, and
-// dS has its own place in TMEM, so S(j+1) only needs
-// S(j) to have been read into registers, dP(j+1) the same of dP(j), and the
-// tensor pipe runs S(j+1), dP(j+1) while block j is exponentiated.  Tensor
-// order: S(j+1), dP(j+1), dQ(j).
+// (144 at d = 64) stream through two rings.  The warpgroups work on the same
+// block, and dS has its own place in TMEM, so S(j+1) only needs S(j) to have
+// been read into registers, dP(j+1) the same of dP(j), and the tensor pipe runs
+// S(j+1), dP(j+1) while block j is exponentiated.  Tensor order: S(j+1),
+// dP(j+1), dQ(j).
 //
 // 96 keys: S, dP (fp32) and dS (bf16) take 240 columns beside dq, Q and dO; at
 // d = 64 there is room for 144, and the softmax warps, which bound it, pay
@@ -574,19 +574,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // V.dO^T with the tile's K and V as A operands and blocks of Q and dO as B;
 // P^T and dS^T then are the A operands of dv += P^T.dO and dk += dS^T.Q, whose
 // B operands are the same Q and dO blocks read along their rows.  The two
-// accumulators and one S^T and dP^T buffer each fill TMEM; the
-// warpgroups work on the same block.  Tensor order: dV(j),
-// S(j+1), dK(j), dP(j+1): P(j+1) is computed under dK(j) and dP(j+1), dS(j)
-// under dV(j) and S(j+1).
+// accumulators and one S^T and dP^T buffer each fill TMEM; the warpgroups work
+// on the same block.  Tensor order: dV(j), S(j+1), dK(j), dP(j+1): P(j+1) is
+// computed under dK(j) and dP(j+1), dS(j) under dV(j) and S(j+1).  P is
+// released in two parts, so that dV(j) starts on the first.
 //
 // The softmax statistics differ by column here.  They enter through the MMA:
 // one more K step of 16 whose A operand holds ones in three columns and whose
 // B operand holds -lse / s (for S^T) or -delta (for dP^T) split into three
 // bf16 values a query, so the accumulators come out as S^T - lse / s and dP^T
-// - delta.  P is released in two parts, so that dV(j) starts on the first.
-// (Read
-// from shared memory as vectors per column, they took 30% of its cycles, which
-// the MMAs' operands need.)
+// - delta.  (Read from shared memory as vectors per column, they took 30% of
+// its cycles, which the MMAs' operands need.)
+//
+// 96 queries: 144 at d = 64, as in the query pass; at d = 128, 64 with both
+// tiles in TMEM and 128 with both in shared memory measured within 1%.
 template <int D>
 constexpr int kBq = D == 64 ? 144 : 96;  // queries per block
 
