@@ -13,8 +13,8 @@
 // so both gradients through the post norm need only the frames' sums Z_f.
 // Everything is fp32 but the stored results, which are rounded once.
 //
-// A row belongs to a group of W warps, eight columns a vector and two vectors
-// a thread (one up to 1024 columns, four above 8192), so a row's values stay
+// A row belongs to a group of W warps, eight columns a vector and one or two
+// vectors a thread (four above 8192 columns), so a row's values stay
 // in registers from its arrival to its stores, and a row sum is a warp
 // shuffle and one exchange through shared memory.  A group works through its
 // item's rows; gamma and gate stay with it, and the next rows are on their way
@@ -98,22 +98,27 @@ __device__ __forceinline__ void clear_exchange(Exchange<N> (&ex)[kMaxGroups]) {
 }
 
 // Stages of a row ring.  Rows of at most four warps: two (forward) or three
-// (backward) cover HBM's latency with the CTAs that fit; wider rows: what
-// shared memory holds (V = 4: 16,384 columns, 192 KB a stage in the fp32
-// backward).
-template <int V, bool kWide>
+// (backward) cover HBM's latency with the CTAs that fit; wider rows in the
+// backward: what shared memory holds beside what else the threads keep there.
+template <int V>
 constexpr int kRingFwd = V == 4 ? 1 : 2;
-template <class R, int V, bool kWide>
-constexpr int kRingBwd = !kWide ? (sizeof(R) == 16 ? 3 : 2) : V == 2 && sizeof(R) == 16 ? 2 : 1;
+template <int V, bool kWide>
+constexpr int kKeptPieces = (V == 2 ? 4 : 0) + (V == 2 && kWide ? 4 : 0);  // 16 bytes a vector: Params, Sums
+template <int V, bool kWide, int kVec, bool kF32>
+__host__ __device__ constexpr int ring_bwd() {
+  if (!kWide) return kF32 ? 2 : 3;
+  const int fit = (232448 - 2048 - 512 * 16 * V * kKeptPieces<V, kWide>) / (512 * 16 * V * kVec);
+  return fit < 1 ? 1 : fit < 4 ? fit : 4;
+}
 
 // Asynchronous copies of this thread's bytes into its own shared memory.
-template <int kBytes>
+// kL1: the other half of the sector is asked for next, so it goes by L1.
+template <int kBytes, bool kL1 = kBytes == 8>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  static_assert(kBytes == 8 || kBytes == 16, "");
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  if constexpr (kL1)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -135,7 +140,7 @@ struct RingPos {
 template <class X>
 __device__ __forceinline__ void ring_load(uint32_t dst, uint32_t step, const uint8_t* src) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(X) / 16; ++i) copy_async<16>(dst + i * step, src + i * 16);
+  for (int i = 0; i < (int)sizeof(X) / 16; ++i) copy_async<16, sizeof(X) == 32>(dst + i * step, src + i * 16);
 }
 __device__ __forceinline__ uint4 ring_piece(uint32_t addr) {
   uint4 v;
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
   const int64_t row_step = (int64_t)stride * C;  // elements between the item's rows
   const float inv_c = 1.0f / (float)C;
   extern __shared__ uint4 ring[];
-  constexpr int S = kRingFwd<V, kWide>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
+  constexpr int S = kRingFwd<V>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   bool in[V];
   int col[V];
@@ -420,6 +425,58 @@ struct Params {
   }
 };
 
+// The two column sums of a thread's columns: in registers, or (V = 2 in rows
+// of more than four warps, 128 registers a thread) in shared memory.
+template <int V, bool kSmem>
+struct Sums {
+  vec::P2 z_[kSmem ? 1 : V][4], d_[kSmem ? 1 : V][4];
+  uint32_t at, step;
+  __device__ __forceinline__ uint32_t piece(int v, int i) const { return at + (v * 4 + i) * step; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (kSmem) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v2.u64 [%0], {%1, %1};" ::"r"(piece(v, i)), "l"(0ull) : "memory");
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z_[v][e] = d_[v][e] = vec::both(0.f);
+      }
+    }
+  }
+  // The sums' four pairs (which: 0 Z, 1 dgamma_pre) += a * b.
+  template <int kWhich>
+  __device__ __forceinline__ void add(int v, const vec::P2 (&a)[4], const vec::P2 (&b)[4]) {
+    if constexpr (kSmem) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        vec::P2 s0, s1;
+        const uint32_t p = piece(v, kWhich * 2 + i);
+        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(s0.v), "=l"(s1.v) : "r"(p));
+        s0 = vec::fma2(a[2 * i], b[2 * i], s0);
+        s1 = vec::fma2(a[2 * i + 1], b[2 * i + 1], s1);
+        asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(p), "l"(s0.v), "l"(s1.v) : "memory");
+      }
+    } else {
+      vec::P2(&s)[4] = kWhich ? d_[v] : z_[v];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = vec::fma2(a[e], b[e], s[e]);
+    }
+  }
+  template <int kWhich>
+  __device__ __forceinline__ void get(int v, vec::P2 (&s)[4]) const {
+    if constexpr (kSmem) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(s[2 * i].v), "=l"(s[2 * i + 1].v) : "r"(piece(v, kWhich * 2 + i)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = kWhich ? d_[v][e] : z_[v][e];
+    }
+  }
+};
+
 // Both row means come from one exchange: with t = dx' + r_x a (g = t - r_x xh
 // m1), sum(b yh) = sum(coef yh t) - r_x m1 sum(coef yh xh), coef = alpha gate
 // gamma_post, so the three sums of a xh, coef yh t and coef yh xh give both.
@@ -443,7 +500,8 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
   const int64_t row_step = (int64_t)stride * C;  // elements between the item's rows
   extern __shared__ uint4 ring[];
   using H = Held<R, k8>;
-  constexpr int S = kRingBwd<R, V, kWide>, kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
+  constexpr int kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
+  constexpr int S = ring_bwd<V, kWide, kVec, sizeof(R) == 32>();
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   int col[V];
   bool in[V];
@@ -507,15 +565,16 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
   load_small(0, small[0]);
   load_small(1, small[1]);
   const P2 zero = both(0.f);
-  P2 z[V][4], dg[V][4];
   Params<V> params;
   params.at = base + S * V * kVec * step;
   params.step = step;
+  Sums<V, V == 2 && kWide> sums;
+  sums.at = params.at + V * Params<V>::kPieces * step;
+  sums.step = step;
+  sums.clear();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     P2 c[4] = {zero, zero, zero, zero}, g[4] = {zero, zero, zero, zero};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z[v][e] = dg[v][e] = zero;
     if (in[v]) {
       load_param(a.gamma_post + col[v], c);
       load_param(a.gamma_pre + col[v], g);
@@ -550,7 +609,6 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
       for (int e = 0; e < 4; ++e) {
         y[v][e] = mul2(y[v][e], ry2);
         x[v][e] = mul2(x[v][e], rx2);
-        dg[v][e] = fma2(h[e], x[v][e], dg[v][e]);
         const P2 ah = mul2(h[e], gpre[e]);
         sa = fma2(ah, x[v][e], sa);
         t[v][e] = fma2(rx2, ah, t[v][e]);
@@ -558,6 +616,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
         sb = fma2(cy, t[v][e], sb);
         sc = fma2(cy, x[v][e], sc);
       }
+      sums.template add<1>(v, h, x[v]);
     }
     rd.next();
     load();
@@ -573,9 +632,9 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         t[v][e] = fma2(nrm1, x[v][e], t[v][e]);  // g
-        z[v][e] = fma2(y[v][e], t[v][e], z[v][e]);
         d[e] = mul2(ry2, fma2(nm2, y[v][e], mul2(coef[e], t[v][e])));
       }
+      sums.template add<0>(v, y[v], t[v]);
       Bf16 dv;
       R ov;
       dv.set(d);
@@ -596,9 +655,12 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
   for (int v = 0; v < V; ++v)
     if (in[v]) {
       F32 o;
-      o.set(z[v]);
+      P2 s[4];
+      sums.template get<0>(v, s);
+      o.set(s);
       o.store(a.z_part, item * C + col[v]);
-      o.set(dg[v]);
+      sums.template get<1>(v, s);
+      o.set(s);
       o.store(a.d_part, item * C + col[v]);
     }
 }
@@ -677,13 +739,20 @@ __global__ void __launch_bounds__(kSumThreads)
   }
 }
 
-// Warps per row and vectors per thread for a width.
+
 struct Shape {
   int V, W, G;
 };
-Shape shape_of(int width) {
-  const int vecs = width / 8;
-  const int V = vecs <= 32 * kMaxGroups ? 1 : vecs <= 64 * kMaxWarps ? 2 : 4;
+// One or two vectors a thread in at most four warps (128 threads, whose
+// registers the launch bounds fix); above that the forward takes two vectors
+// a thread, the backward one while sixteen warps are enough (at two its sums
+// no longer fit in registers), and both four above 8192 columns.
+Shape shape_of(int width, bool backward) {
+  const int vecs = width / 8, most = 32 * kMaxWarps;
+  const int V = vecs <= 32 * kMaxGroups ? 1
+                : vecs <= 64 * kMaxGroups ? 2
+                : backward && vecs <= most ? 1
+                : vecs <= 2 * most ? 2 : 4;
   const int W = (vecs + 32 * V - 1) / (32 * V);
   return {V, W, std::max(1, kMaxGroups / W)};
 }
@@ -704,7 +773,7 @@ cudaError_t allow_ring(K kern, size_t smem, bool many) {
 template <class R, int V, bool kCkpt, bool kWide, class Items>
 cudaError_t fwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
   auto kern = residual_norm_fwd<R, V, kCkpt, kWide, Items>;
-  const size_t smem = (size_t)32 * s.W * s.G * kRingFwd<V, kWide> * V * (16 + sizeof(R));
+  const size_t smem = (size_t)32 * s.W * s.G * kRingFwd<V> * V * (16 + sizeof(R));
   const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
@@ -729,8 +798,9 @@ cudaError_t fwd_all(const NormArgs& a, const Items& it, const Shape& s, cudaStre
 template <class R, int V, bool k8, bool kWide, class Items>
 cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
   auto kern = residual_norm_bwd<R, V, k8, kWide, Items>;
+  constexpr int kVec = sizeof(R) / 16 + 1 + Held<R, k8>::kPieces;
   const size_t smem = (size_t)32 * s.W * s.G * V * 16 *
-                      (kRingBwd<R, V, kWide> * (sizeof(R) / 16 + 1 + Held<R, k8>::kPieces) + Params<V>::kPieces);
+                      (ring_bwd<V, kWide, kVec, sizeof(R) == 32>() * kVec + kKeptPieces<V, kWide>);
   const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
@@ -738,8 +808,7 @@ cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t
 }
 template <class R, int V, class Items>
 cudaError_t bwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  if constexpr (V >= 2)
-    if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true>(a, it, s, st) : bwd<R, V, false, true>(a, it, s, st);
+  if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true>(a, it, s, st) : bwd<R, V, false, true>(a, it, s, st);
   if constexpr (V <= 2) return a.y8 ? bwd<R, V, true, false>(a, it, s, st) : bwd<R, V, false, false>(a, it, s, st);
   return cudaErrorInvalidValue;  // V = 4 has more warps
 }
@@ -808,7 +877,7 @@ cudaError_t with_items(const NormItems& n, const int32_t* spans, int n_frames, i
 
 cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
                                  cudaStream_t st) {
-  const Shape s = shape_of(a.width);
+  const Shape s = shape_of(a.width, false);
   const NormItems n = split(a.rows, s, spans, n_frames, span, sms, kFwdPerSm);
   a.warps = s.W;
   a.groups = s.G;
@@ -818,14 +887,14 @@ cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames,
 }
 
 NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms) {
-  NormItems r = split(rows, shape_of(width), spans, n_frames, span, sms, kBwdPerSm);
+  NormItems r = split(rows, shape_of(width, true), spans, n_frames, span, sms, kBwdPerSm);
   r.bytes = 2 * align256(r.items * width * 4);
   return r;
 }
 
 cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
                                           int64_t span, int sms, void* workspace, cudaStream_t st) {
-  const Shape s = shape_of(a.width);
+  const Shape s = shape_of(a.width, true);
   a.sms = sms;
   a.warps = s.W;
   a.groups = s.G;

@@ -59,10 +59,18 @@ struct Bf16 {
 
 struct F32 {
   float4 a, b;
+  // Two 16-byte accesses leave half of each 32-byte sector to the other; one
+  // of 32 bytes, where the address allows it, asks L2 once.
   __device__ __forceinline__ void load(const void* base, int64_t i) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    a = p[0];
-    b = p[1];
+    const float* p = static_cast<const float*>(base) + i;
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                   : "l"(p));
+    } else {
+      a = reinterpret_cast<const float4*>(p)[0];
+      b = reinterpret_cast<const float4*>(p)[1];
+    }
   }
   __device__ __forceinline__ void get(P2 (&x)[4]) const {
     x[0] = pair(a.x, a.y);
@@ -75,9 +83,15 @@ struct F32 {
     b = make_float4(lo(x[2]), hi(x[2]), lo(x[3]), hi(x[3]));
   }
   __device__ __forceinline__ void store(void* base, int64_t i) const {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-    p[0] = a;
-    p[1] = b;
+    float* p = static_cast<float*>(base) + i;
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a.x), "f"(a.y), "f"(a.z),
+                   "f"(a.w), "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(p)[0] = a;
+      reinterpret_cast<float4*>(p)[1] = b;
+    }
   }
 };
 
