@@ -204,7 +204,8 @@ struct NormArgs {
   float *z_part = nullptr, *d_part = nullptr;    // [items, width] partial column sums
   int64_t rows = 0, items = 0;
   int width = 0;
-  int warps = 1, groups = 1;      // warps per row, rows per CTA (set by the launcher)
+  int warps = 1, lanes = 32;      // warps per row, and lanes of each (set by the launcher)
+  int groups = 1;                 // rows a CTA works on (set by the launcher)
   int sms = 1;                    // SMs of the device (set by the launcher)
   bool f32 = false;               // residual type
   float alpha = 1.f, eps = 0.f;

@@ -52,8 +52,9 @@ constexpr int kMaxWarps = 16;   // warps per row
 // 3, 44 with 5; backward 66 with 3, 74 with 2, 173 with 4, which spills.
 constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
 
-// Sums over the W warps of the row group.  `slot` alternates, so that one
-// barrier a call is enough (a slot is written again two calls later).
+// Sums over the row's lanes and the W warps of its group.  `slot` alternates,
+// so that one barrier a call is enough (a slot is written again two calls
+// later).
 template <int N>
 struct Exchange {
   float v[2][N][kMaxWarps];
@@ -69,14 +70,15 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
     default: asm volatile("bar.sync 4, %0;" ::"r"(threads) : "memory"); break;
   }
 }
-template <int N>
-__device__ __forceinline__ void group_sums(float (&v)[N], Exchange<N>& ex, int slot, int warps, int w, int lane,
-                                           int group) {
+template <bool kNarrow, int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], Exchange<N>& ex, int slot, int warps, int lanes, int w,
+                                           int lane, int group) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
+    if (!kNarrow || o < lanes)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (warps == 1) return;
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (kNarrow || warps == 1) return;
   if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) ex.v[slot][i][w] = v[i];
@@ -195,24 +197,47 @@ struct RaggedItems {
   __device__ __forceinline__ int64_t rows(int f) const { return row[f + 1] - row[f]; }
 };
 
+// Where a thread works: its row group's item.  A row has W warps, or (kNarrow:
+// up to 128 columns) 4, 8 or 16 lanes of one, whose other lanes have other
+// rows: they all go through the longest item's rows together, for the
+// shuffles.
+struct Place {
+  int group, w, lane;  // of the warps that share a row; the lane within the row
+  bool on;             // an item of its own
+  int64_t item;
+  int f, stride, n, turns;  // the item's frame, rows apart, rows; rows of the warp's longest item
+  int64_t r0;               // first row
+};
+template <bool kNarrow, class Items>
+__device__ __forceinline__ Place place(const NormArgs& a, const Items& items) {
+  Place p;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lanes = kNarrow ? a.lanes : 32;
+  p.group = warp / a.warps;
+  p.w = warp % a.warps;
+  p.lane = lane % lanes;
+  const int64_t item = (int64_t)blockIdx.x * a.groups + p.group * (32 / lanes) + lane / lanes;
+  p.on = item < a.items;
+  p.item = p.on ? item : 0;
+  p.f = items.frame(p.item);
+  p.stride = items.count(p.f);
+  const int first = (int)(p.item - items.first(p.f));
+  p.r0 = items.start(p.f) + first;
+  p.n = p.on ? (int)((items.rows(p.f) - first + p.stride - 1) / p.stride) : 0;
+  p.turns = kNarrow ? (int)__reduce_max_sync(0xffffffffu, (unsigned)p.n) : p.n;
+  return p;
+}
+
 // kWide: rows of more than four warps (up to 512 threads a CTA); else 128
 // threads, so that few registers are left over at any count.
-template <class R, int V, bool kCkpt, bool kWide, class Items>
+template <class R, int V, bool kCkpt, bool kWide, bool kNarrow, class Items>
 __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
     residual_norm_fwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
   __shared__ __align__(16) Exchange<1> ex[kMaxGroups];
   clear_exchange(ex);
-  const int W = a.warps, G = a.groups;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int group = warp / W, w = warp % W;
-  const int C = a.width;
-  const int64_t item = (int64_t)blockIdx.x * G + group;
-  if (item >= a.items) return;  // whole groups: the group's barrier is its own
-  const int f = items.frame(item), stride = items.count(f), first = (int)(item - items.first(f));
-  const int64_t r0 = items.start(f) + first;
-  const int n = (int)((items.rows(f) - first + stride - 1) / stride);
-  const int64_t row_step = (int64_t)stride * C;  // elements between the item's rows
+  const Place at = place<kNarrow>(a, items);
+  const int W = a.warps, group = at.group, w = at.w, lane = at.lane, C = a.width, n = at.n;
+  const int64_t r0 = at.r0, row_step = (int64_t)at.stride * C;  // elements between the item's rows
   const float inv_c = 1.0f / (float)C;
   extern __shared__ uint4 ring[];
   constexpr int S = kRingFwd<V>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
@@ -258,19 +283,20 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
       load_param(a.gamma_pre + col[v], gpre[v]);
       load_param(a.gamma_post + col[v], coef[v]);
       P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
-      if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
+      if (a.gate) load_param(a.gate + (int64_t)at.f * C + col[v], gt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], both(a.alpha)), gt[e]);
     }
   }
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < at.turns; ++i) {
+    const bool live = !kNarrow || i < n;
     copy_wait<S - 1>();
     P2 y[V][4], x[V][4], acc = zero;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Bf16 yv{};
       R xv{};
-      if (in[v]) {
+      if (in[v] && live) {
         const uint32_t src = base + rd.off + v * kVec * step;
         yv = ring_read<Bf16>(src, step);
         xv = ring_read<R>(src + step, step);
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
     rd.next();
     load();
     float s[1] = {sum(acc)};
-    group_sums(s, ex[group], 0, W, w, lane, group);
+    group_sums<kNarrow>(s, ex[group], 0, W, a.lanes, w, lane, group);
     const float ry = rsqrtf(s[0] * inv_c + a.eps);
     const P2 ry2 = both(ry);
     acc = zero;
@@ -295,7 +321,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
         acc = fma2(x[v][e], x[v][e], acc);
       }
     s[0] = sum(acc);
-    group_sums(s, ex[group], 1, W, w, lane, group);
+    group_sums<kNarrow>(s, ex[group], 1, W, a.lanes, w, lane, group);
     const float rx = rsqrtf(s[0] * inv_c + a.eps);
     const P2 rx2 = both(rx);
 #pragma unroll
@@ -307,7 +333,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
       R ov;
       hv.set(h);
       ov.set(x[v]);
-      if (in[v]) {
+      if (in[v] && live) {
         hv.store(ph + v * vstep * 2, 0);
         ov.store(po + v * vstep * kElem, 0);
       }
@@ -315,22 +341,22 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
         ov.get(x[v]);  // the checkpoint is of x' as stored
         uint32_t by, bx;
         const uint2 cy = ckpt::encode8(y[v], by), cx = ckpt::encode8(x[v], bx);
-        if (in[v]) {
-          const int64_t at = (r0 + (int64_t)i * stride) * C + col[v];
-          *reinterpret_cast<uint2*>(a.y8 + at) = cy;
-          *reinterpret_cast<uint2*>(a.x8 + at) = cx;
+        if (in[v] && live) {
+          const int64_t o = r0 * C + i * row_step + col[v];
+          *reinterpret_cast<uint2*>(a.y8 + o) = cy;
+          *reinterpret_cast<uint2*>(a.x8 + o) = cx;
           if ((lane & 3) == 0) {
-            a.y8_scale[at / ckpt::kBlock] = (uint8_t)by;
-            a.x8_scale[at / ckpt::kBlock] = (uint8_t)bx;
+            a.y8_scale[o / ckpt::kBlock] = (uint8_t)by;
+            a.x8_scale[o / ckpt::kBlock] = (uint8_t)bx;
           }
         }
       }
     }
     ph += row_step * 2;
     po += row_step * kElem;
-    if (w == 0 && lane == 0) {
-      a.rstd[r0 + (int64_t)i * stride] = ry;
-      a.rstd[a.rows + r0 + (int64_t)i * stride] = rx;
+    if (w == 0 && lane == 0 && live) {
+      a.rstd[r0 + (int64_t)i * at.stride] = ry;
+      a.rstd[a.rows + r0 + (int64_t)i * at.stride] = rx;
     }
   }
 }
@@ -480,24 +506,17 @@ struct Sums {
 // Both row means come from one exchange: with t = dx' + r_x a (g = t - r_x xh
 // m1), sum(b yh) = sum(coef yh t) - r_x m1 sum(coef yh xh), coef = alpha gate
 // gamma_post, so the three sums of a xh, coef yh t and coef yh xh give both.
-template <class R, int V, bool k8, bool kWide, class Items>
+template <class R, int V, bool k8, bool kWide, bool kNarrow, class Items>
 __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
     residual_norm_bwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
   __shared__ __align__(16) Exchange<3> ex[kMaxGroups];
   clear_exchange(ex);
-  const int W = a.warps, G = a.groups;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int group = warp / W, w = warp % W;
-  const int C = a.width;
-  const float inv_c = 1.0f / (float)C;
   ptx::grid_launch_next();
-  const int64_t item = (int64_t)blockIdx.x * G + group;
-  if (item >= a.items) return;  // whole groups: the group's barrier is its own
-  const int f = items.frame(item), stride = items.count(f), first = (int)(item - items.first(f));
-  const int64_t r0 = items.start(f) + first;
-  const int n = (int)((items.rows(f) - first + stride - 1) / stride);
-  const int64_t row_step = (int64_t)stride * C;  // elements between the item's rows
+  const Place at = place<kNarrow>(a, items);
+  const int W = a.warps, group = at.group, w = at.w, lane = at.lane, C = a.width, n = at.n, stride = at.stride;
+  const int64_t r0 = at.r0, row_step = (int64_t)stride * C;  // elements between the item's rows
+  const float inv_c = 1.0f / (float)C;
   extern __shared__ uint4 ring[];
   using H = Held<R, k8>;
   constexpr int kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
@@ -579,7 +598,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
       load_param(a.gamma_post + col[v], c);
       load_param(a.gamma_pre + col[v], g);
       P2 gt[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
-      if (a.gate) load_param(a.gate + (int64_t)f * C + col[v], gt);
+      if (a.gate) load_param(a.gate + (int64_t)at.f * C + col[v], gt);
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[e] = mul2(mul2(c[e], both(a.alpha)), gt[e]);
     }
@@ -587,8 +606,9 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
   }
   auto row = [&](int i, Small& sm, int slot) {
     P2 y[V][4], x[V][4], t[V][4];
-    const float rx = sm.rx;
-    const P2 ry2 = both(sm.ry), rx2 = both(rx);
+    const bool live = !kNarrow || i < n;
+    const float ry = live ? sm.ry : 0.f, rx = live ? sm.rx : 0.f;
+    const P2 ry2 = both(ry), rx2 = both(rx);
     P2 sa = zero, sb = zero, sc = zero;
     copy_wait<S - 1>();
 #pragma unroll
@@ -596,7 +616,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
       P2 h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[v][e] = x[v][e] = t[v][e] = h[e] = zero;
-      if (in[v]) {
+      if (in[v] && live) {
         const uint32_t src = base + rd.off + v * kVec * step;
         ring_read<R>(src, step).get(t[v]);
         ring_read<Bf16>(src + kG * step, step).get(h);
@@ -622,7 +642,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
     load();
     load_small(i + 2, sm);
     float s[3] = {sum(sa), sum(sb), sum(sc)};
-    group_sums(s, ex[group], slot, W, w, lane, group);
+    group_sums<kNarrow>(s, ex[group], slot, W, a.lanes, w, lane, group);
     const float rm1 = rx * s[0] * inv_c, m2 = (s[1] - rm1 * s[2]) * inv_c;
     const P2 nrm1 = both(-rm1), nm2 = both(-m2);
 #pragma unroll
@@ -639,7 +659,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
       R ov;
       dv.set(d);
       ov.set(t[v]);
-      if (in[v]) {
+      if (in[v] && live) {
         dv.store(pdy + v * vstep * 2, 0);
         ov.store(pdx + v * vstep * kElem, 0);
       }
@@ -647,21 +667,21 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
     pdx += row_step * kElem;
     pdy += row_step * 2;
   };
-  for (int i = 0; i < n; i += 2) {
+  for (int i = 0; i < at.turns; i += 2) {
     row(i, small[0], 0);
-    if (i + 1 < n) row(i + 1, small[1], 1);
+    if (i + 1 < at.turns) row(i + 1, small[1], 1);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (in[v]) {
+    if (in[v] && at.on) {
       F32 o;
       P2 s[4];
       sums.template get<0>(v, s);
       o.set(s);
-      o.store(a.z_part, item * C + col[v]);
+      o.store(a.z_part, at.item * C + col[v]);
       sums.template get<1>(v, s);
       o.set(s);
-      o.store(a.d_part, item * C + col[v]);
+      o.store(a.d_part, at.item * C + col[v]);
     }
 }
 
@@ -741,7 +761,7 @@ __global__ void __launch_bounds__(kSumThreads)
 
 
 struct Shape {
-  int V, W, G;
+  int V, W, L, G;  // vectors a thread, warps and lanes a row, rows a CTA works on
 };
 // One or two vectors a thread in at most four warps (128 threads, whose
 // registers the launch bounds fix); above that the forward takes two vectors
@@ -754,8 +774,11 @@ Shape shape_of(int width, bool backward) {
                 : backward && vecs <= most ? 1
                 : vecs <= 2 * most ? 2 : 4;
   const int W = (vecs + 32 * V - 1) / (32 * V);
-  return {V, W, std::max(1, kMaxGroups / W)};
+  const int L = vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
+  return {V, W, L, std::max(1, kMaxGroups / W) * (32 / L)};
 }
+
+int warps_of(const Shape& s) { return s.W * std::max(1, kMaxGroups / s.W); }  // of a CTA
 
 // A kernel's ring: its opt-in shared memory, and, for more CTAs than SMs, the
 // SM's whole share for it (by itself the driver leaves room for fewer CTAs
@@ -770,22 +793,24 @@ cudaError_t allow_ring(K kern, size_t smem, bool many) {
   return e;
 }
 
-template <class R, int V, bool kCkpt, bool kWide, class Items>
+template <class R, int V, bool kCkpt, bool kWide, bool kNarrow, class Items>
 cudaError_t fwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  auto kern = residual_norm_fwd<R, V, kCkpt, kWide, Items>;
-  const size_t smem = (size_t)32 * s.W * s.G * kRingFwd<V> * V * (16 + sizeof(R));
+  auto kern = residual_norm_fwd<R, V, kCkpt, kWide, kNarrow, Items>;
+  const size_t smem = (size_t)32 * warps_of(s) * kRingFwd<V> * V * (16 + sizeof(R));
   const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
+  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * warps_of(s), smem, st>>>(a, it);
   return cudaGetLastError();
 }
 
 template <class R, int V, class Items>
 cudaError_t fwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
+  if constexpr (V == 1)
+    if (s.L < 32) return a.y8 ? fwd<R, V, true, false, true>(a, it, s, st) : fwd<R, V, false, false, true>(a, it, s, st);
   if constexpr (V >= 2)
-    if (s.W > kMaxGroups) return a.y8 ? fwd<R, V, true, true>(a, it, s, st) : fwd<R, V, false, true>(a, it, s, st);
+    if (s.W > kMaxGroups) return a.y8 ? fwd<R, V, true, true, false>(a, it, s, st) : fwd<R, V, false, true, false>(a, it, s, st);
   if constexpr (V <= 2)
-    return a.y8 ? fwd<R, V, true, false>(a, it, s, st) : fwd<R, V, false, false>(a, it, s, st);
+    return a.y8 ? fwd<R, V, true, false, false>(a, it, s, st) : fwd<R, V, false, false, false>(a, it, s, st);
   return cudaErrorInvalidValue;  // V = 4 has more warps
 }
 template <class Items>
@@ -795,21 +820,23 @@ cudaError_t fwd_all(const NormArgs& a, const Items& it, const Shape& s, cudaStre
   return a.f32 ? fwd_c<vec::F32, 4>(a, it, s, st) : fwd_c<vec::Bf16, 4>(a, it, s, st);
 }
 
-template <class R, int V, bool k8, bool kWide, class Items>
+template <class R, int V, bool k8, bool kWide, bool kNarrow, class Items>
 cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  auto kern = residual_norm_bwd<R, V, k8, kWide, Items>;
+  auto kern = residual_norm_bwd<R, V, k8, kWide, kNarrow, Items>;
   constexpr int kVec = sizeof(R) / 16 + 1 + Held<R, k8>::kPieces;
-  const size_t smem = (size_t)32 * s.W * s.G * V * 16 *
+  const size_t smem = (size_t)32 * warps_of(s) * V * 16 *
                       (ring_bwd<V, kWide, kVec, sizeof(R) == 32>() * kVec + kKeptPieces<V, kWide>);
   const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * s.W * s.G, smem, st>>>(a, it);
+  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * warps_of(s), smem, st>>>(a, it);
   return cudaGetLastError();
 }
 template <class R, int V, class Items>
 cudaError_t bwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true>(a, it, s, st) : bwd<R, V, false, true>(a, it, s, st);
-  if constexpr (V <= 2) return a.y8 ? bwd<R, V, true, false>(a, it, s, st) : bwd<R, V, false, false>(a, it, s, st);
+  if constexpr (V == 1)
+    if (s.L < 32) return a.y8 ? bwd<R, V, true, false, true>(a, it, s, st) : bwd<R, V, false, false, true>(a, it, s, st);
+  if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true, false>(a, it, s, st) : bwd<R, V, false, true, false>(a, it, s, st);
+  if constexpr (V <= 2) return a.y8 ? bwd<R, V, true, false, false>(a, it, s, st) : bwd<R, V, false, false, false>(a, it, s, st);
   return cudaErrorInvalidValue;  // V = 4 has more warps
 }
 template <class Items>
@@ -840,7 +867,7 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // across frames.  Depends on the shape and the device alone.
 NormItems split(int64_t rows, const Shape& s, const int32_t* spans, int n_frames, int64_t span, int sms, int per_sm) {
   // per_sm is in CTAs of four warps (which fix the registers a thread).
-  const int ctas = std::max(1, per_sm * kMaxGroups / (s.W * s.G));
+  const int ctas = std::max(1, per_sm * kMaxGroups / warps_of(s));
   const int64_t want = std::max<int64_t>(n_frames, (int64_t)ctas * sms * s.G);
   auto count = [&](int64_t chunk) {
     if (!spans) return (int64_t)n_frames * ((span + chunk - 1) / chunk);
@@ -880,6 +907,7 @@ cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames,
   const Shape s = shape_of(a.width, false);
   const NormItems n = split(a.rows, s, spans, n_frames, span, sms, kFwdPerSm);
   a.warps = s.W;
+  a.lanes = s.L;
   a.groups = s.G;
   a.items = n.items;
   a.sms = sms;
@@ -897,6 +925,7 @@ cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const 
   const Shape s = shape_of(a.width, true);
   a.sms = sms;
   a.warps = s.W;
+  a.lanes = s.L;
   a.groups = s.G;
   a.items = n.items;
   a.z_part = static_cast<float*>(workspace);
