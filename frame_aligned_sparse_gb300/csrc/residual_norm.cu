@@ -37,6 +37,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "checkpoint.cuh"
 #include "kernels.h"
@@ -104,12 +105,15 @@ __device__ __forceinline__ void clear_exchange(Exchange<N> (&ex)[kMaxGroups]) {
 // backward: what shared memory holds beside what else the threads keep there.
 template <int V>
 constexpr int kRingFwd = V == 4 ? 1 : 2;
-template <int V, bool kWide>
-constexpr int kKeptPieces = (V == 2 ? 4 : 0) + (V == 2 && kWide ? 4 : 0);  // 16 bytes a vector: Params, Sums
-template <int V, bool kWide, int kVec, bool kF32>
+// kT: most threads a CTA of the backward has; CTAs of it that share an SM.
+template <int kT>
+constexpr int kCtas = kT == 128 ? kBwdPerSm : kT == 192 ? 2 : 1;
+template <int V, int kT>
+constexpr int kKeptPieces = (V == 2 ? 4 : 0) + (V == 2 && kT == 512 ? 4 : 0);  // 16 bytes a vector: Params, Sums
+template <int V, int kT, int kVec, bool kF32>
 __host__ __device__ constexpr int ring_bwd() {
-  if (!kWide) return kF32 ? 2 : 3;
-  const int fit = (232448 - 2048 - 512 * 16 * V * kKeptPieces<V, kWide>) / (512 * 16 * V * kVec);
+  if (kT == 128) return kF32 ? 2 : 3;
+  const int fit = (232448 / kCtas<kT> - 3072 - kT * 16 * V * kKeptPieces<V, kT>) / (kT * 16 * V * kVec);
   return fit < 1 ? 1 : fit < 4 ? fit : 4;
 }
 
@@ -227,8 +231,7 @@ __device__ __forceinline__ Place place(const NormArgs& a, const Items& items) {
   return p;
 }
 
-// kWide: rows of more than four warps (up to 512 threads a CTA); else 128
-// threads, so that few registers are left over at any count.
+// kWide: rows of more than four warps (up to 512 threads a CTA); else 128.
 template <class R, int V, bool kCkpt, bool kWide, bool kNarrow, class Items>
 __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
     residual_norm_fwd(const NormArgs a, const __grid_constant__ Items items) {
@@ -452,7 +455,7 @@ struct Params {
 };
 
 // The two column sums of a thread's columns: in registers, or (V = 2 in rows
-// of more than four warps, 128 registers a thread) in shared memory.
+// of more than eight warps, 128 registers a thread) in shared memory.
 template <int V, bool kSmem>
 struct Sums {
   vec::P2 z_[kSmem ? 1 : V][4], d_[kSmem ? 1 : V][4];
@@ -506,8 +509,8 @@ struct Sums {
 // Both row means come from one exchange: with t = dx' + r_x a (g = t - r_x xh
 // m1), sum(b yh) = sum(coef yh t) - r_x m1 sum(coef yh xh), coef = alpha gate
 // gamma_post, so the three sums of a xh, coef yh t and coef yh xh give both.
-template <class R, int V, bool k8, bool kWide, bool kNarrow, class Items>
-__global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
+template <class R, int V, bool k8, int kT, bool kNarrow, class Items>
+__global__ void __launch_bounds__(kT, kCtas<kT>)
     residual_norm_bwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
   __shared__ __align__(16) Exchange<3> ex[kMaxGroups];
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
   extern __shared__ uint4 ring[];
   using H = Held<R, k8>;
   constexpr int kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
-  constexpr int S = ring_bwd<V, kWide, kVec, sizeof(R) == 32>();
+  constexpr int S = ring_bwd<V, kT, kVec, sizeof(R) == 32>();
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   int col[V];
   bool in[V];
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kBwdPerSm)
   Params<V> params;
   params.at = base + S * V * kVec * step;
   params.step = step;
-  Sums<V, V == 2 && kWide> sums;
+  Sums<V, V == 2 && kT == 512> sums;
   sums.at = params.at + V * Params<V>::kPieces * step;
   sums.step = step;
   sums.clear();
@@ -763,16 +766,11 @@ __global__ void __launch_bounds__(kSumThreads)
 struct Shape {
   int V, W, L, G;  // vectors a thread, warps and lanes a row, rows a CTA works on
 };
-// One or two vectors a thread in at most four warps (128 threads, whose
-// registers the launch bounds fix); above that the forward takes two vectors
-// a thread, the backward one while sixteen warps are enough (at two its sums
-// no longer fit in registers), and both four above 8192 columns.
-Shape shape_of(int width, bool backward) {
-  const int vecs = width / 8, most = 32 * kMaxWarps;
-  const int V = vecs <= 32 * kMaxGroups ? 1
-                : vecs <= 64 * kMaxGroups ? 2
-                : backward && vecs <= most ? 1
-                : vecs <= 2 * most ? 2 : 4;
+// One vector a thread up to 256 columns, four above 8192, else two (half the
+// instructions a row that one takes).
+Shape shape_of(int width) {
+  const int vecs = width / 8;
+  const int V = vecs <= 32 ? 1 : vecs <= 64 * kMaxWarps ? 2 : 4;
   const int W = (vecs + 32 * V - 1) / (32 * V);
   const int L = vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
   return {V, W, L, std::max(1, kMaxGroups / W) * (32 / L)};
@@ -820,12 +818,12 @@ cudaError_t fwd_all(const NormArgs& a, const Items& it, const Shape& s, cudaStre
   return a.f32 ? fwd_c<vec::F32, 4>(a, it, s, st) : fwd_c<vec::Bf16, 4>(a, it, s, st);
 }
 
-template <class R, int V, bool k8, bool kWide, bool kNarrow, class Items>
+template <class R, int V, bool k8, int kT, bool kNarrow, class Items>
 cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  auto kern = residual_norm_bwd<R, V, k8, kWide, kNarrow, Items>;
+  auto kern = residual_norm_bwd<R, V, k8, kT, kNarrow, Items>;
   constexpr int kVec = sizeof(R) / 16 + 1 + Held<R, k8>::kPieces;
   const size_t smem = (size_t)32 * warps_of(s) * V * 16 *
-                      (ring_bwd<V, kWide, kVec, sizeof(R) == 32>() * kVec + kKeptPieces<V, kWide>);
+                      (ring_bwd<V, kT, kVec, sizeof(R) == 32>() * kVec + kKeptPieces<V, kT>);
   const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * warps_of(s), smem, st>>>(a, it);
@@ -833,11 +831,24 @@ cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t
 }
 template <class R, int V, class Items>
 cudaError_t bwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  if constexpr (V == 1)
-    if (s.L < 32) return a.y8 ? bwd<R, V, true, false, true>(a, it, s, st) : bwd<R, V, false, false, true>(a, it, s, st);
-  if (s.W > kMaxGroups) return a.y8 ? bwd<R, V, true, true, false>(a, it, s, st) : bwd<R, V, false, true, false>(a, it, s, st);
-  if constexpr (V <= 2) return a.y8 ? bwd<R, V, true, false, false>(a, it, s, st) : bwd<R, V, false, false, false>(a, it, s, st);
-  return cudaErrorInvalidValue;  // V = 4 has more warps
+  auto go = [&](auto t, auto narrow) {
+    constexpr int kT = decltype(t)::value;
+    constexpr bool kN = decltype(narrow)::value;
+    return a.y8 ? bwd<R, V, true, kT, kN>(a, it, s, st) : bwd<R, V, false, kT, kN>(a, it, s, st);
+  };
+  using std::integral_constant;
+  const std::false_type no;
+  if constexpr (V == 1) {
+    if (s.L < 32) return go(integral_constant<int, 128>(), std::true_type());
+    return go(integral_constant<int, 128>(), no);
+  } else if constexpr (V == 2) {
+    if (s.W <= 4) return go(integral_constant<int, 128>(), no);
+    if (s.W <= 6) return go(integral_constant<int, 192>(), no);
+    if (s.W <= 8) return go(integral_constant<int, 256>(), no);
+    return go(integral_constant<int, 512>(), no);
+  } else {
+    return go(integral_constant<int, 512>(), no);
+  }
 }
 template <class Items>
 cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shape& s, cudaStream_t st) {
@@ -904,7 +915,7 @@ cudaError_t with_items(const NormItems& n, const int32_t* spans, int n_frames, i
 
 cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
                                  cudaStream_t st) {
-  const Shape s = shape_of(a.width, false);
+  const Shape s = shape_of(a.width);
   const NormItems n = split(a.rows, s, spans, n_frames, span, sms, kFwdPerSm);
   a.warps = s.W;
   a.lanes = s.L;
@@ -915,14 +926,14 @@ cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames,
 }
 
 NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms) {
-  NormItems r = split(rows, shape_of(width, true), spans, n_frames, span, sms, kBwdPerSm);
+  NormItems r = split(rows, shape_of(width), spans, n_frames, span, sms, kBwdPerSm);
   r.bytes = 2 * align256(r.items * width * 4);
   return r;
 }
 
 cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
                                           int64_t span, int sms, void* workspace, cudaStream_t st) {
-  const Shape s = shape_of(a.width, true);
+  const Shape s = shape_of(a.width);
   a.sms = sms;
   a.warps = s.W;
   a.lanes = s.L;
