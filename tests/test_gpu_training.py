@@ -333,7 +333,8 @@ NORM_SHAPES = [
     # spans, width
     ([1], 8), ([1], 2048), ([3], 40), ([1, 1, 1], 264), ([5, 1, 7], 256), ([48] * 9, 128), ([33, 100, 1, 20], 96),
     ([17] * 5, 1000), ([300], 1536), ([64, 63], 2056), ([700, 40, 900], 2048), ([9, 4], 4104), ([6] * 3, 8192), ([5, 2], 8200),
-    ([3, 4], 16384),
+    ([3, 4], 16384), ([2000, 3], 64), ([90] * 3, 16), ([40, 9], 2824), ([21], 3576), ([50, 5], 4096), ([11], 5120),
+    ([1] * 1024, 72), ([3, 2] * 300, 32),
 ]
 
 
@@ -352,7 +353,8 @@ def test_residual_norm_and_its_backward(spans, width, gated, residual):
 
 
 @pytest.mark.parametrize("residual", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("spans,width", [([1], 32), ([5, 1, 7], 96), ([33, 100, 1, 20], 2048), ([64, 63], 2080), ([3, 4], 8224)],
+@pytest.mark.parametrize("spans,width", [([1], 32), ([5, 1, 7], 96), ([33, 100, 1, 20], 2048), ([64, 63], 2080), ([3, 4], 8224),
+                                         ([70, 1], 32), ([9] * 20, 64), ([40, 3], 3328), ([12], 5120)],
                          ids=lambda v: str(v) if isinstance(v, int) else "x".join(map(str, v)))
 def test_checkpoints_from_the_forward_and_in_the_backward(spans, width, residual):
     """The forward's checkpoints are exactly those of y and of the x' it
@@ -428,6 +430,58 @@ def test_residual_norm_zero_rows():
     assert bool((h == 0).all()) and torch.isfinite(rstd).all()
     got = fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, x, rstd, c.post, c.pre, **c.kw)
     c.check_backward(got, c.y, x, rstd)
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 elements: their last rows as if alone."""
+    n, c = 1_100_000, 2048
+    small = Norm([7], c, torch.bfloat16, False)
+    big = {}
+    for name in ("y", "x", "dx_out", "dh"):
+        t = torch.zeros(n, c, dtype=torch.bfloat16, device="cuda")
+        t[-7:] = getattr(small, name)
+        big[name] = t
+    want = fas.fas_residual_norm(small.y, small.x, small.post, small.pre, alpha=0.7, checkpoint=True)
+    got = fas.fas_residual_norm(big["y"], big["x"], small.post, small.pre, alpha=0.7, checkpoint=True)
+    assert torch.equal(got[0][-7:], want[0]) and torch.equal(got[1][-7:], want[1]) and torch.equal(got[2][:, -7:], want[2])
+    for a, b in zip(got[3:], want[3:]):
+        assert torch.equal(a.codes[-7:].view(torch.uint8), b.codes.view(torch.uint8)) and torch.equal(a.scales[-7:], b.scales)
+    packed = fas.fas_checkpoint_pack(got[0])
+    assert torch.equal(packed.codes[-7:].view(torch.uint8), want[4].codes.view(torch.uint8))
+    back = fas.fas_checkpoint_unpack(packed)
+    assert torch.equal(back[-7:], fas.fas_checkpoint_unpack(want[4])) and not back[:-7].any()
+    del packed, back
+    for held in ((got[3], got[4]), (big["y"], got[0])):
+        alone = (want[3], want[4]) if held[0] is got[3] else (small.y, want[0])
+        a = fas.fas_residual_norm_backward(big["dx_out"], big["dh"], *held, got[2], small.post, small.pre, alpha=0.7)
+        b = fas.fas_residual_norm_backward(small.dx_out, small.dh, *alone, want[2], small.post, small.pre, alpha=0.7)
+        assert torch.equal(a[0][-7:], b[0]) and torch.equal(a[1][-7:], b[1])
+        for x, y in zip(a[2:4], b[2:4]):  # the zero rows add nothing, in another order
+            assert float((x - y).norm() / y.norm()) <= 1e-6
+
+
+def test_attention_backward_offsets_beyond_32_bits():
+    """200 heads of 89,600 tokens (2.3 G elements a tensor): the last head's
+    gradients, in both layouts, as that head's alone."""
+    spans, h, d = [128] * 700, 200, 128
+    one = Attention(spans, 0, 0, 1, d)
+    want = one.run()
+    for layout in ("hnd", "nhd"):
+        plan(spans, 0, 0, h, d, layout)
+        shape = (h, sum(spans), d) if layout == "hnd" else (sum(spans), h, d)
+        at = (slice(-1, None),) if layout == "hnd" else (slice(None), slice(-1, None))
+        big = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(5)]
+        for t, src in zip(big, (one.q, one.k, one.v, one.out, one.dout)):
+            t[at] = src if layout == "hnd" else src.transpose(0, 1)
+        lse = torch.zeros(h, sum(spans), device="cuda")
+        lse[-1] = one.lse[0]
+        got = fas.fas_backward(*big[:4], lse, big[4])
+        assert fas.fas_status() == fas.FAS_OK
+        for n, g in zip(("dq", "dk", "dv"), got):
+            g = g[at] if layout == "hnd" else g[at].transpose(0, 1)
+            assert torch.equal(g, want[n]), (layout, n)
+        del big, got, lse
+        torch.cuda.empty_cache()
 
 
 def test_norm_binding_refuses():
