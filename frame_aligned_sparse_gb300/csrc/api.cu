@@ -1118,10 +1118,12 @@ int fas_status(void* cuda_stream) {
   unsigned int e = 0, f = 0;
   if (cudaMemcpy(&e, g_state.err, sizeof(e), cudaMemcpyDeviceToHost) != cudaSuccess) return FAS_ERR_CUDA;
   if (cudaMemcpy(&f, g_state.flags, sizeof(f), cudaMemcpyDeviceToHost) != cudaSuccess) return FAS_ERR_CUDA;
-  if (e == 0 && f == 0) return FAS_OK;
+  bool rows = false;
+  if (fas::residual_norm_gave_up(&rows) != cudaSuccess) return FAS_ERR_CUDA;
+  if (e == 0 && f == 0 && !rows) return FAS_OK;
   if (e && cudaMemset(g_state.err, 0, sizeof(e)) != cudaSuccess) return FAS_ERR_CUDA;
   if (f && cudaMemset(g_state.flags, 0, sizeof(f)) != cudaSuccess) return FAS_ERR_CUDA;
-  return e ? FAS_ERR_TIMEOUT : FAS_ERR_BOUND;
+  return e || rows ? FAS_ERR_TIMEOUT : FAS_ERR_BOUND;
 }
 
 int fas_prepass_readback(float* mu, float* frame_max, float* stat, uint8_t* elig, float* row_bound,

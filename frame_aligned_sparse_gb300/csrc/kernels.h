@@ -206,6 +206,7 @@ struct NormArgs {
   int width = 0;
   int warps = 1, lanes = 32;      // warps per row, and lanes of each (set by the launcher)
   int groups = 1;                 // rows a CTA works on (set by the launcher)
+  int ctas = 1;                   // CTAs a row, a cluster (set by the launcher)
   int sms = 1;                    // SMs of the device (set by the launcher)
   bool f32 = false;               // residual type
   float alpha = 1.f, eps = 0.f;
@@ -222,6 +223,10 @@ cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames,
                                  cudaStream_t stream);
 cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
                                           int64_t span, int sms, void* workspace, cudaStream_t stream);
+
+// Whether a row's wait on the other CTAs of its cluster ran out since the last
+// call (the rows then hold NaN); clears it.  Current device.
+cudaError_t residual_norm_gave_up(bool* gave_up);
 
 // n elements (a multiple of 32) to and from 8-bit checkpoints.
 cudaError_t launch_checkpoint_pack(const void* x, bool f32, uint8_t* codes, uint8_t* scales, int64_t n,

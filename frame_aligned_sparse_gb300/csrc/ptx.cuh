@@ -288,6 +288,40 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// try_wait for what other CTAs of the cluster wrote.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Stores one or three values at `addr`'s offset in the shared memory of the
+// cluster's CTA `rank`; they count (4 or 16 bytes) on the mbarrier at `bar`'s
+// offset there.
+__device__ __forceinline__ void store_async_cluster(uint32_t addr, uint32_t bar, int rank, const float (&v)[1]) {
+  asm volatile(
+      "{\n\t.reg .b32 r, m;\n\t"
+      "mapa.shared::cluster.u32 r, %0, %2;\n\t"
+      "mapa.shared::cluster.u32 m, %1, %2;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [r], %3, [m];\n\t}" ::"r"(addr), "r"(bar), "r"(rank), "f"(v[0])
+      : "memory");
+}
+__device__ __forceinline__ void store_async_cluster(uint32_t addr, uint32_t bar, int rank, const float (&v)[3]) {
+  asm volatile(
+      "{\n\t.reg .b32 r, m;\n\t"
+      "mapa.shared::cluster.u32 r, %0, %2;\n\t"
+      "mapa.shared::cluster.u32 m, %1, %2;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [r], {%3, %4, %5, %5}, [m];\n\t}" ::"r"(addr), "r"(bar), "r"(rank),
+      "f"(v[0]), "f"(v[1]), "f"(v[2])
+      : "memory");
+}
+
 // All threads of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

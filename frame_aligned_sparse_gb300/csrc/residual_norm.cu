@@ -14,19 +14,20 @@
 // Everything is fp32 but the stored results, which are rounded once.
 //
 // A row belongs to a group of W warps, eight columns a vector and one or two
-// vectors a thread (four above 8192 columns), so a row's values stay
-// in registers from its arrival to its stores, and a row sum is a warp
-// shuffle and one exchange through shared memory.  A group works through its
-// item's rows; gamma and gate stay with it, and the next rows are on their way
-// into a ring in shared memory.  Each thread copies just the bytes it will
-// read itself (cp.async), so the ring needs no barrier.  (One vector a thread
-// and rows prefetched into registers: twice the instructions a row, 57 us
-// forward and 80 backward at 14,960 x 2048.)
+// vectors a thread, so a row's values stay in registers from its arrival to
+// its stores, and a row sum is a warp shuffle and one exchange through shared
+// memory: of the CTA, or, for rows of more warps than a CTA takes, of the CTAs
+// of a cluster.  A group works through its item's rows; gamma and gate stay
+// with it, and the next rows are on their way into a ring in shared memory.
+// Each thread copies just the bytes it will read itself (cp.async), so the
+// ring needs no barrier.  (One vector a thread and rows prefetched into
+// registers: twice the instructions a row, 57 us forward and 80 backward at
+// 14,960 x 2048.)
 //
-// Bound by HBM: forward 41.5 us at 14,960 x 2048 bf16 (5.9 TB/s, 0.87 of the
+// Bound by HBM: forward 42 us at 14,960 x 2048 bf16 (5.8 TB/s, 0.86 of the
 // measured copy rate), backward 59 us (6.2 TB/s, 0.91) and 7 for its sums;
-// 292 us (0.82) from 8-bit checkpoints at 79,200 x 2048, where decoding takes
-// issue slots; device time of captured calls.
+// 291 us (0.82) from 8-bit checkpoints at 79,200 x 2048, where decoding takes
+// issue slots; device time of captured calls.  Narrow and wide rows: see Row.
 //
 // Backward: a group's rows never cross frames, so it adds its columns of Z
 // and of dgamma_pre in registers and writes one partial row of each at its
@@ -37,6 +38,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "checkpoint.cuh"
@@ -46,20 +48,25 @@
 namespace fas {
 namespace {
 
-constexpr int kMaxGroups = 4;   // row groups per CTA (named barriers 1 .. 4), and warps of a CTA unless a row needs more
-constexpr int kMaxWarps = 16;   // warps per row
+constexpr int kMaxGroups = 4;  // row groups per CTA (named barriers 1 .. 4), and warps of a CTA unless a row needs more
+constexpr int kMaxCtas = 8;    // CTAs of a cluster that share a row
 // CTAs of four warps per SM: what the registers allow without spilling (16
 // warps of 128, 12 of 168).  On 14,960 x 2048: forward 41.5 us with 4, 43 with
-// 3, 44 with 5; backward 66 with 3, 74 with 2, 173 with 4, which spills.
+// 3, 44 with 5; backward 65 with 3, 74 with 2, 173 with 4, which spills.
 constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
 
-// Sums over the row's lanes and the W warps of its group.  `slot` alternates,
-// so that one barrier a call is enough (a slot is written again two calls
-// later).
-template <int N>
-struct Exchange {
-  float v[2][N][kMaxWarps];
-};
+// Who shares a row: 4, 8 or 16 lanes of a warp (up to 128 columns), one to
+// four warps of a CTA, a CTA of more (kWide), or a cluster of CTAs of up to
+// four warps.  A CTA that has a row to itself stands still while its row sums
+// are exchanged, and the few such CTAs an SM holds hide less of it than three
+// or four whose sums cross the cluster.  % of the copy rate, CTA against
+// cluster (30 M elements): forward at 2,560 columns 84 against 60, 4,096 84 /
+// 79, 5,120 (ten warps) 60 / 82, 16,384 (whose rows spilled in one CTA) 50 /
+// 71; backward 76 / 64, 67 / 75, 64 / 71, 24 / 61; from 8 bits 63 / 44, 56 /
+// 59, 38 / 55, 17 / 47.  Narrow rows: 64 columns 84, 61 and 53.
+enum Row { kLanes, kWarps, kWide, kCluster };
+constexpr int kWideFwd = 8, kWideBwd = 6;  // most warps of a kWide CTA
+
 // A barrier of one row group.  The numbers are constants: with one in a
 // register the kernel would claim all sixteen barriers, and an SM holds
 // sixty-four.
@@ -71,51 +78,122 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
     default: asm volatile("bar.sync 4, %0;" ::"r"(threads) : "memory"); break;
   }
 }
-template <bool kNarrow, int N>
-__device__ __forceinline__ void group_sums(float (&v)[N], Exchange<N>& ex, int slot, int warps, int lanes, int w,
-                                           int lane, int group) {
+
+// Sums over the row's lanes and the W warps of its group.  `slot` alternates,
+// so that one barrier a call is enough (a slot is written again two calls
+// later); `phase` counts a slot's uses.
+template <Row kRow, int N>
+struct Exchange {
+  static constexpr int kSlots = kRow == kWide ? 8 : 4, kGroups = kRow == kWide ? 1 : kMaxGroups;
+  float v[kGroups][2][N][kSlots];
+  __device__ __forceinline__ void start() {  // zero where no warp writes
+    float* p = &v[0][0][0][0];
+    for (int i = threadIdx.x; i < (int)(sizeof(v) / 4); i += blockDim.x) p[i] = 0.f;
+    __syncthreads();
+  }
+  // v's sums over the warps.
+  __device__ __forceinline__ void sum(float (&x)[N], int slot, int, const NormArgs& a, int w, int lane, int group) {
+    if (lane == 0)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (!kNarrow || o < lanes)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (kNarrow || warps == 1) return;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) ex.v[slot][i][w] = v[i];
-  group_sync(group, warps * 32);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int k = 0; k < warps; k += 4)  // the row's tail is zero
+      for (int i = 0; i < N; ++i) v[group][slot][i][w] = x[i];
+    group_sync(group, a.warps * 32);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float4 p = *reinterpret_cast<const float4*>(&ex.v[slot][i][k]);
-      v[i] += (p.x + p.y) + (p.z + p.w);
+      const float4* p = reinterpret_cast<const float4*>(v[group][slot][i]);
+      x[i] = (p[0].x + p[0].y) + (p[0].z + p[0].w);
+      if (kRow == kWide) x[i] += (p[1].x + p[1].y) + (p[1].z + p[1].w);
     }
-}
+  }
+  __device__ __forceinline__ void finish() {}
+};
+
+// Set where a cluster's wait was given up.
+__device__ unsigned int g_gave_up;
+std::atomic<bool> g_clusters{false};  // a cluster was launched
+
+// In a cluster each warp sends its sums to every CTA of the row (st.async) and
+// each CTA waits on its own mbarrier for all warps' bytes: one trip between
+// SMs, where storing and a barrier of the cluster take several (4,096 columns:
+// 79% of the copy rate against 54 forward, 76 against 59 backward).  A slot is
+// free again as in one CTA: who sends for call n + 2 has all of call n + 1,
+// which each warp sent after reading call n.
 template <int N>
-__device__ __forceinline__ void clear_exchange(Exchange<N> (&ex)[kMaxGroups]) {
-  float* p = reinterpret_cast<float*>(ex);
-  for (int i = threadIdx.x; i < (int)(sizeof(ex) / 4); i += blockDim.x) p[i] = 0.f;
-  __syncthreads();
+struct Exchange<kCluster, N> {
+  static constexpr int kPart = N == 1 ? 1 : 4;  // floats a warp sends: one, or three and a pad
+  float part[2][kMaxCtas * kMaxGroups][kPart];
+  uint64_t bar[2];
+  int given_up;
+  __device__ __forceinline__ void start() {
+    for (int i = threadIdx.x; i < 2 * kMaxCtas * kMaxGroups * kPart; i += blockDim.x) (&part[0][0][0])[i] = 0.f;
+    if (threadIdx.x == 0) {
+      given_up = 0;
+      ptx::mbar_init(ptx::smem_addr(&bar[0]), 1);
+      ptx::mbar_init(ptx::smem_addr(&bar[1]), 1);
+      ptx::fence_mbar_init();
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+  }
+  // All CTAs of a cluster run together, so the wait ends.  Should it not, the
+  // rows that are left become NaN and the module's error word is set.
+  __device__ __forceinline__ bool wait(uint32_t b, int phase) {
+    if (ptx::mbar_try_wait_cluster(b, phase & 1)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+      if (ptx::mbar_try_wait_cluster(b, phase & 1)) return true;
+      if ((it & 7u) != 0u) continue;
+      if (*reinterpret_cast<volatile int*>(&given_up)) return false;
+      const uint64_t now = ptx::global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile int*>(&given_up) = 1;
+        atomicOr(&g_gave_up, 1u);
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ void sum(float (&x)[N], int slot, int phase, const NormArgs& a, int w, int lane, int) {
+    const uint32_t b = ptx::smem_addr(&bar[slot]);
+    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(b, a.warps * kPart * 4);
+    if (lane < a.ctas) ptx::store_async_cluster(ptx::smem_addr(part[slot][w]), b, lane, x);
+    const bool got = wait(b, phase);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = got ? 0.f : __int_as_float(0x7fffffff);
+#pragma unroll 4
+    for (int k = 0; k < a.warps; k += 4 / kPart) {  // the row's tail is zero
+      const float4 p = *reinterpret_cast<const float4*>(part[slot][k]);
+      if constexpr (N == 1) {
+        x[0] += (p.x + p.y) + (p.z + p.w);
+      } else {
+        x[0] += p.x;
+        x[1] += p.y;
+        x[2] += p.z;
+      }
+    }
+  }
+  // No CTA leaves while another may still send to it.
+  __device__ __forceinline__ void finish() {
+    __syncwarp();
+    ptx::cluster_sync();
+  }
+};
+template <Row kRow, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], Exchange<kRow, N>& ex, int slot, int phase, const NormArgs& a,
+                                         int w, int lane, int group) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (kRow != kLanes || o < a.lanes)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (kRow == kLanes || (kRow == kWarps && a.warps == 1)) return;
+  ex.sum(v, slot, phase, a, w, lane, group);
 }
 
-// Stages of a row ring.  Rows of at most four warps: two (forward) or three
-// (backward) cover HBM's latency with the CTAs that fit; wider rows in the
-// backward: what shared memory holds beside what else the threads keep there.
-template <int V>
-constexpr int kRingFwd = V == 4 ? 1 : 2;
-// kT: most threads a CTA of the backward has; CTAs of it that share an SM.
-template <int kT>
-constexpr int kCtas = kT == 128 ? kBwdPerSm : kT == 192 ? 2 : 1;
-template <int V, int kT>
-constexpr int kKeptPieces = (V == 2 ? 4 : 0) + (V == 2 && kT == 512 ? 4 : 0);  // 16 bytes a vector: Params, Sums
-template <int V, int kT, int kVec, bool kF32>
-__host__ __device__ constexpr int ring_bwd() {
-  if (kT == 128) return kF32 ? 2 : 3;
-  const int fit = (232448 / kCtas<kT> - 3072 - kT * 16 * V * kKeptPieces<V, kT>) / (kT * 16 * V * kVec);
-  return fit < 1 ? 1 : fit < 4 ? fit : 4;
-}
+// Stages of a row ring: two (forward) or three (backward; two for fp32) cover
+// HBM's latency with the CTAs that fit.
+constexpr int kRingFwd = 2;
+template <bool kF32>
+constexpr int kRingBwd = kF32 ? 2 : 3;
 
 // Asynchronous copies of this thread's bytes into its own shared memory.
 // kL1: the other half of the sector is asked for next, so it goes by L1.
@@ -163,6 +241,29 @@ __device__ __forceinline__ X ring_read(uint32_t addr, uint32_t step) {
 }
 __device__ __forceinline__ const uint8_t* bytes_of(const void* p) { return static_cast<const uint8_t*>(p); }
 __device__ __forceinline__ uint8_t* bytes_of(void* p) { return static_cast<uint8_t*>(p); }
+
+// A load that leaves x as it was unless `on`.  kInPlace: without a copy of x,
+// which would wait for an earlier load, and without a branch.  (In clusters 61
+// instead of 56% of the copy rate from 8 bits at 4,096 columns.  Elsewhere the
+// compiler makes no copies, and this costs registers, to spilling.)
+template <bool kInPlace>
+__device__ __forceinline__ void load_if(bool on, float& x, const float* p) {
+  if constexpr (kInPlace)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.f32 %0, [%1];\n\t}"
+                 : "+f"(x)
+                 : "l"(p), "r"((uint32_t)on));
+  else if (on)
+    x = *p;
+}
+template <bool kInPlace>
+__device__ __forceinline__ void load_if(bool on, uint32_t& x, const uint8_t* p) {
+  if constexpr (kInPlace)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u8 %0, [%1];\n\t}"
+                 : "+r"(x)
+                 : "l"(p), "r"((uint32_t)on));
+  else if (on)
+    x = *p;
+}
 
 // Eight consecutive fp32 parameters.
 __device__ __forceinline__ void load_param(const float* p, vec::P2 (&x)[4]) {
@@ -212,14 +313,17 @@ struct Place {
   int f, stride, n, turns;  // the item's frame, rows apart, rows; rows of the warp's longest item
   int64_t r0;               // first row
 };
-template <bool kNarrow, class Items>
+template <Row kRow, class Items>
 __device__ __forceinline__ Place place(const NormArgs& a, const Items& items) {
   Place p;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lanes = kNarrow ? a.lanes : 32;
-  p.group = warp / a.warps;
-  p.w = warp % a.warps;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, lanes = kRow == kLanes ? a.lanes : 32;
+  // (kWide's is 0, but with barriers of a constant number its backward ran at
+  // 70 instead of 76% of the copy rate at 2,560 columns.)
+  p.group = kRow == kCluster ? 0 : warp / a.warps;
+  p.w = kRow == kCluster ? (int)(ptx::cluster_ctarank() * (blockDim.x / 32)) + warp : warp % a.warps;
   p.lane = lane % lanes;
-  const int64_t item = (int64_t)blockIdx.x * a.groups + p.group * (32 / lanes) + lane / lanes;
+  const int64_t item = kRow == kCluster ? (int64_t)(blockIdx.x / a.ctas)
+                                        : (int64_t)blockIdx.x * a.groups + p.group * (32 / lanes) + lane / lanes;
   p.on = item < a.items;
   p.item = p.on ? item : 0;
   p.f = items.frame(p.item);
@@ -227,23 +331,22 @@ __device__ __forceinline__ Place place(const NormArgs& a, const Items& items) {
   const int first = (int)(p.item - items.first(p.f));
   p.r0 = items.start(p.f) + first;
   p.n = p.on ? (int)((items.rows(p.f) - first + p.stride - 1) / p.stride) : 0;
-  p.turns = kNarrow ? (int)__reduce_max_sync(0xffffffffu, (unsigned)p.n) : p.n;
+  p.turns = kRow == kLanes ? (int)__reduce_max_sync(0xffffffffu, (unsigned)p.n) : p.n;
   return p;
 }
 
-// kWide: rows of more than four warps (up to 512 threads a CTA); else 128.
-template <class R, int V, bool kCkpt, bool kWide, bool kNarrow, class Items>
-__global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
+template <class R, int V, bool kCkpt, Row kRow, class Items>
+__global__ void __launch_bounds__(kRow == kWide ? 32 * kWideFwd : 128, kRow == kWide ? 2 : kFwdPerSm)
     residual_norm_fwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
-  __shared__ __align__(16) Exchange<1> ex[kMaxGroups];
-  clear_exchange(ex);
-  const Place at = place<kNarrow>(a, items);
+  __shared__ __align__(16) Exchange<kRow, 1> ex;
+  ex.start();
+  const Place at = place<kRow>(a, items);
   const int W = a.warps, group = at.group, w = at.w, lane = at.lane, C = a.width, n = at.n;
   const int64_t r0 = at.r0, row_step = (int64_t)at.stride * C;  // elements between the item's rows
   const float inv_c = 1.0f / (float)C;
   extern __shared__ uint4 ring[];
-  constexpr int S = kRingFwd<V>, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
+  constexpr int S = kRingFwd, kX = sizeof(R) / 16, kVec = 1 + kX, kElem = sizeof(R) / 8;
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   bool in[V];
   int col[V];
@@ -292,7 +395,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
     }
   }
   for (int i = 0; i < at.turns; ++i) {
-    const bool live = !kNarrow || i < n;
+    const bool live = kRow != kLanes || i < n;
     copy_wait<S - 1>();
     P2 y[V][4], x[V][4], acc = zero;
 #pragma unroll
@@ -312,7 +415,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
     rd.next();
     load();
     float s[1] = {sum(acc)};
-    group_sums<kNarrow>(s, ex[group], 0, W, a.lanes, w, lane, group);
+    row_sums(s, ex, 0, i, a, w, lane, group);
     const float ry = rsqrtf(s[0] * inv_c + a.eps);
     const P2 ry2 = both(ry);
     acc = zero;
@@ -324,7 +427,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
         acc = fma2(x[v][e], x[v][e], acc);
       }
     s[0] = sum(acc);
-    group_sums<kNarrow>(s, ex[group], 1, W, a.lanes, w, lane, group);
+    row_sums(s, ex, 1, i, a, w, lane, group);
     const float rx = rsqrtf(s[0] * inv_c + a.eps);
     const P2 rx2 = both(rx);
 #pragma unroll
@@ -362,6 +465,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 128, kWide ? 1 : kFwdPerSm)
       a.rstd[a.rows + r0 + (int64_t)i * at.stride] = rx;
     }
   }
+  ex.finish();
 }
 
 // y and x' of one thread's eight columns, 16 bits (or fp32 x') or 8 bits.
@@ -454,76 +558,24 @@ struct Params {
   }
 };
 
-// The two column sums of a thread's columns: in registers, or (V = 2 in rows
-// of more than eight warps, 128 registers a thread) in shared memory.
-template <int V, bool kSmem>
-struct Sums {
-  vec::P2 z_[kSmem ? 1 : V][4], d_[kSmem ? 1 : V][4];
-  uint32_t at, step;
-  __device__ __forceinline__ uint32_t piece(int v, int i) const { return at + (v * 4 + i) * step; }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if constexpr (kSmem) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v2.u64 [%0], {%1, %1};" ::"r"(piece(v, i)), "l"(0ull) : "memory");
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z_[v][e] = d_[v][e] = vec::both(0.f);
-      }
-    }
-  }
-  // The sums' four pairs (which: 0 Z, 1 dgamma_pre) += a * b.
-  template <int kWhich>
-  __device__ __forceinline__ void add(int v, const vec::P2 (&a)[4], const vec::P2 (&b)[4]) {
-    if constexpr (kSmem) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        vec::P2 s0, s1;
-        const uint32_t p = piece(v, kWhich * 2 + i);
-        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(s0.v), "=l"(s1.v) : "r"(p));
-        s0 = vec::fma2(a[2 * i], b[2 * i], s0);
-        s1 = vec::fma2(a[2 * i + 1], b[2 * i + 1], s1);
-        asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(p), "l"(s0.v), "l"(s1.v) : "memory");
-      }
-    } else {
-      vec::P2(&s)[4] = kWhich ? d_[v] : z_[v];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = vec::fma2(a[e], b[e], s[e]);
-    }
-  }
-  template <int kWhich>
-  __device__ __forceinline__ void get(int v, vec::P2 (&s)[4]) const {
-    if constexpr (kSmem) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(s[2 * i].v), "=l"(s[2 * i + 1].v) : "r"(piece(v, kWhich * 2 + i)));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = kWhich ? d_[v][e] : z_[v][e];
-    }
-  }
-};
-
 // Both row means come from one exchange: with t = dx' + r_x a (g = t - r_x xh
 // m1), sum(b yh) = sum(coef yh t) - r_x m1 sum(coef yh xh), coef = alpha gate
 // gamma_post, so the three sums of a xh, coef yh t and coef yh xh give both.
-template <class R, int V, bool k8, int kT, bool kNarrow, class Items>
-__global__ void __launch_bounds__(kT, kCtas<kT>)
+template <class R, int V, bool k8, Row kRow, class Items>
+__global__ void __launch_bounds__(kRow == kWide ? 32 * kWideBwd : 128, kRow == kWide ? 2 : kBwdPerSm)
     residual_norm_bwd(const NormArgs a, const __grid_constant__ Items items) {
   using namespace vec;
-  __shared__ __align__(16) Exchange<3> ex[kMaxGroups];
-  clear_exchange(ex);
+  __shared__ __align__(16) Exchange<kRow, 3> ex;
+  ex.start();
   ptx::grid_launch_next();
-  const Place at = place<kNarrow>(a, items);
+  const Place at = place<kRow>(a, items);
   const int W = a.warps, group = at.group, w = at.w, lane = at.lane, C = a.width, n = at.n, stride = at.stride;
   const int64_t r0 = at.r0, row_step = (int64_t)stride * C;  // elements between the item's rows
   const float inv_c = 1.0f / (float)C;
   extern __shared__ uint4 ring[];
   using H = Held<R, k8>;
   constexpr int kG = sizeof(R) / 16, kVec = kG + 1 + H::kPieces, kElem = sizeof(R) / 8;
-  constexpr int S = ring_bwd<V, kT, kVec, sizeof(R) == 32>();
+  constexpr int S = kRingBwd<sizeof(R) == 32>;
   const uint32_t step = blockDim.x * 16, base = ptx::smem_addr(ring + threadIdx.x);
   int col[V];
   bool in[V];
@@ -571,17 +623,18 @@ __global__ void __launch_bounds__(kT, kCtas<kT>)
     sx = a.x8_scale + at0 / ckpt::kBlock;
   }
   auto load_small = [&](int i, Small& s) {
-    if (i < n) {
-      s.ry = pr[(int64_t)i * stride];
-      s.rx = pr[(int64_t)i * stride + a.rows];
-      if (k8)
+    const bool on = i < n;
+    if (kRow != kCluster && !on) return;
+    const float* p = pr + (int64_t)i * stride;
+    load_if<kRow == kCluster>(on, s.ry, p);
+    load_if<kRow == kCluster>(on, s.rx, p + a.rows);
+    if (k8)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (in[v]) {
-            s.by[v] = sy[i * (row_step / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
-            s.bx[v] = sx[i * (row_step / ckpt::kBlock) + v * (vstep / ckpt::kBlock)];
-          }
-    }
+      for (int v = 0; v < V; ++v) {
+        const int64_t o = i * (row_step / ckpt::kBlock) + v * (vstep / ckpt::kBlock);
+        load_if<kRow == kCluster>(on && in[v], s.by[v], sy + o);
+        load_if<kRow == kCluster>(on && in[v], s.bx[v], sx + o);
+      }
   };
   Small small[2] = {};
   load_small(0, small[0]);
@@ -590,10 +643,11 @@ __global__ void __launch_bounds__(kT, kCtas<kT>)
   Params<V> params;
   params.at = base + S * V * kVec * step;
   params.step = step;
-  Sums<V, V == 2 && kT == 512> sums;
-  sums.at = params.at + V * Params<V>::kPieces * step;
-  sums.step = step;
-  sums.clear();
+  P2 zs[V][4], ds[V][4];  // sums of the thread's columns of Z and dgamma_pre
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) zs[v][e] = ds[v][e] = zero;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     P2 c[4] = {zero, zero, zero, zero}, g[4] = {zero, zero, zero, zero};
@@ -609,7 +663,7 @@ __global__ void __launch_bounds__(kT, kCtas<kT>)
   }
   auto row = [&](int i, Small& sm, int slot) {
     P2 y[V][4], x[V][4], t[V][4];
-    const bool live = !kNarrow || i < n;
+    const bool live = kRow != kLanes || i < n;
     const float ry = live ? sm.ry : 0.f, rx = live ? sm.rx : 0.f;
     const P2 ry2 = both(ry), rx2 = both(rx);
     P2 sa = zero, sb = zero, sc = zero;
@@ -639,13 +693,14 @@ __global__ void __launch_bounds__(kT, kCtas<kT>)
         sb = fma2(cy, t[v][e], sb);
         sc = fma2(cy, x[v][e], sc);
       }
-      sums.template add<1>(v, h, x[v]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ds[v][e] = fma2(h[e], x[v][e], ds[v][e]);
     }
     rd.next();
     load();
     load_small(i + 2, sm);
     float s[3] = {sum(sa), sum(sb), sum(sc)};
-    group_sums<kNarrow>(s, ex[group], slot, W, a.lanes, w, lane, group);
+    row_sums(s, ex, slot, i >> 1, a, w, lane, group);
     const float rm1 = rx * s[0] * inv_c, m2 = (s[1] - rm1 * s[2]) * inv_c;
     const P2 nrm1 = both(-rm1), nm2 = both(-m2);
 #pragma unroll
@@ -657,7 +712,8 @@ __global__ void __launch_bounds__(kT, kCtas<kT>)
         t[v][e] = fma2(nrm1, x[v][e], t[v][e]);  // g
         d[e] = mul2(ry2, fma2(nm2, y[v][e], mul2(coef[e], t[v][e])));
       }
-      sums.template add<0>(v, y[v], t[v]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) zs[v][e] = fma2(y[v][e], t[v][e], zs[v][e]);
       Bf16 dv;
       R ov;
       dv.set(d);
@@ -678,14 +734,12 @@ __global__ void __launch_bounds__(kT, kCtas<kT>)
   for (int v = 0; v < V; ++v)
     if (in[v] && at.on) {
       F32 o;
-      P2 s[4];
-      sums.template get<0>(v, s);
-      o.set(s);
+      o.set(zs[v]);
       o.store(a.z_part, at.item * C + col[v]);
-      sums.template get<1>(v, s);
-      o.set(s);
+      o.set(ds[v]);
       o.store(a.d_part, at.item * C + col[v]);
     }
+  ex.finish();
 }
 
 // Adds the partials: a CTA per 16 columns, 128 lanes of four-column loads.
@@ -764,19 +818,29 @@ __global__ void __launch_bounds__(kSumThreads)
 
 
 struct Shape {
-  int V, W, L, G;  // vectors a thread, warps and lanes a row, rows a CTA works on
+  int V, W, L, G, N;  // vectors a thread, warps and lanes a row, rows a CTA works on, CTAs a row
+  Row row;
+  int warps() const { return N > 1 ? W / N : W * std::max(1, kMaxGroups / W); }  // of a CTA
+  int threads() const { return 32 * warps(); }
+  int64_t ctas(int64_t items) const { return (items + G - 1) / G * N; }
 };
-// One vector a thread up to 256 columns, four above 8192, else two (half the
-// instructions a row that one takes).
-Shape shape_of(int width) {
-  const int vecs = width / 8;
-  const int V = vecs <= 32 ? 1 : vecs <= 64 * kMaxWarps ? 2 : 4;
-  const int W = (vecs + 32 * V - 1) / (32 * V);
-  const int L = vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
-  return {V, W, L, std::max(1, kMaxGroups / W) * (32 / L)};
+// One vector a thread up to 256 columns, else two (half the instructions a row
+// that one takes).  Clusters: the CTAs of two to four warps that leave the
+// fewest idle, and the largest of those.
+Shape shape_of(int width, int wide) {
+  const int vecs = width / 8, V = vecs <= 32 ? 1 : 2, W = (vecs + 32 * V - 1) / (32 * V);
+  if (W <= kMaxGroups) {
+    const int L = vecs <= 4 ? 4 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
+    return {V, W, L, kMaxGroups / W * (32 / L), 1, L < 32 ? kLanes : kWarps};
+  }
+  if (W <= wide) return {V, W, 32, 1, 1, kWide};
+  int ctas = 0, warps = 0;
+  for (int w = kMaxGroups; w >= 2; --w) {
+    const int n = (W + w - 1) / w;
+    if (n <= kMaxCtas && (!ctas || n * w < ctas * warps)) ctas = n, warps = w;
+  }
+  return {V, ctas * warps, 32, 1, ctas, kCluster};
 }
-
-int warps_of(const Shape& s) { return s.W * std::max(1, kMaxGroups / s.W); }  // of a CTA
 
 // A kernel's ring: its opt-in shared memory, and, for more CTAs than SMs, the
 // SM's whole share for it (by itself the driver leaves room for fewer CTAs
@@ -791,74 +855,103 @@ cudaError_t allow_ring(K kern, size_t smem, bool many) {
   return e;
 }
 
-template <class R, int V, bool kCkpt, bool kWide, bool kNarrow, class Items>
-cudaError_t fwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  auto kern = residual_norm_fwd<R, V, kCkpt, kWide, kNarrow, Items>;
-  const size_t smem = (size_t)32 * warps_of(s) * kRingFwd<V> * V * (16 + sizeof(R));
-  const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
+// A kernel's launch with Shape s, for `items` items.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  Launch(const Shape& s, int64_t items, size_t smem, cudaStream_t st) {
+    cfg.gridDim = dim3((unsigned)s.ctas(items));
+    cfg.blockDim = dim3(s.threads());
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s.N;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = s.N > 1 ? 1 : 0;
+  }
+  Launch(const Launch&) = delete;
+};
+template <class K, class Items>
+cudaError_t launch(K kern, const NormArgs& a, const Items& it, const Shape& s, size_t smem, cudaStream_t st) {
+  const cudaError_t e = allow_ring(kern, smem, s.ctas(a.items) > a.sms);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * warps_of(s), smem, st>>>(a, it);
-  return cudaGetLastError();
+  if (s.N > 1) g_clusters = true;
+  Launch l(s, a.items, smem, st);
+  return cudaLaunchKernelEx(&l.cfg, kern, a, it);
 }
 
-template <class R, int V, class Items>
-cudaError_t fwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  if constexpr (V == 1)
-    if (s.L < 32) return a.y8 ? fwd<R, V, true, false, true>(a, it, s, st) : fwd<R, V, false, false, true>(a, it, s, st);
-  if constexpr (V >= 2)
-    if (s.W > kMaxGroups) return a.y8 ? fwd<R, V, true, true, false>(a, it, s, st) : fwd<R, V, false, true, false>(a, it, s, st);
-  if constexpr (V <= 2)
-    return a.y8 ? fwd<R, V, true, false, false>(a, it, s, st) : fwd<R, V, false, false, false>(a, it, s, st);
-  return cudaErrorInvalidValue;  // V = 4 has more warps
+template <class R, int V>
+size_t smem_fwd(const Shape& s) {
+  return (size_t)s.threads() * kRingFwd * V * (16 + sizeof(R));
 }
+template <class R, int V, bool k8>
+size_t smem_bwd(const Shape& s) {
+  constexpr int kVec = sizeof(R) / 16 + 1 + Held<R, k8>::kPieces;
+  return (size_t)s.threads() * V * 16 * (kRingBwd<sizeof(R) == 32> * kVec + Params<V>::kPieces);
+}
+
+// Clusters of Shape s that the device runs at once, by the variant that needs
+// most: which SMs a cluster may share is the device's, so it is asked once.
+template <bool kBwd>
+int clusters_at_once(const Shape& s) {
+  static std::atomic<int> known[64][kMaxCtas + 1][kMaxGroups + 1];
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  std::atomic<int>& k = known[dev][s.N][s.warps()];
+  if ((n = k.load()) > 0) return n;
+  using vec::F32;
+  auto ask = [&](auto kern, size_t smem) {
+    const cudaError_t e = allow_ring(kern, smem, true);
+    Launch l(s, 1, smem, nullptr);
+    return e == cudaSuccess ? cudaOccupancyMaxActiveClusters(&n, kern, &l.cfg) : e;
+  };
+  const cudaError_t e = kBwd ? ask(residual_norm_bwd<F32, 2, false, kCluster, UniformItems>, smem_bwd<F32, 2, false>(s))
+                             : ask(residual_norm_fwd<F32, 2, true, kCluster, UniformItems>, smem_fwd<F32, 2>(s));
+  if (e != cudaSuccess || n < 1) return 1;
+  k.store(n);
+  return n;
+}
+
+// Calls fn with the type of the stream, the vectors a thread and who shares a row.
+template <class Fn>
+cudaError_t with_shape(const Shape& s, bool f32, Fn fn) {
+  using std::integral_constant;
+  auto rows = [&](auto r) {
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    if (s.row == kLanes) return fn(r, one, integral_constant<Row, kLanes>());
+    if (s.row == kWide) return fn(r, two, integral_constant<Row, kWide>());
+    if (s.row == kCluster) return fn(r, two, integral_constant<Row, kCluster>());
+    return s.V == 1 ? fn(r, one, integral_constant<Row, kWarps>()) : fn(r, two, integral_constant<Row, kWarps>());
+  };
+  return f32 ? rows(vec::F32()) : rows(vec::Bf16());
+}
+
 template <class Items>
 cudaError_t fwd_all(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  if (s.V == 1) return a.f32 ? fwd_c<vec::F32, 1>(a, it, s, st) : fwd_c<vec::Bf16, 1>(a, it, s, st);
-  if (s.V == 2) return a.f32 ? fwd_c<vec::F32, 2>(a, it, s, st) : fwd_c<vec::Bf16, 2>(a, it, s, st);
-  return a.f32 ? fwd_c<vec::F32, 4>(a, it, s, st) : fwd_c<vec::Bf16, 4>(a, it, s, st);
+  return with_shape(s, a.f32, [&](auto r, auto v, auto row) {
+    using R = decltype(r);
+    constexpr int V = decltype(v)::value;
+    constexpr Row kRow = decltype(row)::value;
+    const size_t smem = smem_fwd<R, V>(s);
+    return a.y8 ? launch(residual_norm_fwd<R, V, true, kRow, Items>, a, it, s, smem, st)
+                : launch(residual_norm_fwd<R, V, false, kRow, Items>, a, it, s, smem, st);
+  });
 }
 
-template <class R, int V, bool k8, int kT, bool kNarrow, class Items>
-cudaError_t bwd(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  auto kern = residual_norm_bwd<R, V, k8, kT, kNarrow, Items>;
-  constexpr int kVec = sizeof(R) / 16 + 1 + Held<R, k8>::kPieces;
-  const size_t smem = (size_t)32 * warps_of(s) * V * 16 *
-                      (ring_bwd<V, kT, kVec, sizeof(R) == 32>() * kVec + kKeptPieces<V, kT>);
-  const cudaError_t e = allow_ring(kern, smem, a.items / s.G > a.sms);
-  if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((a.items + s.G - 1) / s.G), 32 * warps_of(s), smem, st>>>(a, it);
-  return cudaGetLastError();
-}
-template <class R, int V, class Items>
-cudaError_t bwd_c(const NormArgs& a, const Items& it, const Shape& s, cudaStream_t st) {
-  auto go = [&](auto t, auto narrow) {
-    constexpr int kT = decltype(t)::value;
-    constexpr bool kN = decltype(narrow)::value;
-    return a.y8 ? bwd<R, V, true, kT, kN>(a, it, s, st) : bwd<R, V, false, kT, kN>(a, it, s, st);
-  };
-  using std::integral_constant;
-  const std::false_type no;
-  if constexpr (V == 1) {
-    if (s.L < 32) return go(integral_constant<int, 128>(), std::true_type());
-    return go(integral_constant<int, 128>(), no);
-  } else if constexpr (V == 2) {
-    if (s.W <= 4) return go(integral_constant<int, 128>(), no);
-    if (s.W <= 6) return go(integral_constant<int, 192>(), no);
-    if (s.W <= 8) return go(integral_constant<int, 256>(), no);
-    return go(integral_constant<int, 512>(), no);
-  } else {
-    return go(integral_constant<int, 512>(), no);
-  }
-}
 template <class Items>
 cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shape& s, cudaStream_t st) {
-  cudaError_t e;
-  if (s.V == 1)
-    e = a.f32 ? bwd_c<vec::F32, 1>(a, it, s, st) : bwd_c<vec::Bf16, 1>(a, it, s, st);
-  else if (s.V == 2)
-    e = a.f32 ? bwd_c<vec::F32, 2>(a, it, s, st) : bwd_c<vec::Bf16, 2>(a, it, s, st);
-  else
-    e = a.f32 ? bwd_c<vec::F32, 4>(a, it, s, st) : bwd_c<vec::Bf16, 4>(a, it, s, st);
+  const cudaError_t e = with_shape(s, a.f32, [&](auto r, auto v, auto row) {
+    using R = decltype(r);
+    constexpr int V = decltype(v)::value;
+    constexpr Row kRow = decltype(row)::value;
+    auto go = [&](auto eight) {
+      constexpr bool k8 = decltype(eight)::value;
+      return launch(residual_norm_bwd<R, V, k8, kRow, Items>, a, it, s, smem_bwd<R, V, k8>(s), st);
+    };
+    return a.y8 ? go(std::true_type()) : go(std::false_type());
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.width + kSumCols - 1) / kSumCols));
@@ -876,10 +969,12 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Splits the rows: about one item per row group that runs at once, none
 // across frames.  Depends on the shape and the device alone.
-NormItems split(int64_t rows, const Shape& s, const int32_t* spans, int n_frames, int64_t span, int sms, int per_sm) {
-  // per_sm is in CTAs of four warps (which fix the registers a thread).
-  const int ctas = std::max(1, per_sm * kMaxGroups / warps_of(s));
-  const int64_t want = std::max<int64_t>(n_frames, (int64_t)ctas * sms * s.G);
+template <bool kBwd>
+NormItems split(int64_t rows, const Shape& s, const int32_t* spans, int n_frames, int64_t span, int sms) {
+  // In CTAs of four warps (which fix the registers a thread).
+  constexpr int per_sm = kBwd ? kBwdPerSm : kFwdPerSm;
+  const int ctas = std::max(1, per_sm * kMaxGroups / s.warps());
+  const int64_t want = std::max<int64_t>(n_frames, s.N > 1 ? clusters_at_once<kBwd>(s) : (int64_t)ctas * sms * s.G);
   auto count = [&](int64_t chunk) {
     if (!spans) return (int64_t)n_frames * ((span + chunk - 1) / chunk);
     int64_t n = 0;
@@ -915,29 +1010,42 @@ cudaError_t with_items(const NormItems& n, const int32_t* spans, int n_frames, i
 
 cudaError_t launch_residual_norm(NormArgs a, const int32_t* spans, int n_frames, int64_t span, int sms,
                                  cudaStream_t st) {
-  const Shape s = shape_of(a.width);
-  const NormItems n = split(a.rows, s, spans, n_frames, span, sms, kFwdPerSm);
+  const Shape s = shape_of(a.width, kWideFwd);
+  const NormItems n = split<false>(a.rows, s, spans, n_frames, span, sms);
   a.warps = s.W;
   a.lanes = s.L;
   a.groups = s.G;
+  a.ctas = s.N;
   a.items = n.items;
   a.sms = sms;
   return with_items(n, spans, n_frames, span, [&](const auto& it) { return fwd_all(a, it, s, st); });
 }
 
+cudaError_t residual_norm_gave_up(bool* gave_up) {
+  *gave_up = false;
+  if (!g_clusters) return cudaSuccess;
+  unsigned int e = 0;
+  const cudaError_t rc = cudaMemcpyFromSymbol(&e, g_gave_up, sizeof(e));
+  if (rc != cudaSuccess || !e) return rc;
+  *gave_up = true;
+  e = 0;
+  return cudaMemcpyToSymbol(g_gave_up, &e, sizeof(e));
+}
+
 NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms) {
-  NormItems r = split(rows, shape_of(width), spans, n_frames, span, sms, kBwdPerSm);
+  NormItems r = split<true>(rows, shape_of(width, kWideBwd), spans, n_frames, span, sms);
   r.bytes = 2 * align256(r.items * width * 4);
   return r;
 }
 
 cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const int32_t* spans, int n_frames,
                                           int64_t span, int sms, void* workspace, cudaStream_t st) {
-  const Shape s = shape_of(a.width);
+  const Shape s = shape_of(a.width, kWideBwd);
   a.sms = sms;
   a.warps = s.W;
   a.lanes = s.L;
   a.groups = s.G;
+  a.ctas = s.N;
   a.items = n.items;
   a.z_part = static_cast<float*>(workspace);
   a.d_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(n.items * a.width * 4));

@@ -423,7 +423,9 @@ int fas_backward(const void* q, const void* k, const void* v, const void* out, c
  * supported.  width: a multiple of 8 (of 32 with checkpoints), at most
  * 16384 (FAS_ERR_UNSUPPORTED above); eps >= 0; tokens >= 1.  Pointers
  * 16-byte aligned (scales: any).  Sums are fp32.  Asynchronous on
- * cuda_stream; allocates nothing. */
+ * cuda_stream; allocates nothing.  Should CTAs that share a wide row ever not
+ * reach one another, the rows left hold NaN and fas_status (with a plan)
+ * reports FAS_ERR_TIMEOUT. */
 int fas_residual_norm(const void* y, const void* x, int residual, const float* gate, const float* gamma_post,
                       const float* gamma_pre, float alpha, float eps, int64_t tokens, int width,
                       const int32_t* frame_tokens, int n_frames, void* x_out, void* h, float* rstd, uint8_t* y_codes,

@@ -372,6 +372,60 @@ def test_checkpoints_from_the_forward_and_in_the_backward(spans, width, residual
     c.check_backward(got, fas.fas_checkpoint_unpack(y8, torch.float32), fas.fas_checkpoint_unpack(x8, torch.float32), rstd)
 
 
+@pytest.mark.parametrize("residual", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("spans,width", [([3, 3, 3], 6656), ([1] * 400, 4104), ([2, 9], 11264), ([700], 9216), ([40, 1], 14336),
+                                         ([1], 16376), ([1000, 7], 4352), ([150] * 2, 2560)],
+                         ids=lambda v: str(v) if isinstance(v, int) else f"{len(v)}x{v[0]}")
+def test_rows_over_several_ctas(spans, width, residual):
+    """Clusters of two to eight CTAs of two to four warps, more rows and more
+    frames than the clusters that run at once."""
+    c = Norm(spans, width, residual, True, seed=4)
+    x, h, rstd = c.forward()
+    c.check_forward(x, h, rstd)
+    got = fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, x, rstd, c.post, c.pre, **c.kw)
+    c.check_backward(got, c.y, x, rstd)
+    if width % 32 == 0:
+        x2, h2, rstd2, y8, x8 = c.forward(checkpoint=True)
+        assert torch.equal(x2, x) and torch.equal(h2, h) and torch.equal(rstd2, rstd)
+        for t, c8 in ((c.y, y8), (x, x8)):
+            want = fas.fas_checkpoint_pack(t)
+            assert torch.equal(c8.codes.view(torch.uint8), want.codes.view(torch.uint8)) and torch.equal(c8.scales, want.scales)
+        got = fas.fas_residual_norm_backward(c.dx_out, c.dh, y8, x8, rstd, c.post, c.pre, **c.kw)
+        c.check_backward(got, fas.fas_checkpoint_unpack(y8, torch.float32), fas.fas_checkpoint_unpack(x8, torch.float32), rstd)
+
+
+def test_rows_over_several_ctas_on_several_streams():
+    """Clusters of different sizes that share the SMs, eager and captured."""
+    plan([48] * 3, 0, 1, 2, 128)
+    cases, want, graphs = [], [], []
+    for width in (4608, 8192, 16384):
+        c = Norm([90, 211], width, torch.bfloat16, True, seed=width)
+        x, h, rstd = c.forward()
+        cases.append(c)
+        want.append((x, h, rstd, *fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, x, rstd, c.post, c.pre, **c.kw)))
+        graphs.append(torch.cuda.CUDAGraph())
+    outs = []
+    for c, gr in zip(cases, graphs):
+        with torch.cuda.graph(gr):
+            fw = c.forward()
+            bw = fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, fw[0], fw[2], c.post, c.pre, **c.kw)
+        outs.append((*fw, *bw))
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        eager = []
+        for i, (c, gr) in enumerate(zip(cases, graphs)):
+            with torch.cuda.stream(streams[i]):
+                gr.replay()
+            with torch.cuda.stream(streams[i + 3]):
+                fw = c.forward()
+                eager.append((*fw, *fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, fw[0], fw[2], c.post, c.pre, **c.kw)))
+        torch.cuda.synchronize()
+        for got in (outs, eager):
+            assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    assert fas.fas_status() == fas.FAS_OK
+
+
 def test_residual_norm_in_place_streams_and_graphs():
     c = Norm([200, 56, 300], 1536, torch.bfloat16, True)
     x, h, rstd = c.forward()
