@@ -568,14 +568,17 @@ def _norm_frames(tokens: int, width: int, gate, frame_tokens, device: int):
         if n == 0 or tokens % n:
             raise ValueError(f"{tokens} tokens are not {n} equal frames (one per row of gate)")
         return ptr, None, n
-    if isinstance(frame_tokens, int) or np.ndim(frame_tokens) == 0:
-        if n * int(frame_tokens) != tokens:
-            raise ValueError(f"gate has {n} frames of {frame_tokens} tokens; x has {tokens} tokens")
-        return ptr, None, n
-    spans = np.ascontiguousarray(frame_tokens, dtype=np.int32)
-    if spans.ndim != 1 or len(spans) != n or int(spans.sum(dtype=np.int64)) != tokens:
+    if not isinstance(frame_tokens, (list, tuple)):
+        if np.ndim(frame_tokens) == 0:
+            if n * int(frame_tokens) != tokens:
+                raise ValueError(f"gate has {n} frames of {frame_tokens} tokens; x has {tokens} tokens")
+            return ptr, None, n
+    if not (isinstance(frame_tokens, (list, tuple)) and all(type(t) is int for t in frame_tokens)):
+        spans = np.asarray(frame_tokens, dtype=np.int32)
+        frame_tokens = spans.tolist() if spans.ndim == 1 else ()
+    if len(frame_tokens) != n or sum(frame_tokens) != tokens or min(frame_tokens) < 0:
         raise ValueError(f"frame_tokens must hold {n} spans (one per row of gate) that add up to {tokens} tokens")
-    return ptr, spans, n
+    return ptr, (ctypes.c_int32 * n)(*frame_tokens), n
 
 
 @functools.lru_cache(maxsize=256)
@@ -617,7 +620,7 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
         parts = (*held[0], *held[1])
         ptrs = [t.data_ptr() for t in parts]
     rc = load().fas_residual_norm(py, px, residual, pgate, ppost, ppre, alpha, eps, N, C,
-                                  None if spans is None else spans.ctypes.data, frames, px_out, ph, rstd.data_ptr(),
+                                  spans, frames, px_out, ph, rstd.data_ptr(),
                                   *ptrs, _on(stream, current))
     if rc:
         _check("fas_residual_norm", rc)
@@ -655,12 +658,12 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
     args[-3], spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
     dx, pdx = _output("dx", dx, dx_out, device)
     dy, pdy = _output("dy", dy, dh, device)
-    need = _norm_workspace(N, C, None if spans is None else spans.tobytes(), frames, device)
+    need = _norm_workspace(N, C, None if spans is None else bytes(spans), frames, device)
     workspace = torch.empty(need, dtype=torch.uint8, device=dx_out.device)
     dpost, dpre = torch.empty_like(gamma_post), torch.empty_like(gamma_pre)
     dgate = None if gate is None else torch.empty_like(gate)
     rc = load().fas_residual_norm_backward(
-        *args, alpha, N, C, None if spans is None else spans.ctypes.data, frames,
+        *args, alpha, N, C, spans, frames,
         pdx, pdy,
         None if dgate is None else dgate.data_ptr(), dpost.data_ptr(), dpre.data_ptr(), workspace.data_ptr(), need,
         _on(stream, current))

@@ -394,6 +394,17 @@ def test_rows_over_several_ctas(spans, width, residual):
         c.check_backward(got, fas.fas_checkpoint_unpack(y8, torch.float32), fas.fas_checkpoint_unpack(x8, torch.float32), rstd)
 
 
+def test_residual_norm_takes_spans_of_any_integer_sequence():
+    c = Norm([3, 9, 4], 64, torch.bfloat16, True)
+    want = c.forward()
+    for spans in ((3, 9, 4), np.array([3, 9, 4]), [np.int64(3), 9, np.int32(4)], torch.tensor([3, 9, 4])):
+        got = fas.fas_residual_norm(c.y, c.x, c.post, c.pre, gate=c.gate, frame_tokens=spans, alpha=c.alpha)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for spans in ([2**32 + 3, 9, 4 - 2**32], [[3, 9, 4]], [-3, 15, 4], [3, 9], ()):
+        with pytest.raises((ValueError, OverflowError)):
+            fas.fas_residual_norm(c.y, c.x, c.post, c.pre, gate=c.gate, frame_tokens=spans, alpha=c.alpha)
+
+
 def test_rows_over_several_ctas_on_several_streams():
     """Clusters of different sizes that share the SMs, eager and captured."""
     plan([48] * 3, 0, 1, 2, 128)
