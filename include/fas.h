@@ -444,8 +444,9 @@ int fas_residual_norm(const void* y, const void* x, int residual, const float* g
  * dgamma_post, dgamma_pre: fp32 [width].  workspace: device memory of at
  * least fas_residual_norm_backward_workspace bytes (FAS_ERR_SCRATCH if
  * smaller), the call's own until it has run.  Column sums are added in a
- * fixed order: results are bit-reproducible on one device type.  Other
- * arguments and limits as fas_residual_norm.  Two kernels, asynchronous on
+ * fixed order: results are bit-reproducible on one device (the rows are
+ * split by its SMs and the clusters that it runs at once).  Other arguments
+ * and limits as fas_residual_norm.  Two kernels, asynchronous on
  * cuda_stream. */
 int fas_residual_norm_backward(const void* dx_out, const void* dh, const void* y, const void* x_out, int residual,
                                const uint8_t* y_codes, const uint8_t* y_scales, const uint8_t* x_codes,
