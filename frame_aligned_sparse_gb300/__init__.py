@@ -41,6 +41,7 @@ LAYOUTS = {"hnd": 0, "nhd": 1}  # q, k, v, out as [H, N, d] or [N, H, d]
 PROLOGUE_LAYOUTS = {"hnd": 0, "nhd": 1, "a2a": 2}  # fas_prologue's outputs (a2a: [G, P, n, H/(G*P), d])
 RMS_EPS = 1e-6
 CHECKPOINT_BLOCK = 32  # elements of a checkpoint that share one scale
+BACKWARD_WORKSPACE = 32  # FAS_BACKWARD_WORKSPACE: bytes a row and head
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -140,6 +141,42 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _LIB = lib
     return _LIB
+
+
+_HOST = None
+
+
+def _host():
+    """The operators' calls on torch tensors in native code (csrc/host), bound
+    to the loaded library."""
+    global _HOST
+    if _HOST is None:
+        import importlib.machinery
+        import importlib.util
+        import torch  # its libraries, which the module uses  # noqa: F401
+        lib = load()
+        path = os.path.join(os.path.dirname(library_path()), "_host.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m frame_aligned_sparse_gb300.build`.")
+        loader = importlib.machinery.ExtensionFileLoader("_host", path)
+        host = importlib.util.module_from_spec(importlib.util.spec_from_loader("_host", loader))
+        loader.exec_module(host)
+        host.bind(*(ctypes.cast(getattr(lib, f"fas_{name}"), ctypes.c_void_p).value for name in (
+            "backward", "residual_norm", "residual_norm_backward", "residual_norm_backward_workspace",
+            "checkpoint_pack", "checkpoint_unpack")))
+        _HOST = host
+    return _HOST
+
+
+def _native(call: str, first, *args):
+    """The call's results from native code, or None if it is not a plain one
+    (see csrc/host/calls.cpp) and the caller has to go on by itself."""
+    if not getattr(first, "is_cuda", False):
+        return None
+    got = getattr(_HOST or _host(), call)(*args)
+    if type(got) is int:
+        _check(f"fas_{call}", got)
+    return got
 
 
 def _check(call: str, rc: int) -> None:
@@ -462,6 +499,10 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
     (bf16, the plan's layout).  Returns (dq, dk, dv)."""
     import torch
     shape, lse_shape, bf16 = _qkv_shape(), _lse_shape(), torch.bfloat16
+    if dq is None and dk is None and dv is None and stream is None:
+        got = _native("backward", q, q, k, v, out, lse, dout, shape, lse_shape, BACKWARD_WORKSPACE)
+        if got is not None:
+            return got
     device, current = _current("q", q)
     ptrs = [_check_here("q", q, shape, bf16, device), _check_here("k", k, shape, bf16, device),
             _check_here("v", v, shape, bf16, device), _check_here("out", out, shape, bf16, device),
@@ -473,7 +514,7 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
     ptrs.append(p)
     dv, p = _output("dv", dv, q, device)
     ptrs.append(p)
-    workspace = torch.empty((32, *lse_shape), dtype=torch.uint8, device=q.device)  # FAS_BACKWARD_WORKSPACE
+    workspace = torch.empty((BACKWARD_WORKSPACE, *lse_shape), dtype=torch.uint8, device=q.device)
     rc = load().fas_backward(*ptrs, workspace.data_ptr(), _on(stream, current))
     _check("fas_backward", rc)
     if stream is not None:
@@ -525,6 +566,10 @@ def _check_checkpoint(name, c, device: int, shape=None):
 def fas_checkpoint_pack(x, out: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
     """Holds x (bf16 or fp32, contiguous, last axis a multiple of 32) in 8
     bits: see ``fas_checkpoint_pack`` in fas.h."""
+    if out is None and stream is None:
+        got = _native("checkpoint_pack", x, x)
+        if got is not None:
+            return Checkpoint(*got)
     dtype = _dtype_code("x", x)
     device, current = _current("x", x)
     ptr = _check_here("x", x, x.shape, x.dtype, device)
@@ -541,6 +586,10 @@ def fas_checkpoint_unpack(c: Checkpoint, dtype=None, out=None, stream=None):
     import torch
     if not isinstance(c, tuple) or len(c) != 2:
         raise TypeError("c must be a Checkpoint (codes, scales)")
+    if out is None and stream is None:
+        got = _native("checkpoint_unpack", c[0], c, dtype)
+        if got is not None:
+            return got[0]
     device, current = _current("c.codes", c[0])
     c, ptrs = _check_checkpoint("c", c, device)
     shape = c.codes.shape
@@ -601,6 +650,10 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
     Returns (x', h, rstd [2, N]), and with ``checkpoint`` also the 8-bit
     Checkpoints of y and of x'."""
     import torch
+    if x_out is None and h is None and stream is None:
+        got = _native("residual_norm", x, y, x, gamma_post, gamma_pre, gate, frame_tokens, alpha, eps, checkpoint)
+        if got is not None:
+            return (*got[:3], Checkpoint(*got[3:5]), Checkpoint(*got[5:])) if checkpoint else got
     residual = _dtype_code("x", x)
     if x.ndim != 2:
         raise ValueError(f"x must be [tokens, width], got {tuple(x.shape)}")
@@ -637,6 +690,11 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
     and dy may be dh.  Returns (dx, dy, dgamma_post, dgamma_pre, dgate), dgate
     None without a gate."""
     import torch
+    if dx is None and dy is None and stream is None:
+        got = _native("residual_norm_backward", dx_out, dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre, gate,
+                      frame_tokens, alpha)
+        if got is not None:
+            return got
     residual = _dtype_code("dx_out", dx_out)
     if dx_out.ndim != 2:
         raise ValueError(f"dx_out must be [tokens, width], got {tuple(dx_out.shape)}")

@@ -1,4 +1,5 @@
-"""Builds libfas.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libfas.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_host.so (its calls on torch tensors) with the host compiler.
 
 Usage: ``python -m frame_aligned_sparse_gb300.build`` or ``build()``.
 Translation units compile in parallel; the shared object lands next to this
@@ -7,10 +8,12 @@ file.  Objects go to ``_build/`` (git-ignored).
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfas.so")
+HOST_SRC = os.path.join(CSRC, "host", "calls.cpp")
+HOST_OUT = os.path.join(PKG, "_host.so")
 BUILD = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -34,23 +39,43 @@ def _sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
+def _host_command(out: str) -> list:
+    """Compiles _host.so against the installed torch, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found: _host.so is built against it")
+    torch = spec.submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    includes = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", HOST_SRC, "-o", out] + ["-I" + i for i in includes] +
+            ["-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+
+
+def _torch_version() -> str:
+    spec = importlib.util.find_spec("torch")
+    path = os.path.join(spec.submodule_search_locations[0], "version.py") if spec else ""
+    return open(path).read() if os.path.exists(path) else ""
+
+
 def _fingerprint() -> str:
     h = hashlib.sha256()
     files = _sources() + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh")))
-    files.append(os.path.join(INCLUDE, "fas.h"))
+    files += [os.path.join(INCLUDE, "fas.h"), HOST_SRC]
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
     h.update(" ".join(ARCH + FLAGS).encode())
     h.update(os.uname().machine.encode())
+    h.update((" ".join(_host_command("")) + _torch_version()).encode())
     return h.hexdigest()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     stamp = os.path.join(BUILD, "stamp")
     fp = _fingerprint()
-    if not force and os.path.exists(OUT) and os.path.exists(stamp) and open(stamp).read() == fp:
+    if not force and os.path.exists(OUT) and os.path.exists(HOST_OUT) and os.path.exists(stamp) and open(stamp).read() == fp:
         return OUT
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -65,9 +90,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(res.stdout + res.stderr, file=sys.stderr)
         return obj
 
+    def compile_host() -> None:
+        tmp = HOST_OUT + ".tmp"
+        res = subprocess.run(_host_command(tmp), capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, HOST_OUT)
+
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
+        host = ex.submit(compile_host)
         objs = list(ex.map(compile_one, srcs))
+        host.result()
     tmp = OUT + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -497,6 +497,70 @@ def test_residual_norm_zero_rows():
     c.check_backward(got, c.y, x, rstd)
 
 
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+@pytest.mark.parametrize("held", [True, False], ids=["8bit", "tensors"])
+def test_plain_calls_take_native_code_and_give_the_same(held, gated, monkeypatch):
+    """A call without outputs or stream is made by native code, one with them
+    step by step in Python: the same results, types and shapes."""
+    c = Norm([5, 90, 31], 256, torch.float32, gated)
+    native = []
+    real = fas._native
+    monkeypatch.setattr(fas, "_native", lambda call, *a: native.append((call, real(call, *a))) or native[-1][1])
+    x, h, rstd, y8, x8 = c.forward(checkpoint=True)
+    y, xo = (y8, x8) if held else (c.y, x)
+    post, pre = torch.nn.Parameter(c.post), torch.nn.Parameter(c.pre)
+    got = fas.fas_residual_norm_backward(c.dx_out, c.dh, y, xo, rstd, post, pre, **c.kw)
+    p8 = fas.fas_checkpoint_pack(x)
+    un = [fas.fas_checkpoint_unpack(p8, t) for t in (None, torch.bfloat16, torch.float32)]
+    assert len(native) == 6 and all(r is not None for _, r in native)
+    assert isinstance(p8, fas.Checkpoint) and isinstance(y8, fas.Checkpoint) and not got[2].requires_grad
+    del native[:]
+    e = torch.empty_like
+    x2, h2, r2, y82, x82 = c.forward(checkpoint=True, x_out=e(c.x), h=e(c.y))
+    want = fas.fas_residual_norm_backward(c.dx_out, c.dh, y, xo, rstd, c.post, c.pre, **c.kw, dx=e(c.dx_out), dy=e(c.dh))
+    p82 = fas.fas_checkpoint_pack(x, out=fas.Checkpoint(e(p8.codes), e(p8.scales)))
+    un2 = [fas.fas_checkpoint_unpack(p8, out=e(u)) for u in un]
+    assert not native
+    flat = lambda *ts: [t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t for t in ts if t is not None]
+    for a, b in zip(flat(x, h, rstd, *y8, *x8, *got, *p8, *un), flat(x2, h2, r2, *y82, *x82, *want, *p82, *un2), strict=True):
+        assert a.dtype == b.dtype and a.shape == b.shape and a.device == b.device and torch.equal(a, b)
+    assert (got[4] is None) == (not gated)
+
+
+def test_native_calls_run_on_the_current_stream_and_in_several_threads():
+    """Each thread's stream, and the memory of a call's own buffers."""
+    import threading
+    cases = [Norm([200 + i, 100], 1024, torch.bfloat16, True, seed=i) for i in range(4)]
+    step = lambda c: (lambda f: (*f, *fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, f[0], f[2], c.post, c.pre, **c.kw)))(c.forward())
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, w):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                got = step(c)
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                    bad.append(c)
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_attention_backward_native_and_with_outputs():
+    c = Attention([48, 64, 16], 1, 1, 2, 64)
+    got = c.run()
+    want = c.run(dq=torch.empty_like(c.q), dk=torch.empty_like(c.q), dv=torch.empty_like(c.q))
+    assert all(torch.equal(got[name], want[name]) for name in want)
+    with pytest.raises(ValueError):
+        c.run(dq=torch.empty_like(c.q)[:1])
+
+
 def test_offsets_beyond_32_bits():
     """Tensors of more than 2^31 elements: their last rows as if alone."""
     n, c = 1_100_000, 2048

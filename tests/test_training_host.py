@@ -171,3 +171,11 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fas.fas_checkpoint_pack(x.half())
     with pytest.raises(TypeError):
         fas.fas_checkpoint_unpack(x)
+
+
+def test_native_calls_load_without_a_gpu():
+    host = fas._host()
+    assert all(callable(getattr(host, f"{n}")) for n in (
+        "backward", "residual_norm", "residual_norm_backward", "checkpoint_pack", "checkpoint_unpack"))
+    with pytest.raises(TypeError):
+        host.bind(1, 2)
