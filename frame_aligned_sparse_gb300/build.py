@@ -15,6 +15,7 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfas.so")
 HOST_SRC = os.path.join(CSRC, "host", "calls.cpp")
 HOST_OUT = os.path.join(PKG, "_host.so")
+HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 BUILD = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -39,23 +41,18 @@ def _sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
-def _host_command(out: str) -> list:
-    """Compiles _host.so against the installed torch, without importing it."""
+def _torch() -> Optional[str]:
+    """The installed torch's folder, without importing it (a slow import)."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found: _host.so is built against it")
-    torch = spec.submodule_search_locations[0]
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _host_command(torch: str, out: str) -> list:
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     includes = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
-    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", HOST_SRC, "-o", out] + ["-I" + i for i in includes] +
-            ["-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
-
-
-def _torch_version() -> str:
-    spec = importlib.util.find_spec("torch")
-    path = os.path.join(spec.submodule_search_locations[0], "version.py") if spec else ""
-    return open(path).read() if os.path.exists(path) else ""
+    return (["g++", HOST_SRC, "-o", out] + ["-I" + i for i in includes] + ["-L" + os.path.join(torch, "lib")] +
+            HOST_FLAGS)
 
 
 def _fingerprint() -> str:
@@ -68,14 +65,20 @@ def _fingerprint() -> str:
             h.update(fh.read())
     h.update(" ".join(ARCH + FLAGS).encode())
     h.update(os.uname().machine.encode())
-    h.update((" ".join(_host_command("")) + _torch_version()).encode())
+    torch = _torch()
+    if torch:
+        h.update(" ".join([torch] + HOST_FLAGS).encode())
+        with open(os.path.join(torch, "version.py"), "rb") as fh:
+            h.update(fh.read())
     return h.hexdigest()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     stamp = os.path.join(BUILD, "stamp")
     fp = _fingerprint()
-    if not force and os.path.exists(OUT) and os.path.exists(HOST_OUT) and os.path.exists(stamp) and open(stamp).read() == fp:
+    torch = _torch()  # without it libfas.so alone: the C boundary needs none
+    built = os.path.exists(OUT) and (not torch or os.path.exists(HOST_OUT))
+    if not force and built and os.path.exists(stamp) and open(stamp).read() == fp:
         return OUT
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -92,16 +95,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_host() -> None:
         tmp = HOST_OUT + ".tmp"
-        res = subprocess.run(_host_command(tmp), capture_output=True, text=True)
+        res = subprocess.run(_host_command(torch, tmp), capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, HOST_OUT)
 
     srcs = _sources()
     with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
-        host = ex.submit(compile_host)
+        host = ex.submit(compile_host) if torch else None
         objs = list(ex.map(compile_one, srcs))
-        host.result()
+        if host:
+            host.result()
     tmp = OUT + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
