@@ -24,7 +24,8 @@ import numpy as np
 __all__ = [
     "FasError", "PlanInfo", "MODES", "library_path", "load",
     "fas_plan", "fas_plan_describe", "fas_prepass", "fas_forward", "fas_free",
-    "fas_status", "fas_prepass_readback", "fas_selftest_wait_timeout", "fas_last_launch_count",
+    "fas_status", "fas_prepass_readback", "fas_selftest_wait_timeout", "fas_selftest_row_wait_timeout",
+    "fas_last_launch_count",
     "fas_prepass_noalloc", "fas_forward_host", "fas_set_layout", "LAYOUTS", "fas_forward_ablation",
     "fas_prologue", "fas_prologue_fold_weights", "PROLOGUE_LAYOUTS",
     "fas_prologue_with_key_sums", "fas_prepass_with_key_sums", "key_sums_shape",
@@ -105,6 +106,7 @@ _SIGS = {
     "fas_status": (ctypes.c_int, [ctypes.c_void_p]),
     "fas_prepass_readback": (ctypes.c_int, [ctypes.c_void_p] * 6),
     "fas_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
+    "fas_selftest_row_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
     "fas_last_launch_count": (ctypes.c_int, []),
     "fas_prepass_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p] + [ctypes.c_int] * 6 +
                             [ctypes.c_void_p] * 4),
@@ -797,6 +799,10 @@ def fas_prepass_readback(stream=None, row_bound: bool = False) -> dict:
 
 def fas_selftest_wait_timeout(limit_us: int, stream=None) -> int:
     return load().fas_selftest_wait_timeout(limit_us, _stream_handle(stream))
+
+
+def fas_selftest_row_wait_timeout(limit_us: int, stream=None) -> int:
+    return load().fas_selftest_row_wait_timeout(limit_us, _stream_handle(stream))
 
 
 def fas_prepass_noalloc(q, k, frame_tokens: int, n_frames: int, ref_frames: int, window_radius: int,

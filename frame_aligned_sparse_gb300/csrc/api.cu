@@ -1148,21 +1148,34 @@ int fas_prepass_readback(float* mu, float* frame_max, float* stat, uint8_t* elig
   return FAS_OK;
 }
 
-int fas_selftest_wait_timeout(int limit_us, void* cuda_stream) {
+namespace {
+
+// Runs a self-test whose device word is `expected` when its wait ran out as it should.
+int selftest(int limit_us, void* cuda_stream, unsigned int expected,
+             cudaError_t (*launch)(unsigned int*, uint64_t, cudaStream_t)) {
   if (limit_us < 1 || limit_us > 1000000) return FAS_ERR_ARG;
   unsigned int* err = nullptr;
   if (cudaMalloc(&err, sizeof(unsigned int)) != cudaSuccess) return FAS_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   int rc = FAS_ERR_CUDA;
   if (cudaMemsetAsync(err, 0, sizeof(unsigned int), st) == cudaSuccess &&
-      fas::launch_wait_selftest(err, (uint64_t)limit_us * 1000ull, st) == cudaSuccess &&
-      cudaStreamSynchronize(st) == cudaSuccess) {
+      launch(err, (uint64_t)limit_us * 1000ull, st) == cudaSuccess && cudaStreamSynchronize(st) == cudaSuccess) {
     unsigned int e = 0;
     if (cudaMemcpy(&e, err, sizeof(e), cudaMemcpyDeviceToHost) == cudaSuccess)
-      rc = (e & fas::kErrWaitSelftest) ? FAS_ERR_TIMEOUT : FAS_OK;
+      rc = e == expected ? FAS_ERR_TIMEOUT : FAS_OK;
   }
   cudaFree(err);
   return rc;
+}
+
+}  // namespace
+
+int fas_selftest_wait_timeout(int limit_us, void* cuda_stream) {
+  return selftest(limit_us, cuda_stream, fas::kErrWaitSelftest, fas::launch_wait_selftest);
+}
+
+int fas_selftest_row_wait_timeout(int limit_us, void* cuda_stream) {
+  return selftest(limit_us, cuda_stream, 2u, fas::launch_row_wait_selftest);
 }
 
 int fas_last_launch_count(void) { return g_state.last_launches; }

@@ -210,6 +210,7 @@ struct NormArgs {
   int sms = 1;                    // SMs of the device (set by the launcher)
   bool f32 = false;               // residual type
   float alpha = 1.f, eps = 0.f;
+  uint64_t limit_ns = kWaitLimitNs;  // of a wait on the other CTAs of a row
 };
 
 // How the backward pass splits the rows, and its workspace.
@@ -227,6 +228,10 @@ cudaError_t launch_residual_norm_backward(NormArgs a, const NormItems& n, const 
 // Whether a row's wait on the other CTAs of its cluster ran out since the last
 // call (the rows then hold NaN); clears it.  Current device.
 cudaError_t residual_norm_gave_up(bool* gave_up);
+
+// One cluster whose row sums run out of time: 2 in `result` if they became
+// NaN and only they did, and residual_norm_gave_up tells.
+cudaError_t launch_row_wait_selftest(unsigned int* result, uint64_t limit_ns, cudaStream_t stream);
 
 // n elements (a multiple of 32) to and from 8-bit checkpoints.
 cudaError_t launch_checkpoint_pack(const void* x, bool f32, uint8_t* codes, uint8_t* scales, int64_t n,

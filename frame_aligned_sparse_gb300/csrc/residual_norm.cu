@@ -92,7 +92,8 @@ struct Exchange {
     __syncthreads();
   }
   // v's sums over the warps.
-  __device__ __forceinline__ void sum(float (&x)[N], int slot, int, const NormArgs& a, int w, int lane, int group) {
+  __device__ __forceinline__ void sum(float (&x)[N], int slot, int, const NormArgs& a, int w, int lane, int group,
+                                      bool&) {
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[group][slot][i][w] = x[i];
@@ -117,6 +118,14 @@ std::atomic<bool> g_clusters{false};  // a cluster was launched
 // 79% of the copy rate against 54 forward, 76 against 59 backward).  A slot is
 // free again as in one CTA: who sends for call n + 2 has all of call n + 1,
 // which each warp sent after reading call n.
+//
+// All CTAs of a cluster run together, so the waits end.  Should one not, its
+// thread is `lost`: it sets the CTA's and the module's word and from then on
+// neither waits, arrives nor sends, and its sums are NaN.  A phase ends only
+// with every warp's bytes, and a lane that is lost sends none, so no other
+// thread ever takes a sum that lacks some: it has the whole sum, or its own
+// wait runs out too.
+constexpr uint64_t kSettleNs = 1000000;  // for sums in flight to a CTA that has stopped waiting for them
 template <int N>
 struct Exchange<kCluster, N> {
   static constexpr int kPart = N == 1 ? 1 : 4;  // floats a warp sends: one, or three and a pad
@@ -134,9 +143,7 @@ struct Exchange<kCluster, N> {
     __syncwarp();
     ptx::cluster_sync();
   }
-  // All CTAs of a cluster run together, so the wait ends.  Should it not, the
-  // rows that are left become NaN and the module's error word is set.
-  __device__ __forceinline__ bool wait(uint32_t b, int phase) {
+  __device__ __forceinline__ bool wait(uint32_t b, int phase, uint64_t limit_ns) {
     if (ptx::mbar_try_wait_cluster(b, phase & 1)) return true;
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
@@ -145,20 +152,23 @@ struct Exchange<kCluster, N> {
       if (*reinterpret_cast<volatile int*>(&given_up)) return false;
       const uint64_t now = ptx::global_timer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) {
+      if (now - t0 > limit_ns) {
         *reinterpret_cast<volatile int*>(&given_up) = 1;
         atomicOr(&g_gave_up, 1u);
         return false;
       }
     }
   }
-  __device__ __forceinline__ void sum(float (&x)[N], int slot, int phase, const NormArgs& a, int w, int lane, int) {
+  __device__ __forceinline__ void sum(float (&x)[N], int slot, int phase, const NormArgs& a, int w, int lane, int,
+                                      bool& lost) {
     const uint32_t b = ptx::smem_addr(&bar[slot]);
-    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(b, a.warps * kPart * 4);
-    if (lane < a.ctas) ptx::store_async_cluster(ptx::smem_addr(part[slot][w]), b, lane, x);
-    const bool got = wait(b, phase);
+    if (!lost) {
+      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(b, a.warps * kPart * 4);
+      if (lane < a.ctas) ptx::store_async_cluster(ptx::smem_addr(part[slot][w]), b, lane, x);
+      lost = !wait(b, phase, a.limit_ns);
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = got ? 0.f : __int_as_float(0x7fffffff);
+    for (int i = 0; i < N; ++i) x[i] = lost ? __int_as_float(0x7fffffff) : 0.f;
 #pragma unroll 4
     for (int k = 0; k < a.warps; k += 4 / kPart) {  // the row's tail is zero
       const float4 p = *reinterpret_cast<const float4*>(part[slot][k]);
@@ -171,22 +181,30 @@ struct Exchange<kCluster, N> {
       }
     }
   }
-  // No CTA leaves while another may still send to it.
+  // No CTA leaves while another may still send to it.  The barrier has no
+  // limit of its own and needs none: every wait before it has one.  A CTA that
+  // is not lost has waited for all that was sent to it; one that is gives what
+  // the others sent last the time to land.
   __device__ __forceinline__ void finish() {
     __syncwarp();
     ptx::cluster_sync();
+    if (*reinterpret_cast<volatile int*>(&given_up)) {
+      const uint64_t t0 = ptx::global_timer_ns();
+      while (ptx::global_timer_ns() - t0 < kSettleNs) {
+      }
+    }
   }
 };
 template <Row kRow, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], Exchange<kRow, N>& ex, int slot, int phase, const NormArgs& a,
-                                         int w, int lane, int group) {
+                                         int w, int lane, int group, bool& lost) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (kRow != kLanes || o < a.lanes)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (kRow == kLanes || (kRow == kWarps && a.warps == 1)) return;
-  ex.sum(v, slot, phase, a, w, lane, group);
+  ex.sum(v, slot, phase, a, w, lane, group, lost);
 }
 
 // Stages of a row ring: two (forward) or three (backward; two for fp32) cover
@@ -394,6 +412,7 @@ __global__ void __launch_bounds__(kRow == kWide ? 32 * kWideFwd : 128, kRow == k
       for (int e = 0; e < 4; ++e) coef[v][e] = mul2(mul2(coef[v][e], both(a.alpha)), gt[e]);
     }
   }
+  bool lost = false;
   for (int i = 0; i < at.turns; ++i) {
     const bool live = kRow != kLanes || i < n;
     copy_wait<S - 1>();
@@ -415,7 +434,7 @@ __global__ void __launch_bounds__(kRow == kWide ? 32 * kWideFwd : 128, kRow == k
     rd.next();
     load();
     float s[1] = {sum(acc)};
-    row_sums(s, ex, 0, i, a, w, lane, group);
+    row_sums(s, ex, 0, i, a, w, lane, group, lost);
     const float ry = rsqrtf(s[0] * inv_c + a.eps);
     const P2 ry2 = both(ry);
     acc = zero;
@@ -427,7 +446,7 @@ __global__ void __launch_bounds__(kRow == kWide ? 32 * kWideFwd : 128, kRow == k
         acc = fma2(x[v][e], x[v][e], acc);
       }
     s[0] = sum(acc);
-    row_sums(s, ex, 1, i, a, w, lane, group);
+    row_sums(s, ex, 1, i, a, w, lane, group, lost);
     const float rx = rsqrtf(s[0] * inv_c + a.eps);
     const P2 rx2 = both(rx);
 #pragma unroll
@@ -661,6 +680,7 @@ __global__ void __launch_bounds__(kRow == kWide ? 32 * kWideBwd : 128, kRow == k
     }
     params.set(v, c, g);
   }
+  bool lost = false;
   auto row = [&](int i, Small& sm, int slot) {
     P2 y[V][4], x[V][4], t[V][4];
     const bool live = kRow != kLanes || i < n;
@@ -700,7 +720,7 @@ __global__ void __launch_bounds__(kRow == kWide ? 32 * kWideBwd : 128, kRow == k
     load();
     load_small(i + 2, sm);
     float s[3] = {sum(sa), sum(sb), sum(sc)};
-    row_sums(s, ex, slot, i >> 1, a, w, lane, group);
+    row_sums(s, ex, slot, i >> 1, a, w, lane, group, lost);
     const float rm1 = rx * s[0] * inv_c, m2 = (s[1] - rm1 * s[2]) * inv_c;
     const P2 nrm1 = both(-rm1), nm2 = both(-m2);
 #pragma unroll
@@ -913,6 +933,24 @@ int clusters_at_once(const Shape& s) {
   return n;
 }
 
+// A row of four warps in two CTAs: one exchange that all take part in, then
+// some that the second CTA never joins.  Sets bit 0 of `result` for a sum that
+// is not as it should be and bit 1 for one that was given up.
+__global__ void __launch_bounds__(64) row_wait_selftest(const NormArgs a, unsigned int* result) {
+  __shared__ __align__(16) Exchange<kCluster, 3> ex;
+  ex.start();
+  const int rank = (int)ptx::cluster_ctarank(), lane = threadIdx.x % 32, w = rank * 2 + threadIdx.x / 32;
+  bool lost = false;
+  for (int n = 0; n < (rank == 0 ? 6 : 1); ++n) {
+    float s[3] = {w + 1.f, 10.f * (w + 1), 1.f};
+    ex.sum(s, n & 1, n >> 1, a, w, lane, 0, lost);
+    const bool right = s[0] == 10.f && s[1] == 100.f && s[2] == 4.f;
+    const bool nan = s[0] != s[0] && s[1] != s[1] && s[2] != s[2];
+    atomicOr(result, (n == 0 ? right && !lost : nan && lost) ? (n == 0 ? 0u : 2u) : 1u);
+  }
+  ex.finish();
+}
+
 // Calls fn with the type of the stream, the vectors a thread and who shares a row.
 template <class Fn>
 cudaError_t with_shape(const Shape& s, bool f32, Fn fn) {
@@ -1030,6 +1068,17 @@ cudaError_t residual_norm_gave_up(bool* gave_up) {
   *gave_up = true;
   e = 0;
   return cudaMemcpyToSymbol(g_gave_up, &e, sizeof(e));
+}
+
+cudaError_t launch_row_wait_selftest(unsigned int* result, uint64_t limit_ns, cudaStream_t st) {
+  const Shape s = {2, 4, 32, 1, 2, kCluster};
+  NormArgs a;
+  a.warps = s.W;
+  a.ctas = s.N;
+  a.limit_ns = limit_ns;
+  g_clusters = true;
+  Launch l(s, 1, 0, st);
+  return cudaLaunchKernelEx(&l.cfg, row_wait_selftest, a, result);
 }
 
 NormItems residual_norm_items(int64_t rows, int width, const int32_t* spans, int n_frames, int64_t span, int sms) {

@@ -281,6 +281,12 @@ int fas_prepass_readback(float* mu, float* frame_max, float* stat, uint8_t* elig
  * (1..1000000).  Expected result: FAS_ERR_TIMEOUT, with the context intact. */
 int fas_selftest_wait_timeout(int limit_us, void* cuda_stream);
 
+/* The same for the CTAs that share a wide row in fas_residual_norm: one of
+ * two stops taking part.  Expected result: FAS_ERR_TIMEOUT (the sums that
+ * arrived were right and the others NaN), after which fas_status reports
+ * FAS_ERR_TIMEOUT once. */
+int fas_selftest_row_wait_timeout(int limit_us, void* cuda_stream);
+
 /* Bytes of the fixed device array that fas_prepass_noalloc uses as scratch. */
 #define FAS_NOALLOC_SCRATCH_BYTES (4u << 20)
 
@@ -424,8 +430,8 @@ int fas_backward(const void* q, const void* k, const void* v, const void* out, c
  * 16384 (FAS_ERR_UNSUPPORTED above); eps >= 0; tokens >= 1.  Pointers
  * 16-byte aligned (scales: any).  Sums are fp32.  Asynchronous on
  * cuda_stream; allocates nothing.  Should CTAs that share a wide row ever not
- * reach one another, the rows left hold NaN and fas_status (with a plan)
- * reports FAS_ERR_TIMEOUT. */
+ * reach one another within half a second, what hangs on the sums they lack is
+ * NaN, the kernel ends, and fas_status (with a plan) reports FAS_ERR_TIMEOUT. */
 int fas_residual_norm(const void* y, const void* x, int residual, const float* gate, const float* gamma_post,
                       const float* gamma_pre, float alpha, float eps, int64_t tokens, int width,
                       const int32_t* frame_tokens, int n_frames, void* x_out, void* h, float* rstd, uint8_t* y_codes,

@@ -437,6 +437,21 @@ def test_rows_over_several_ctas_on_several_streams():
     assert fas.fas_status() == fas.FAS_OK
 
 
+def test_a_row_whose_ctas_do_not_reach_one_another_is_reported():
+    """A CTA that stops taking part: the other one's sums become NaN after the
+    limit, the kernel ends, the status says so once, and the next call is as
+    before."""
+    plan([48] * 3, 0, 1, 2, 128)
+    c = Norm([5, 40], 8192, torch.float32, True)
+    want = c.forward()
+    assert fas.fas_status() == fas.FAS_OK
+    for limit_us in (2000, 1):
+        assert fas.fas_selftest_row_wait_timeout(limit_us) == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_status() == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_status() == fas.FAS_OK
+    assert all(torch.equal(a, b) for a, b in zip(c.forward(), want))
+
+
 def test_residual_norm_in_place_streams_and_graphs():
     c = Norm([200, 56, 300], 1536, torch.bfloat16, True)
     x, h, rstd = c.forward()

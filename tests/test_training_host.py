@@ -173,6 +173,11 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fas.fas_checkpoint_unpack(x)
 
 
+def test_row_wait_selftest_refuses():
+    assert fas.load().fas_selftest_row_wait_timeout(0, None) == fas.FAS_ERR_ARG
+    assert fas.load().fas_selftest_row_wait_timeout(1000001, None) == fas.FAS_ERR_ARG
+
+
 def test_native_calls_load_without_a_gpu():
     host = fas._host()
     assert all(callable(getattr(host, f"{n}")) for n in (
