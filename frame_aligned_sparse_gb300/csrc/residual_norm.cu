@@ -864,12 +864,14 @@ Shape shape_of(int width, int wide) {
 
 // A kernel's ring: its opt-in shared memory, and, for more CTAs than SMs, the
 // SM's whole share for it (by itself the driver leaves room for fewer CTAs
-// than fit).  Set on every launch: it belongs to the device's context.
+// than fit).  Set on every launch, as it belongs to the device's context, and
+// always to the same value, the ring of the kernel's largest CTA: another
+// thread may be about to launch the kernel with more threads than this call's.
 template <class K>
-cudaError_t allow_ring(K kern, size_t smem, bool many) {
+cudaError_t allow_ring(K kern, size_t most, bool many) {
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024)  // up to 48 KB with the static part goes without
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (most > 40 * 1024)  // up to 48 KB with the static part goes without
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e == cudaSuccess && many)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   return e;
@@ -892,24 +894,26 @@ struct Launch {
   }
   Launch(const Launch&) = delete;
 };
+// thread_bytes: the ring's share of one thread.
 template <class K, class Items>
-cudaError_t launch(K kern, const NormArgs& a, const Items& it, const Shape& s, size_t smem, cudaStream_t st) {
-  const cudaError_t e = allow_ring(kern, smem, s.ctas(a.items) > a.sms);
+cudaError_t launch(K kern, const NormArgs& a, const Items& it, const Shape& s, int most_threads, size_t thread_bytes,
+                   cudaStream_t st) {
+  const cudaError_t e = allow_ring(kern, most_threads * thread_bytes, s.ctas(a.items) > a.sms);
   if (e != cudaSuccess) return e;
   if (s.N > 1) g_clusters = true;
-  Launch l(s, a.items, smem, st);
+  Launch l(s, a.items, s.threads() * thread_bytes, st);
   return cudaLaunchKernelEx(&l.cfg, kern, a, it);
 }
 
+// Threads of the largest CTA of a kind of row.
+template <Row kRow, bool kBwd>
+constexpr int kMostThreads = 32 * (kRow != kWide ? kMaxGroups : kBwd ? kWideBwd : kWideFwd);
+
 template <class R, int V>
-size_t smem_fwd(const Shape& s) {
-  return (size_t)s.threads() * kRingFwd * V * (16 + sizeof(R));
-}
+constexpr size_t kThreadFwd = kRingFwd * V * (16 + sizeof(R));
 template <class R, int V, bool k8>
-size_t smem_bwd(const Shape& s) {
-  constexpr int kVec = sizeof(R) / 16 + 1 + Held<R, k8>::kPieces;
-  return (size_t)s.threads() * V * 16 * (kRingBwd<sizeof(R) == 32> * kVec + Params<V>::kPieces);
-}
+constexpr size_t kThreadBwd =
+    V * 16 * (kRingBwd<sizeof(R) == 32> * (sizeof(R) / 16 + 1 + Held<R, k8>::kPieces) + Params<V>::kPieces);
 
 // Clusters of Shape s that the device runs at once, by the variant that needs
 // most: which SMs a cluster may share is the device's, so it is asked once.
@@ -921,13 +925,13 @@ int clusters_at_once(const Shape& s) {
   std::atomic<int>& k = known[dev][s.N][s.warps()];
   if ((n = k.load()) > 0) return n;
   using vec::F32;
-  auto ask = [&](auto kern, size_t smem) {
-    const cudaError_t e = allow_ring(kern, smem, true);
-    Launch l(s, 1, smem, nullptr);
+  auto ask = [&](auto kern, size_t thread_bytes) {
+    const cudaError_t e = allow_ring(kern, kMostThreads<kCluster, kBwd> * thread_bytes, true);
+    Launch l(s, 1, s.threads() * thread_bytes, nullptr);
     return e == cudaSuccess ? cudaOccupancyMaxActiveClusters(&n, kern, &l.cfg) : e;
   };
-  const cudaError_t e = kBwd ? ask(residual_norm_bwd<F32, 2, false, kCluster, UniformItems>, smem_bwd<F32, 2, false>(s))
-                             : ask(residual_norm_fwd<F32, 2, true, kCluster, UniformItems>, smem_fwd<F32, 2>(s));
+  const cudaError_t e = kBwd ? ask(residual_norm_bwd<F32, 2, false, kCluster, UniformItems>, kThreadBwd<F32, 2, false>)
+                             : ask(residual_norm_fwd<F32, 2, true, kCluster, UniformItems>, kThreadFwd<F32, 2>);
   if (e != cudaSuccess || n < 1) return 1;
   k.store(n);
   return n;
@@ -972,9 +976,9 @@ cudaError_t fwd_all(const NormArgs& a, const Items& it, const Shape& s, cudaStre
     using R = decltype(r);
     constexpr int V = decltype(v)::value;
     constexpr Row kRow = decltype(row)::value;
-    const size_t smem = smem_fwd<R, V>(s);
-    return a.y8 ? launch(residual_norm_fwd<R, V, true, kRow, Items>, a, it, s, smem, st)
-                : launch(residual_norm_fwd<R, V, false, kRow, Items>, a, it, s, smem, st);
+    constexpr int most = kMostThreads<kRow, false>;
+    return a.y8 ? launch(residual_norm_fwd<R, V, true, kRow, Items>, a, it, s, most, kThreadFwd<R, V>, st)
+                : launch(residual_norm_fwd<R, V, false, kRow, Items>, a, it, s, most, kThreadFwd<R, V>, st);
   });
 }
 
@@ -986,7 +990,7 @@ cudaError_t bwd_all(const NormArgs& a, const Items& it, int n_frames, const Shap
     constexpr Row kRow = decltype(row)::value;
     auto go = [&](auto eight) {
       constexpr bool k8 = decltype(eight)::value;
-      return launch(residual_norm_bwd<R, V, k8, kRow, Items>, a, it, s, smem_bwd<R, V, k8>(s), st);
+      return launch(residual_norm_bwd<R, V, k8, kRow, Items>, a, it, s, kMostThreads<kRow, true>, kThreadBwd<R, V, k8>, st);
     };
     return a.y8 ? go(std::true_type()) : go(std::false_type());
   });

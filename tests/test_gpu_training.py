@@ -567,6 +567,37 @@ def test_native_calls_run_on_the_current_stream_and_in_several_threads():
     assert not bad
 
 
+def test_calls_of_several_widths_in_several_threads():
+    """Widths that share a kernel and take rings of different sizes (three and
+    four warps, a CTA of five and six, clusters of CTAs of three and four): no
+    thread's call changes what another's launch may use."""
+    import threading
+    pairs = [(1536, 2048), (2560, 3056), (4608, 8192)]
+    for widths in pairs:
+        cases = [Norm([7, 3], w, torch.bfloat16, True, seed=w) for w in widths]
+        step = lambda c: (lambda f: (*f, *fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, f[0], f[2], c.post, c.pre, **c.kw)))(c.forward())
+        want = [step(c) for c in cases]
+        torch.cuda.synchronize()
+        bad = []
+
+        def work(c, w):
+            try:
+                with torch.cuda.stream(torch.cuda.Stream()):
+                    for _ in range(1500):
+                        got = step(c)
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                        bad.append((widths, "values"))
+            except fas.FasError as e:
+                bad.append((widths, str(e)))
+        threads = [threading.Thread(target=work, args=a) for a in zip(cases * 2, want * 2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not bad
+
+
 def test_attention_backward_native_and_with_outputs():
     c = Attention([48, 64, 16], 1, 1, 2, 64)
     got = c.run()
