@@ -144,7 +144,6 @@ struct Exchange<kCluster, N> {
     ptx::cluster_sync();
   }
   __device__ __forceinline__ bool wait(uint32_t b, int phase, uint64_t limit_ns) {
-    if (ptx::mbar_try_wait_cluster(b, phase & 1)) return true;
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
       if (ptx::mbar_try_wait_cluster(b, phase & 1)) return true;
@@ -162,11 +161,11 @@ struct Exchange<kCluster, N> {
   __device__ __forceinline__ void sum(float (&x)[N], int slot, int phase, const NormArgs& a, int w, int lane, int,
                                       bool& lost) {
     const uint32_t b = ptx::smem_addr(&bar[slot]);
-    if (!lost) {
-      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(b, a.warps * kPart * 4);
-      if (lane < a.ctas) ptx::store_async_cluster(ptx::smem_addr(part[slot][w]), b, lane, x);
-      lost = !wait(b, phase, a.limit_ns);
-    }
+    if (threadIdx.x == 0 && !lost) ptx::mbar_arrive_expect_tx(b, a.warps * kPart * 4);
+    if (lane < a.ctas && !lost) ptx::store_async_cluster(ptx::smem_addr(part[slot][w]), b, lane, x);
+    // The state is touched after a first look at the barrier: in front of it, it cost the backward 2 to 5 points of
+    // the copy rate.
+    if (!ptx::mbar_try_wait_cluster(b, phase & 1) || lost) lost = lost || !wait(b, phase, a.limit_ns);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = lost ? __int_as_float(0x7fffffff) : 0.f;
 #pragma unroll 4
