@@ -193,6 +193,31 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream):
+    """A torch stream for a stream argument (a stream or a handle)."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream_handle(stream)
+    # (Handle 0 is the default stream; an ExternalStream of 0 would be a new one.)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _empty(stream, shape, dtype, device):
+    """A tensor that a call on ``stream`` (None: the current one) writes.
+
+    Its memory is that stream's own: a block of the current stream may have
+    been freed with work on it still queued there, which the call would not
+    wait for.  The current stream, where the caller goes on, is a user too."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_object(stream)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _info(c: _PlanInfoC, table: Optional[np.ndarray] = None) -> PlanInfo:
     if table is None:
         table = np.ctypeslib.as_array(c.host_table, shape=(c.total_frames * 4,)).reshape(-1, 4).copy()
@@ -334,9 +359,9 @@ def fas_forward(q, k, v, out=None, lse=None, mode: str = "auto", stream=None):
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_tensor(name, t, shape, torch.bfloat16)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, shape, torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty(_lse_shape(), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, _lse_shape(), torch.float32, q.device)
     _check_tensor("out", out, shape, torch.bfloat16)
     _check_tensor("lse", lse, _lse_shape(), torch.float32)
     rc = load().fas_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -354,9 +379,9 @@ def fas_forward_ablation(q, k, v, out=None, lse=None, stream=None):
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_tensor(name, t, shape, torch.bfloat16)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, shape, torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty(_lse_shape(), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, _lse_shape(), torch.float32, q.device)
     _check_tensor("out", out, shape, torch.bfloat16)
     _check_tensor("lse", lse, _lse_shape(), torch.float32)
     rc = load().fas_forward_ablation(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -373,7 +398,7 @@ def fas_prologue_fold_weights(w, gamma, out=None, stream=None):
     _check_tensor("w", w, (O, C), torch.bfloat16)
     _check_tensor("gamma", gamma, (C,), torch.float32)
     if out is None:
-        out = torch.empty_like(w)
+        out = _empty(stream, w.shape, w.dtype, w.device)
     _check_tensor("out", out, (O, C), torch.bfloat16)
     _check("fas_prologue_fold_weights",
            load().fas_prologue_fold_weights(w.data_ptr(), gamma.data_ptr(), out.data_ptr(), C, O,
@@ -421,7 +446,7 @@ def _prologue(x, w_folded, cos, sin, heads, head_dim, layout, groups, ranks, q, 
     outs = []
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            t = _empty(stream, shape, torch.bfloat16, x.device)
         _check_tensor(name, t, shape, torch.bfloat16)
         outs.append(t)
     if not sums:
@@ -432,7 +457,7 @@ def _prologue(x, w_folded, cos, sin, heads, head_dim, layout, groups, ranks, q, 
         return tuple(outs)
     ks_shape = key_sums_shape(heads, N, head_dim)
     if key_sums is None:
-        key_sums = torch.empty(ks_shape, dtype=torch.float32, device=x.device)
+        key_sums = _empty(stream, ks_shape, torch.float32, x.device)
     _check_tensor("key_sums", key_sums, ks_shape, torch.float32)
     rc = load().fas_prologue_with_key_sums(x.data_ptr(), w_folded.data_ptr(), cos.data_ptr(), sin.data_ptr(), N, C,
                                            heads, head_dim, float(eps), outs[0].data_ptr(), outs[1].data_ptr(),
@@ -471,11 +496,10 @@ def _current_device_stream() -> Tuple[int, int]:
     return device, torch._C._cuda_getCurrentRawStream(device)
 
 
-def _output(name, t, like, device: int):
+def _output(name, t, like, device: int, stream):
     """An output with like's type and shape, and its address."""
     if t is None:
-        import torch
-        t = torch.empty_like(like)
+        t = _empty(stream, like.shape, like.dtype, like.device)
         return t, t.data_ptr()
     return t, _check_here(name, t, like.shape, like.dtype, device)
 
@@ -484,14 +508,13 @@ def _on(stream, current: int) -> int:
     return current if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _own_until_run(stream, *temps):
-    """Keeps the memory of tensors the binding allocated for a call on
-    another stream than the current one until that stream has used it."""
+def _own_until_run(stream, *outputs):
+    """Keeps the memory of a caller's outputs until the stream of a call has
+    written them."""
     import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+    stream = _stream_object(stream)
     if stream != torch.cuda.current_stream():
-        for t in temps:
+        for t in outputs:
             t.record_stream(stream)
 
 
@@ -510,17 +533,17 @@ def fas_backward(q, k, v, out, lse, dout, dq=None, dk=None, dv=None, stream=None
             _check_here("v", v, shape, bf16, device), _check_here("out", out, shape, bf16, device),
             _check_here("lse", lse, lse_shape, torch.float32, device),
             _check_here("dout", dout, shape, bf16, device)]
-    dq, p = _output("dq", dq, q, device)
+    dq, p = _output("dq", dq, q, device, stream)
     ptrs.append(p)
-    dk, p = _output("dk", dk, q, device)
+    dk, p = _output("dk", dk, q, device, stream)
     ptrs.append(p)
-    dv, p = _output("dv", dv, q, device)
+    dv, p = _output("dv", dv, q, device, stream)
     ptrs.append(p)
-    workspace = torch.empty((BACKWARD_WORKSPACE, *lse_shape), dtype=torch.uint8, device=q.device)
+    workspace = _empty(stream, (BACKWARD_WORKSPACE, *lse_shape), torch.uint8, q.device)
     rc = load().fas_backward(*ptrs, workspace.data_ptr(), _on(stream, current))
     _check("fas_backward", rc)
     if stream is not None:
-        _own_until_run(stream, workspace, dq, dk, dv)
+        _own_until_run(stream, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -542,13 +565,13 @@ def _dtype_code(name, t) -> int:
     raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
 
 
-def _checkpoint_empty(shape, device):
+def _checkpoint_empty(shape, device, stream):
     import torch
     if not shape or shape[-1] % CHECKPOINT_BLOCK or 0 in shape:
         raise ValueError(f"a checkpointed tensor's last axis must be a positive multiple of {CHECKPOINT_BLOCK} "
                          f"and its shape not empty, got {tuple(shape)}")
-    return Checkpoint(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
-                      torch.empty((*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), dtype=torch.uint8, device=device))
+    return Checkpoint(_empty(stream, shape, torch.float8_e4m3fn, device),
+                      _empty(stream, (*shape[:-1], shape[-1] // CHECKPOINT_BLOCK), torch.uint8, device))
 
 
 def _check_checkpoint(name, c, device: int, shape=None):
@@ -575,7 +598,7 @@ def fas_checkpoint_pack(x, out: Optional[Checkpoint] = None, stream=None) -> Che
     dtype = _dtype_code("x", x)
     device, current = _current("x", x)
     ptr = _check_here("x", x, x.shape, x.dtype, device)
-    c = _checkpoint_empty(tuple(x.shape), x.device) if out is None else out
+    c = _checkpoint_empty(tuple(x.shape), x.device, stream) if out is None else out
     c, ptrs = _check_checkpoint("out", c, device, x.shape)
     _check("fas_checkpoint_pack", load().fas_checkpoint_pack(ptr, dtype, *ptrs, x.numel(), _on(stream, current)))
     if stream is not None:
@@ -596,7 +619,7 @@ def fas_checkpoint_unpack(c: Checkpoint, dtype=None, out=None, stream=None):
     c, ptrs = _check_checkpoint("c", c, device)
     shape = c.codes.shape
     if out is None:
-        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=c.codes.device)
+        out = _empty(stream, shape, dtype or torch.bfloat16, c.codes.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out must be {dtype}, got {out.dtype}")
     code = _dtype_code("out", out)
@@ -666,21 +689,20 @@ def fas_residual_norm(y, x, gamma_post, gamma_pre, gate=None, frame_tokens=None,
     ppost = _check_here("gamma_post", gamma_post, (C,), f32, device)
     ppre = _check_here("gamma_pre", gamma_pre, (C,), f32, device)
     pgate, spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
-    x_out, px_out = _output("x_out", x_out, x, device)
-    h, ph = _output("h", h, y, device)
-    rstd = torch.empty((2, N), dtype=f32, device=x.device)
-    held, parts, ptrs = (), (), (None, None, None, None)
+    x_out, px_out = _output("x_out", x_out, x, device, stream)
+    h, ph = _output("h", h, y, device, stream)
+    rstd = _empty(stream, (2, N), f32, x.device)
+    held, ptrs = (), (None, None, None, None)
     if checkpoint:
-        held = _checkpoint_empty((N, C), x.device), _checkpoint_empty((N, C), x.device)
-        parts = (*held[0], *held[1])
-        ptrs = [t.data_ptr() for t in parts]
+        held = _checkpoint_empty((N, C), x.device, stream), _checkpoint_empty((N, C), x.device, stream)
+        ptrs = [t.data_ptr() for t in (*held[0], *held[1])]
     rc = load().fas_residual_norm(py, px, residual, pgate, ppost, ppre, alpha, eps, N, C,
                                   spans, frames, px_out, ph, rstd.data_ptr(),
                                   *ptrs, _on(stream, current))
     if rc:
         _check("fas_residual_norm", rc)
     if stream is not None:
-        _own_until_run(stream, x_out, h, rstd, *parts)
+        _own_until_run(stream, x_out, h)
     return (x_out, h, rstd, *held)
 
 
@@ -716,12 +738,12 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
              _check_here("gamma_post", gamma_post, (C,), f32, device),
              _check_here("gamma_pre", gamma_pre, (C,), f32, device)]
     args[-3], spans, frames = _norm_frames(N, C, gate, frame_tokens, device)
-    dx, pdx = _output("dx", dx, dx_out, device)
-    dy, pdy = _output("dy", dy, dh, device)
+    dx, pdx = _output("dx", dx, dx_out, device, stream)
+    dy, pdy = _output("dy", dy, dh, device, stream)
     need = _norm_workspace(N, C, None if spans is None else bytes(spans), frames, device)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dx_out.device)
-    dpost, dpre = torch.empty_like(gamma_post), torch.empty_like(gamma_pre)
-    dgate = None if gate is None else torch.empty_like(gate)
+    workspace = _empty(stream, need, torch.uint8, dx_out.device)
+    dpost, dpre = (_empty(stream, (C,), f32, dx_out.device) for _ in range(2))
+    dgate = None if gate is None else _empty(stream, gate.shape, f32, dx_out.device)
     rc = load().fas_residual_norm_backward(
         *args, alpha, N, C, spans, frames,
         pdx, pdy,
@@ -729,7 +751,7 @@ def fas_residual_norm_backward(dx_out, dh, y, x_out, rstd, gamma_post, gamma_pre
         _on(stream, current))
     _check("fas_residual_norm_backward", rc)
     if stream is not None:
-        _own_until_run(stream, workspace, dpost, dpre, dx, dy, *([] if dgate is None else [dgate]))
+        _own_until_run(stream, dx, dy)
     return dx, dy, dpost, dpre, dgate
 
 

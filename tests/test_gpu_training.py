@@ -598,6 +598,41 @@ def test_calls_of_several_widths_in_several_threads():
         assert not bad
 
 
+def test_calls_on_a_stream_leave_the_current_streams_memory():
+    """A tensor that is freed while work that reads it is still queued on the
+    current stream keeps its values until that work has run, whatever a call
+    on another stream allocates meanwhile."""
+    c = Norm([64, 192], 2048, torch.bfloat16, True)
+    a = Attention([128] * 8, 1, 1, 4, 128)
+    want = (*c.forward(checkpoint=True)[:3], *(t for t in a.run().values()))
+    back = fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, want[0], want[2], c.post, c.pre, **c.kw)
+    packed = fas.fas_checkpoint_pack(c.x)
+    s = torch.cuda.Stream()
+    for sizes in ([c.x.numel() * 2] * 6, [c.x.numel()] * 6, [a.q.numel() * 2] * 6, [1 << 18] * 40):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        held = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in sizes]
+        inputs = torch.cuda.current_stream().record_event()
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        copies = [t.clone() for t in held]
+        freed = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in held]
+        del held
+        s.wait_event(inputs)
+        got = (*fas.fas_residual_norm(c.y, c.x, c.post, c.pre, **c.kw, checkpoint=True, stream=s)[:3],
+               *fas.fas_backward(a.q, a.k, a.v, a.out, a.lse, a.dout, stream=s))
+        gb = fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, want[0], want[2], c.post, c.pre, **c.kw, stream=s)
+        p8 = fas.fas_checkpoint_pack(c.x, stream=s.cuda_stream)
+        assert not any(lo <= t.data_ptr() < hi for t in (*got, *gb, *p8) for lo, hi in freed)
+        torch.cuda.synchronize()
+        assert all(bool((t == 77).all()) for t in copies)
+        assert all(torch.equal(x, y) for x, y in zip((*got, *gb), (*want, *back)))
+        assert torch.equal(p8.codes.view(torch.uint8), packed.codes.view(torch.uint8)) and torch.equal(p8.scales, packed.scales)
+    # Handle 0 is the default stream.
+    p8 = fas.fas_checkpoint_pack(c.x, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(p8.scales, packed.scales)
+
+
 def test_attention_backward_native_and_with_outputs():
     c = Attention([48, 64, 16], 1, 1, 2, 64)
     got = c.run()

@@ -173,6 +173,78 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fas.fas_checkpoint_unpack(x)
 
 
+class FakeStream:
+    cuda_stream = 7
+
+
+class FakeLibrary:
+    """Every call succeeds and writes nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: 0
+
+
+STREAM_CALLS = {
+    "backward": lambda t, s: fas.fas_backward(t.q, t.q, t.q, t.q, t.lse, t.q, stream=s),
+    "norm": lambda t, s: fas.fas_residual_norm(t.x, t.x, t.g, t.g, gate=t.gate, checkpoint=True, stream=s),
+    "norm_backward": lambda t, s: fas.fas_residual_norm_backward(t.x, t.x, t.x, t.x, t.rstd, t.g, t.g, gate=t.gate, stream=s),
+    "pack": lambda t, s: fas.fas_checkpoint_pack(t.x, stream=s),
+    "unpack": lambda t, s: fas.fas_checkpoint_unpack((t.codes, t.scales), stream=s),
+    "forward": lambda t, s: fas.fas_forward(t.q, t.q, t.q, stream=s),
+    "ablation": lambda t, s: fas.fas_forward_ablation(t.q, t.q, t.q, stream=s),
+    "fold": lambda t, s: fas.fas_prologue_fold_weights(t.x, t.g, stream=s),
+    "prologue": lambda t, s: fas.fas_prologue_with_key_sums(t.hidden, t.w, t.angles, t.angles, 2, 64, stream=s),
+}
+BUFFERS = {"backward": 4, "norm": 7, "norm_backward": 6, "pack": 2, "unpack": 1, "forward": 2, "ablation": 2, "fold": 1, "prologue": 4}
+
+
+@pytest.mark.parametrize("given", [FakeStream(), None], ids=["stream", "current"])
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_buffers_of_a_call_are_of_the_stream_it_runs_on(name, given, monkeypatch):
+    """What a call allocates comes from the pool of the stream that writes it:
+    memory of the current stream may have been freed with work still queued on
+    it.  (The library and the streams are stand-ins: no kernel runs.)"""
+    import contextlib
+    import types
+    bf16 = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    t = types.SimpleNamespace(q=bf16(2, 32, 64), lse=torch.zeros(2, 32), x=bf16(6, 64), g=torch.zeros(64), gate=torch.zeros(2, 64),
+                              rstd=torch.zeros(2, 6), codes=torch.zeros(4, 64).to(torch.float8_e4m3fn),
+                              scales=torch.zeros(4, 2, dtype=torch.uint8), hidden=bf16(32, 64), w=bf16(384, 64),
+                              angles=torch.zeros(32, 32))
+    active, made, kept = ["current"], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        active.append(stream)
+        yield
+        active.pop()
+
+    def counted(real):
+        def make(*args, **kw):
+            got = real(*args, **kw)
+            made.append((got.data_ptr(), active[-1]))
+            return got
+        return make
+    for f in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, f, counted(getattr(torch, f)))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: kept.append((self.data_ptr(), s)))
+    monkeypatch.setattr(fas, "load", FakeLibrary)
+    monkeypatch.setattr(fas, "_current", lambda *a: (-1, 0))
+    monkeypatch.setattr(fas, "_current_device_stream", lambda *a: (-1, 0))
+    monkeypatch.setattr(fas, "_check_tensor", lambda *a: None)
+    monkeypatch.setattr(fas, "_norm_workspace", lambda *a: 256)
+    monkeypatch.setattr(fas, "_PLAN", dict(heads=2, tokens=32, head_dim=64))
+    STREAM_CALLS[name](t, given)
+    where = given or "current"
+    assert len(made) == BUFFERS[name] and all(s is where for _, s in made), made
+    # The caller goes on with the results on the current stream.
+    if given:
+        assert all((p, "current") in kept for p, _ in made)
+
+
 def test_row_wait_selftest_refuses():
     assert fas.load().fas_selftest_row_wait_timeout(0, None) == fas.FAS_ERR_ARG
     assert fas.load().fas_selftest_row_wait_timeout(1000001, None) == fas.FAS_ERR_ARG
