@@ -631,6 +631,16 @@ def fas_checkpoint_unpack(c: Checkpoint, dtype=None, out=None, stream=None):
     return out
 
 
+def _whole(frame_tokens):
+    """Tokens of the frames as Python ints: a list, or one number for all."""
+    given = np.asarray(frame_tokens)
+    with np.errstate(invalid="ignore"):
+        spans = given.astype(np.int64)
+    if (spans != given).any():
+        raise ValueError(f"frame_tokens must be whole numbers, got {frame_tokens}")
+    return spans.tolist()
+
+
 def _norm_frames(tokens: int, width: int, gate, frame_tokens, device: int):
     """(gate's address, host spans or None, number of frames)."""
     import torch
@@ -642,14 +652,14 @@ def _norm_frames(tokens: int, width: int, gate, frame_tokens, device: int):
         if n == 0 or tokens % n:
             raise ValueError(f"{tokens} tokens are not {n} equal frames (one per row of gate)")
         return ptr, None, n
-    if not isinstance(frame_tokens, (list, tuple)):
-        if np.ndim(frame_tokens) == 0:
-            if n * int(frame_tokens) != tokens:
-                raise ValueError(f"gate has {n} frames of {frame_tokens} tokens; x has {tokens} tokens")
-            return ptr, None, n
     if not (isinstance(frame_tokens, (list, tuple)) and all(type(t) is int for t in frame_tokens)):
-        spans = np.asarray(frame_tokens, dtype=np.int32)
-        frame_tokens = spans.tolist() if spans.ndim == 1 else ()
+        frame_tokens = _whole(frame_tokens)
+    if isinstance(frame_tokens, int):
+        if n * frame_tokens != tokens:
+            raise ValueError(f"gate has {n} frames of {frame_tokens} tokens; x has {tokens} tokens")
+        return ptr, None, n
+    if frame_tokens and isinstance(frame_tokens[0], list):
+        raise ValueError("frame_tokens must be one number or a sequence of numbers")
     if len(frame_tokens) != n or sum(frame_tokens) != tokens or min(frame_tokens) < 0:
         raise ValueError(f"frame_tokens must hold {n} spans (one per row of gate) that add up to {tokens} tokens")
     return ptr, (ctypes.c_int32 * n)(*frame_tokens), n

@@ -173,6 +173,32 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fas.fas_checkpoint_unpack(x)
 
 
+@pytest.mark.parametrize("spans", [
+    [3.9, 9.0, 4.0], np.array([3.2, 9.7, 4.9]), np.array([2**32 + 3, 9, 4]), torch.tensor([3, 9, 2**32 + 4]),
+    np.array([2**64 - 1, 9, 8], dtype=np.uint64), [float("nan"), 9, 4], [[3, 9, 4]], [np.float32(3.5), 9, 4], [True, 2.5, 13], (), [3, 9], "3"],
+    ids=str)
+def test_frames_of_a_norm_are_whole_numbers(spans):
+    """Spans that are no whole numbers, or no 32-bit ones, are not cut to some."""
+    with pytest.raises((ValueError, TypeError, OverflowError)):
+        fas._norm_frames(16, 8, torch.zeros(3, 8), spans, -1)
+
+
+@pytest.mark.parametrize("tokens,spans", [(16, 5.5), (15, 5.4), (15, np.float32(5.0001)), (15, float("inf")), (15, 2**32 + 5),
+                                          (15, np.array([5]))], ids=str)
+def test_one_span_for_all_frames_is_a_whole_number(tokens, spans):
+    with pytest.raises((ValueError, TypeError, OverflowError)):
+        fas._norm_frames(tokens, 8, torch.zeros(3, 8), spans, -1)
+
+
+@pytest.mark.parametrize("spans", [[3, 9, 4], (3, 9, 4), np.array([3, 9, 4]), np.array([3.0, 9.0, 4.0]), torch.tensor([3, 9, 4]),
+                                   [np.int64(3), 9, np.int32(4)]], ids=str)
+def test_frames_of_a_norm_in_every_kind_of_sequence(spans):
+    _, got, n = fas._norm_frames(16, 8, torch.zeros(3, 8), spans, -1)
+    assert n == 3 and list(got) == [3, 9, 4]
+    for one in (5, np.int32(5), 5.0, torch.tensor(5), np.array(5)):
+        assert fas._norm_frames(15, 8, torch.zeros(3, 8), one, -1)[1:] == (None, 3)
+
+
 class FakeStream:
     cuda_stream = 7
 
