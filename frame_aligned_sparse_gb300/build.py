@@ -43,8 +43,12 @@ def _sources():
 
 def _torch() -> Optional[str]:
     """The installed torch's folder, without importing it (a slow import)."""
-    spec = importlib.util.find_spec("torch")
-    return spec.submodule_search_locations[0] if spec else None
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        return None
+    folders = list(spec.submodule_search_locations or ()) if spec else []
+    return folders[0] if folders else None
 
 
 def _host_command(torch: str, out: str) -> list:
@@ -68,18 +72,29 @@ def _fingerprint() -> str:
     torch = _torch()
     if torch:
         h.update(" ".join([torch] + HOST_FLAGS).encode())
-        with open(os.path.join(torch, "version.py"), "rb") as fh:
-            h.update(fh.read())
+        version = os.path.join(torch, "version.py")
+        if os.path.exists(version):
+            with open(version, "rb") as fh:
+                h.update(fh.read())
     return h.hexdigest()
 
 
+_WITHOUT_HOST = " without _host.so"  # in the stamp: it did not compile here
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is not up to date and returns libfas.so's path.  _host.so
+    only saves time on calls with torch tensors, so it is left out, with a
+    warning, where torch or what compiling against it takes is missing (tried
+    again when a source or torch changes, or with force)."""
     stamp = os.path.join(BUILD, "stamp")
     fp = _fingerprint()
     torch = _torch()  # without it libfas.so alone: the C boundary needs none
-    built = os.path.exists(OUT) and (not torch or os.path.exists(HOST_OUT))
-    if not force and built and os.path.exists(stamp) and open(stamp).read() == fp:
-        return OUT
+    if not force and os.path.exists(OUT) and os.path.exists(stamp):
+        with open(stamp) as fh:
+            was = fh.read()
+        if was == fp + _WITHOUT_HOST or (was == fp and (not torch or os.path.exists(HOST_OUT))):
+            return OUT
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
 
@@ -93,19 +108,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(res.stdout + res.stderr, file=sys.stderr)
         return obj
 
-    def compile_host() -> None:
+    def compile_host() -> bool:
         tmp = HOST_OUT + ".tmp"
-        res = subprocess.run(_host_command(torch, tmp), capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, HOST_OUT)
+        try:
+            res = subprocess.run(_host_command(torch, tmp), capture_output=True, text=True)
+            failed = f"{res.stdout}\n{res.stderr}" if res.returncode else ""
+        except OSError as e:
+            failed = str(e)
+        if not failed:
+            os.replace(tmp, HOST_OUT)
+            return True
+        if os.path.exists(HOST_OUT):  # of other sources or another torch
+            os.remove(HOST_OUT)
+        print(f"warning: building without {os.path.basename(HOST_OUT)} (calls on torch tensors take longer): g++ failed "
+              f"on {HOST_SRC}:\n{failed[-4000:]}", file=sys.stderr)
+        return False
 
     srcs = _sources()
     with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
         host = ex.submit(compile_host) if torch else None
         objs = list(ex.map(compile_one, srcs))
-        if host:
-            host.result()
+        without = "" if not host or host.result() else _WITHOUT_HOST
     tmp = OUT + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -113,7 +136,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"nvcc link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, OUT)
     with open(stamp, "w") as fh:
-        fh.write(fp)
+        fh.write(fp + without)
     return OUT
 
 

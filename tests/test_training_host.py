@@ -271,6 +271,32 @@ def test_buffers_of_a_call_are_of_the_stream_it_runs_on(name, given, monkeypatch
         assert all((p, "current") in kept for p, _ in made)
 
 
+def test_build_without_torch_headers(tmp_path, monkeypatch, capsys):
+    """Where _host.so does not compile, libfas.so is built all the same, once,
+    and no _host.so of another build stays."""
+    from frame_aligned_sparse_gb300 import build
+    source = tmp_path / "unit.cpp"
+    source.write_text('extern "C" int answer() { return 42; }\n')
+    (tmp_path / "torch").mkdir()
+    monkeypatch.setattr(build, "_sources", lambda: [str(source)])
+    monkeypatch.setattr(build, "_torch", lambda: str(tmp_path / "torch"))
+    for name, file in (("OUT", "libfas.so"), ("HOST_OUT", "_host.so"), ("BUILD", "_build")):
+        monkeypatch.setattr(build, name, str(tmp_path / file))
+    (tmp_path / "_host.so").write_text("stale")
+    assert build.build() == str(tmp_path / "libfas.so")
+    assert ctypes.CDLL(build.OUT).answer() == 42
+    assert not (tmp_path / "_host.so").exists()
+    assert "without _host.so" in capsys.readouterr().err
+    when = (tmp_path / "libfas.so").stat().st_mtime_ns
+    build.build()
+    assert (tmp_path / "libfas.so").stat().st_mtime_ns == when
+    monkeypatch.setattr(build, "_torch", lambda: None)
+    build.build()
+    source.write_text("no C++")
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        build.build()
+
+
 def test_row_wait_selftest_refuses():
     assert fas.load().fas_selftest_row_wait_timeout(0, None) == fas.FAS_ERR_ARG
     assert fas.load().fas_selftest_row_wait_timeout(1000001, None) == fas.FAS_ERR_ARG
