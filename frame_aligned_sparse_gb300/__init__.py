@@ -145,12 +145,13 @@ def load() -> ctypes.CDLL:
     return _LIB
 
 
-_HOST = None
+_HOST = None  # False: there is none
 
 
 def _host():
     """The operators' calls on torch tensors in native code (csrc/host), bound
-    to the loaded library."""
+    to the loaded library; False, with a warning, if it was not built or does
+    not load (the calls below then do the same, only slower)."""
     global _HOST
     if _HOST is None:
         import importlib.machinery
@@ -158,11 +159,18 @@ def _host():
         import torch  # its libraries, which the module uses  # noqa: F401
         lib = load()
         path = os.path.join(os.path.dirname(library_path()), "_host.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m frame_aligned_sparse_gb300.build`.")
-        loader = importlib.machinery.ExtensionFileLoader("_host", path)
-        host = importlib.util.module_from_spec(importlib.util.spec_from_loader("_host", loader))
-        loader.exec_module(host)
+        try:
+            if not os.path.exists(path):
+                raise ImportError(f"{path} is missing")
+            loader = importlib.machinery.ExtensionFileLoader("_host", path)
+            host = importlib.util.module_from_spec(importlib.util.spec_from_loader("_host", loader))
+            loader.exec_module(host)
+        except ImportError as e:
+            import warnings
+            warnings.warn(f"small calls take longer without the native binding ({e}): build it with "
+                          "`python -m frame_aligned_sparse_gb300.build --force`", RuntimeWarning, stacklevel=4)
+            _HOST = False
+            return _HOST
         host.bind(*(ctypes.cast(getattr(lib, f"fas_{name}"), ctypes.c_void_p).value for name in (
             "backward", "residual_norm", "residual_norm_backward", "residual_norm_backward_workspace",
             "checkpoint_pack", "checkpoint_unpack")))
@@ -175,7 +183,8 @@ def _native(call: str, first, *args):
     (see csrc/host/calls.cpp) and the caller has to go on by itself."""
     if not getattr(first, "is_cuda", False):
         return None
-    got = getattr(_HOST or _host(), call)(*args)
+    host = _host() if _HOST is None else _HOST
+    got = getattr(host, call)(*args) if host else None
     if type(got) is int:
         _check(f"fas_{call}", got)
     return got

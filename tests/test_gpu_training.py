@@ -542,6 +542,21 @@ def test_plain_calls_take_native_code_and_give_the_same(held, gated, monkeypatch
     assert (got[4] is None) == (not gated)
 
 
+def test_calls_without_the_native_binding_give_the_same(monkeypatch):
+    c = Norm([5, 90, 31], 256, torch.float32, True)
+    a = Attention([48] * 3, 1, 1, 2, 64)
+
+    def step():
+        x, h, rstd, y8, x8 = c.forward(checkpoint=True)
+        got = [x, h, rstd, *y8, *x8, *fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, x, rstd, c.post, c.pre, **c.kw),
+               *fas.fas_residual_norm_backward(c.dx_out, c.dh, y8, x8, rstd, c.post, c.pre, **c.kw)]
+        got += [*fas.fas_checkpoint_pack(x), fas.fas_checkpoint_unpack(x8, torch.float32), *a.run().values()]
+        return [t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t for t in got]
+    want = step()
+    monkeypatch.setattr(fas, "_HOST", False)
+    assert all(torch.equal(x, y) and x.dtype == y.dtype for x, y in zip(step(), want, strict=True))
+
+
 def test_native_calls_run_on_the_current_stream_and_in_several_threads():
     """Each thread's stream, and the memory of a call's own buffers."""
     import threading

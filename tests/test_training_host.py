@@ -297,6 +297,24 @@ def test_build_without_torch_headers(tmp_path, monkeypatch, capsys):
         build.build()
 
 
+@pytest.mark.parametrize("there", [False, True], ids=["missing", "unloadable"])
+def test_calls_without_the_native_binding(there, tmp_path, monkeypatch):
+    """Without a _host.so that loads, a call is left to Python, with one warning."""
+    import types
+    import warnings
+    fas._host()
+    if there:
+        (tmp_path / "_host.so").write_text("not a library")
+    monkeypatch.setattr(fas, "library_path", lambda: str(tmp_path / "libfas.so"))
+    monkeypatch.setattr(fas, "_HOST", None)
+    x = types.SimpleNamespace(is_cuda=True)
+    with pytest.warns(RuntimeWarning, match="without the native binding"):
+        assert fas._native("checkpoint_pack", x, x) is None
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        assert fas._native("checkpoint_pack", x, x) is None
+
+
 def test_row_wait_selftest_refuses():
     assert fas.load().fas_selftest_row_wait_timeout(0, None) == fas.FAS_ERR_ARG
     assert fas.load().fas_selftest_row_wait_timeout(1000001, None) == fas.FAS_ERR_ARG
