@@ -822,7 +822,7 @@ int fas_prologue_with_key_sums(const void* x, const void* w_folded, const float*
   const cuuint64_t xs[1] = {(cuuint64_t)width * 2};
   const cuuint32_t xb[2] = {64, 128};
   const cuuint64_t wd[2] = {(cuuint64_t)width, (cuuint64_t)3 * heads * head_dim};
-  const cuuint32_t wb[2] = {64, (cuuint32_t)(tn / fas::prologue_cluster())};  // each CTA loads its share
+  const cuuint32_t wb[2] = {64, (cuuint32_t)tn};
   CUtensorMap tx, tw;
   if (encode(&tx, x, 2, xd, xs, xb) != FAS_OK || encode(&tw, w_folded, 2, wd, xs, wb) != FAS_OK) return FAS_ERR_CUDA;
   fas::PrologueParams pp;

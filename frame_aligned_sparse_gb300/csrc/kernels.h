@@ -148,9 +148,6 @@ struct PrologueParams {
 // H * d is not a multiple of 128).
 int prologue_tile_cols(int heads, int head_dim);
 
-// CTAs per cluster of the prologue kernel (they share each weight tile).
-int prologue_cluster();
-
 cudaError_t launch_prologue(const CUtensorMap& tx, const CUtensorMap& tw, const PrologueParams& p,
                             cudaStream_t stream);
 

@@ -258,3 +258,12 @@ def test_partial_block_statistic_for_128_tiling():
                     # Partial: the block mixes visible and hidden entries.
                     partial += not sub.all()
         assert abs(partial / live - want) < 0.01, (name, partial, live)
+
+
+def test_no_copy_is_multicast():
+    """The prologue also runs as a rank of several GPUs, where TMA loads are
+    not multicast; no source has such a load."""
+    csrc = os.path.join(ROOT, "frame_aligned_sparse_gb300", "csrc")
+    for path, _, names in os.walk(csrc):
+        for name in names:
+            assert "multicast::cluster" not in open(os.path.join(path, name)).read(), name
