@@ -458,8 +458,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       }
     }
     ptx::named_barrier_sync(1, kSoftThreads);
-    const float delta = red[0][trow];
-    // A row past the frame's end gets P = 0 and is never stored.
+    // A row past the frame's end gets P = 0 and is never stored.  One of
+    // infinite lse gets P = 0 too, and its out may hold anything.
+    const float delta = lse == INFINITY ? 0.f : red[0][trow];
     const float nl = -lse * core::kLog2e;
     if (valid && g < 2) {  // group 0: -lse / s, group 1: -delta, as the key pass's MMA takes them
       uint8_t* st = p.stats + ((int64_t)g * p.H * p.N + (int64_t)h * p.N + token) * kStatBytes;

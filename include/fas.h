@@ -397,11 +397,12 @@ int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded,
  * are rounded to bf16 for the products.  Every output row is written exactly
  * once, by one CTA in a fixed order: results are bit-reproducible.  Tokens a
  * row does not see are not read into it, whatever they hold; a query row whose
- * lse is +infinity takes no part (P = 0).  Needs the plan
- * of that fas_forward (uniform or ragged); an output that is also an input or
- * another output returns FAS_ERR_ARG.  Asynchronous on cuda_stream; may be
- * captured into a graph, which is valid as long as the plan is.  (The page has no training; its section "Deleting the Mask" gives
- * the visibility.) */
+ * lse is +infinity takes no part (P = 0, whatever its out holds; its q and
+ * dout have to be finite).  Needs the plan of that fas_forward (uniform or
+ * ragged); an output that is also an input or another output returns
+ * FAS_ERR_ARG.  Asynchronous on cuda_stream; may be captured into a graph,
+ * which is valid as long as the plan is.  (The page has no training; its
+ * section "Deleting the Mask" gives the visibility.) */
 #define FAS_BACKWARD_WORKSPACE(H, N) (32 * (int64_t)(H) * (int64_t)(N))
 int fas_backward(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
                  void* dq, void* dk, void* dv, void* workspace, void* cuda_stream);

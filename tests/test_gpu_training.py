@@ -186,6 +186,20 @@ def test_attention_backward_rows_with_infinite_lse_take_no_part():
     assert torch.equal(got["dv"], want["dv"]) and torch.equal(got["dk"], want["dk"])
 
 
+def test_attention_backward_takes_no_out_of_rows_with_infinite_lse():
+    spans, R0, r = [80, 48, 144], 1, 1
+    for d, layout in ((128, "hnd"), (64, "nhd")):
+        c = Attention(spans, R0, r, 2, d, layout)
+        rows = torch.tensor([3, 81, 130, 271], device="cuda")
+        c.lse[:, rows] = float("inf")
+        want = c.run()
+        assert all(bool(torch.isfinite(t).all()) for t in want.values())
+        for value in (float("nan"), float("inf"), -float("inf")):
+            c.hnd(c.out)[:, rows] = value
+            got = c.run()
+            assert all(torch.equal(got[n], want[n]) for n in want)
+
+
 def test_launch_counts():
     c = Attention([48] * 3, 1, 1, 2, 64)
     c.run()
