@@ -319,7 +319,7 @@ struct RaggedItems {
   __device__ __forceinline__ int64_t rows(int f) const { return row[f + 1] - row[f]; }
 };
 
-// Where a thread works: its row group's item.  A row has W warps, or (kNarrow:
+// Where a thread works: its row group's item.  A row has W warps, or (kLanes:
 // up to 128 columns) 4, 8 or 16 lanes of one, whose other lanes have other
 // rows: they all go through the longest item's rows together, for the
 // shuffles.

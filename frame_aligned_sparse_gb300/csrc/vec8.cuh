@@ -29,11 +29,6 @@ __device__ __forceinline__ P2 mul2(P2 a, P2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
-__device__ __forceinline__ P2 add2(P2 a, P2 b) {
-  P2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 __device__ __forceinline__ float sum(P2 a) { return lo(a) + hi(a); }
 
 struct Bf16 {

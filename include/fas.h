@@ -489,7 +489,9 @@ int fas_checkpoint_pack(const void* x, int dtype, uint8_t* codes, uint8_t* scale
 int fas_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, int dtype, int64_t elements,
                           void* cuda_stream);
 
-/* Kernel launches issued by the last fas_prepass / fas_forward call. */
+/* Kernel launches issued by the last call that launches kernels on a device
+ * stream (fas_prepass, fas_forward, the prologue, the training calls), of any
+ * thread. */
 int fas_last_launch_count(void);
 
 /* Static description of a status code. */
