@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <vector>
 
 #include "fas.h"
@@ -53,7 +54,6 @@ struct State {
   unsigned int* flags = nullptr;  // kFlagBoundRange (attention); cleared by fas_status
   const void* pre_q = nullptr;
   const void* pre_k = nullptr;
-  int last_launches = 0;
   int layout = FAS_LAYOUT_HND;  // of q, k, v and out
   fas_plan_info info{};
   // fas_forward_host: library-owned device copies of q, k, v, out, lse, the
@@ -80,6 +80,7 @@ struct State {
 };
 
 State g_state;
+std::atomic<int> g_last_launches{0};  // the training calls come from several threads
 // Heads per group of fas_forward_host's default schedule in steady state:
 // large enough that each group's attention launch fills the GPU many times
 // over.  The schedule ramps up to it (1, 2, 4, ... heads) so that the first
@@ -141,6 +142,7 @@ void release() {
     if (cur >= 0 && cur != s.device) cudaSetDevice(cur);
   }
   g_state = State();
+  g_last_launches = 0;
 }
 
 // Carves the library's device buffers out of one allocation.
@@ -592,7 +594,7 @@ int run_prepass(const void* q, const void* k, const float* key_sums, void* cuda_
   fas::PrepassArgs a = prepass_args(q, k, 0, p.H);
   a.key_sums = key_sums;
   const int n = fas::launch_prepass(a, st);
-  s.last_launches = n > 0 ? n : 0;
+  g_last_launches = n > 0 ? n : 0;
   if (n < 0) return FAS_ERR_CUDA;
   s.pre_q = q;
   s.pre_k = k;
@@ -631,7 +633,7 @@ int fas_forward(const void* q, const void* k, const void* v, void* out, float* l
   CUtensorMap tq, tk, tv;
   if (encode_qkv(q, k, v, &tq, &tk, &tv) != FAS_OK) return FAS_ERR_CUDA;
   const cudaError_t e = launch_fwd(tq, tk, tv, s.work, p.n_work, out, lse, mode, static_cast<cudaStream_t>(cuda_stream));
-  s.last_launches = e == cudaSuccess ? 1 : 0;
+  g_last_launches = e == cudaSuccess ? 1 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -724,7 +726,7 @@ int fas_forward_host(const void* q, const void* k, const void* v, void* out, flo
   if (cudaStreamWaitEvent(caller, s.ev_exit, 0) != cudaSuccess) return FAS_ERR_CUDA;
   s.pre_q = s.dq;
   s.pre_k = s.dk;
-  s.last_launches = launches;
+  g_last_launches = launches;
   return FAS_OK;
 }
 
@@ -786,7 +788,7 @@ int fas_forward_ablation(const void* q, const void* k, const void* v, void* out,
                                  two ? s.abl_lse[1] : nullptr, static_cast<uint16_t*>(out), lse, p.H, p.N,
                                  s.abl_npad, st) != cudaSuccess)
     return FAS_ERR_CUDA;
-  s.last_launches = launches + 1;
+  g_last_launches = launches + 1;
   return FAS_OK;
 }
 
@@ -843,7 +845,7 @@ int fas_prologue_with_key_sums(const void* x, const void* w_folded, const float*
   pp.err = err;
   pp.limit_ns = fas::kWaitLimitNs;
   const cudaError_t e = fas::launch_prologue(tx, tw, pp, static_cast<cudaStream_t>(cuda_stream));
-  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  g_last_launches = e == cudaSuccess ? 1 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -898,7 +900,7 @@ int fas_backward(const void* q, const void* k, const void* v, const void* out, c
   b.limit_ns = fas::kWaitLimitNs;
   b.scale = (float)(1.0 / sqrt((double)p.d));
   const int n = fas::launch_attention_backward(p.d, b, p.n_work, static_cast<cudaStream_t>(cuda_stream));
-  s.last_launches = n > 0 ? n : 0;
+  g_last_launches = n > 0 ? n : 0;
   return n > 0 ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -984,7 +986,7 @@ int fas_residual_norm(const void* y, const void* x, int residual, const float* g
   a.eps = eps;
   const cudaError_t e =
       fas::launch_residual_norm(a, frame_tokens, n_frames, span, sms, static_cast<cudaStream_t>(cuda_stream));
-  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  g_last_launches = e == cudaSuccess ? 1 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -1056,7 +1058,7 @@ int fas_residual_norm_backward(const void* dx_out, const void* dh, const void* y
   a.alpha = alpha;
   const cudaError_t e = fas::launch_residual_norm_backward(a, items, frame_tokens, n_frames, span, sms, workspace,
                                                            static_cast<cudaStream_t>(cuda_stream));
-  g_state.last_launches = e == cudaSuccess ? 2 : 0;
+  g_last_launches = e == cudaSuccess ? 2 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -1078,7 +1080,7 @@ int fas_checkpoint_pack(const void* x, int dtype, uint8_t* codes, uint8_t* scale
   if (rc != FAS_OK) return rc;
   const cudaError_t e = fas::launch_checkpoint_pack(x, dtype == FAS_DTYPE_F32, codes, scales, elements,
                                                     static_cast<cudaStream_t>(cuda_stream));
-  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  g_last_launches = e == cudaSuccess ? 1 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -1088,7 +1090,7 @@ int fas_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, 
   if (rc != FAS_OK) return rc;
   const cudaError_t e = fas::launch_checkpoint_unpack(codes, scales, x, dtype == FAS_DTYPE_F32, elements,
                                                       static_cast<cudaStream_t>(cuda_stream));
-  g_state.last_launches = e == cudaSuccess ? 1 : 0;
+  g_last_launches = e == cudaSuccess ? 1 : 0;
   return e == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
 }
 
@@ -1178,7 +1180,7 @@ int fas_selftest_row_wait_timeout(int limit_us, void* cuda_stream) {
   return selftest(limit_us, cuda_stream, 2u, fas::launch_row_wait_selftest);
 }
 
-int fas_last_launch_count(void) { return g_state.last_launches; }
+int fas_last_launch_count(void) { return g_last_launches; }
 
 const char* fas_error_string(int status) {
   switch (status) {
