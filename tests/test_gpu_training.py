@@ -128,6 +128,16 @@ def test_attention_backward_at_full_size():
         assert torch.equal(got[n], again[n]), n
 
 
+@pytest.mark.parametrize("geo", [([3600] * 4, 1, 1, 2, 64, "hnd"), ([880] * 9, 1, 2, 4, 64, "nhd"),
+                                 ([1000 // 16 * 16, 16, 2064, 3600], 1, 1, 2, 64, "nhd")], ids=["3600", "880", "ragged"])
+def test_attention_backward_of_long_frames_with_narrow_heads(geo):
+    """Heads of 64 on frames of many blocks: sampled rows of every frame."""
+    c = Attention(*geo, sharp=True)
+    ends = np.cumsum([0] + geo[0])
+    rows = sorted({int(min(a + r, b - 1)) for a, b in zip(ends, ends[1:]) for r in (0, 127, 128, 143, 144, 777, b - a - 1)})
+    c.check(c.run(), rows=torch.tensor(rows, device="cuda"))
+
+
 def test_attention_backward_matches_differences():
     """Along a random direction, the 64-bit loss's central difference against
     the kernel's gradients: off by at most the gradients' own bounds, plus
@@ -660,6 +670,51 @@ def test_calls_on_a_stream_leave_the_current_streams_memory():
     p8 = fas.fas_checkpoint_pack(c.x, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(p8.scales, packed.scales)
+
+
+CAPTURED_FIRST = """
+import torch
+import frame_aligned_sparse_gb300 as fas
+
+def run(width, residual):
+    g = torch.Generator(device="cuda").manual_seed(width)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, dx = rnd(37, width).to(residual), rnd(37, width).to(residual)
+    y, dh = rnd(37, width).bfloat16(), rnd(37, width).bfloat16()
+    post, pre, gate = rnd(width), rnd(width), rnd(1, width)
+
+    def step():
+        xo, h, rstd, y8, x8 = fas.fas_residual_norm(y, x, post, pre, gate=gate, checkpoint=True)
+        a = fas.fas_residual_norm_backward(dx, dh, y, xo, rstd, post, pre, gate=gate)
+        b = fas.fas_residual_norm_backward(dx, dh, y8, x8, rstd, post, pre, gate=gate)
+        return (xo, h, rstd, *a, *b, fas.fas_checkpoint_unpack(fas.fas_checkpoint_pack(xo)))
+    return step
+
+q, k, v, out, dout = (torch.randn(2, 96, 64, device="cuda").bfloat16() for _ in range(5))
+lse = torch.ones(2, 96, device="cuda") * 9
+fas.fas_plan(48, 2, 0, 1, 2, 64)
+steps = [run(w, r) for w in (128, 2048, 2560, 8192) for r in (torch.bfloat16, torch.float32)]
+steps.append(lambda: fas.fas_backward(q, k, v, out, lse, dout))
+torch.cuda.synchronize()
+for step in steps:
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step(), strict=True))
+assert fas.fas_status() == fas.FAS_OK
+"""
+
+
+def test_calls_captured_before_any_other():
+    """A process whose first call of each kernel and shape is a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(fas.__file__)))
+    res = subprocess.run([sys.executable, "-c", CAPTURED_FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-4000:]
 
 
 def test_attention_backward_native_and_with_outputs():
