@@ -14,16 +14,20 @@
 // over the queries that see them.  Together they compute S and dP twice (7
 // products for the 5 that the gradients need), but every gradient stays in
 // TMEM until its one store: no fp32 gradient goes through memory, no atomics,
-// bit-reproducible results.  (One kernel for all five would stage dS in
-// shared memory for two more operands, 208 KB a block of 64 queries, over
-// 1660 clocks of its bandwidth for 1280 of the tensor pipe, and add 64 KB of
-// fp32 reductions to L2 a pair of tiles.)
+// bit-reproducible results.  One kernel for all five has not been built.  By
+// count it would not lose: its operands take some 1660 clocks of shared-memory
+// bandwidth a block of 64 queries (dS is stored there for two more operands),
+// these two kernels' products 1790 of the tensor pipe.  It would add 64 KB of
+// fp32 reductions to L2 a pair of tiles, whose order has to be fixed for
+// results to stay bit-reproducible.
 //
-// Bound by the tensor pipe and, on long runs, by power: the 720p geometry
-// with 6 heads takes 11.9 ms, 1.18 PFLOP/s of the five products and 1.65 of
-// the seven executed, 0.97 of the rate that the library's bf16 product
-// sustains (1.70); at d = 64 the exponentials and their conversions bound it
-// (0.80 PFLOP/s of five on the mid geometry, 0.89 on the 720p one).
+// At d = 128 bound by the tensor pipe and, on long runs, by power: 6 heads of
+// 22 frames of 3600 take 11.8 to 12.1 ms (with the clock), 1.16 to 1.20
+// PFLOP/s of the five products and 1.63 to 1.67 of the seven executed, 0.96 to
+// 0.99 of the rate that the library's bf16 product sustains (1.70); 16 heads of
+// 17 frames of 880, 1.54 ms (1.10).  At d = 64 the exponentials and their
+// conversions bound it, which both kernels compute (0.79 PFLOP/s of five on
+// the frames of 880, 0.88 on those of 3600).
 //
 // A visible range is walked in blocks; its last block is shortened to the
 // tokens it has (a multiple of 16) through the MMA's N or its K steps, so no

@@ -61,7 +61,7 @@ constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
 // are exchanged, and the few such CTAs an SM holds hide less of it than three
 // or four whose sums cross the cluster.  % of the copy rate, CTA against
 // cluster (30 M elements): forward at 2,560 columns 84 against 60, 4,096 84 /
-// 79, 5,120 (ten warps) 60 / 82, 16,384 (whose rows spilled in one CTA) 50 /
+// 79, 5,120 (ten warps) 60 / 78, 16,384 (whose rows spilled in one CTA) 50 /
 // 71; backward 76 / 64, 67 / 75, 64 / 71, 24 / 61; from 8 bits 63 / 44, 56 /
 // 59, 38 / 55, 17 / 47.  Narrow rows: 64 columns 84, 61 and 53.
 enum Row { kLanes, kWarps, kWide, kCluster };

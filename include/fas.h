@@ -383,7 +383,11 @@ int fas_prologue_with_key_sums(const void* x, const void* w_folded, const float*
 int fas_prologue_fold_weights(const void* w, const float* gamma, void* w_folded, int width, int out_features,
                               void* cuda_stream);
 
-/* The attention's backward pass.  With s = 1/sqrt(d), P = exp(s q.k - lse)
+/* The training calls (from here to fas_checkpoint_unpack) compute gradients;
+ * they are no part of an automatic differentiation, and the chain they cover
+ * ends at q, k, v and at the norms' inputs: the prologue has no backward pass.
+ *
+ * The attention's backward pass.  With s = 1/sqrt(d), P = exp(s q.k - lse)
  * over the pairs fas_forward attends to (recomputed, never stored) and
  * delta_i = sum_c dout_ic out_ic:
  *   dS_ij = P_ij (dout_i . v_j - delta_i)
