@@ -717,6 +717,35 @@ def test_calls_captured_before_any_other():
     assert res.returncode == 0, res.stderr[-4000:]
 
 
+def test_calls_captured_on_a_branch_of_the_capture():
+    """stream= a stream that was forked from the capturing one: the branch's
+    buffers and the other branch's are the graph's own at every replay."""
+    c = Norm([64, 192], 2048, torch.bfloat16, True)
+    a = Attention([128] * 8, 1, 1, 4, 128)
+    x, h, rstd = c.forward()
+    norm = lambda **kw: fas.fas_residual_norm_backward(c.dx_out, c.dh, c.y, x, rstd, c.post, c.pre, **c.kw, **kw)
+    back = lambda **kw: fas.fas_backward(a.q, a.k, a.v, a.out, a.lse, a.dout, **kw)
+    want = (*norm(), *back())
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        branch, here = [], []
+        for _ in range(3):
+            branch.append((*norm(stream=side), *back(stream=side)))
+            here.append((*norm(), *back()))
+        main.wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for got in branch + here:
+            assert all(torch.equal(x, y) for x, y in zip(got, want, strict=True))
+            for t in got:
+                t.zero_()
+
+
 def test_attention_backward_native_and_with_outputs():
     c = Attention([48, 64, 16], 1, 1, 2, 64)
     got = c.run()
