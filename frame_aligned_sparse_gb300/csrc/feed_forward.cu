@@ -135,6 +135,20 @@ __device__ __forceinline__ bool wait(uint64_t* barrier, uint32_t parity, volatil
   }
 }
 
+// The same for what is under way to this CTA: it has to have come before the
+// CTA ends, given up or not.
+template <bool kPair>
+__device__ __forceinline__ void settle(uint64_t* barrier, uint32_t parity, uint64_t limit_ns) {
+  const uint32_t bar = ptx::smem_addr(barrier);
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!(kPair ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)))
+    if (ptx::global_timer_ns() - t0 > limit_ns) {
+      atomicOr(&g_gave_up, 1u);
+      return;
+    }
+}
+constexpr uint64_t kLostNs = 1000000;  // for what no barrier counts any more, once a CTA or its partner has given up
+
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
   return ptx::idesc_bf16_f32(m, n, b_mn) | ((a_mn ? 1u : 0u) << 15);
 }
@@ -524,12 +538,13 @@ __global__ void __launch_bounds__(threads(kE), 1)
           }
         }
       }
-      if (!ok && rank == 0) {  // copies in flight land before the CTA ends (a bounded wait)
-        for (int64_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f) {
-          const uint64_t t0 = ptx::global_timer_ns();
-          while (!ptx::mbar_try_wait(ptx::smem_addr(&bars.full[f % kStages]), (uint32_t)(f / kStages) & 1u))
-            if (ptx::global_timer_ns() - t0 > p.limit_ns) break;
-        }
+      // The last stages' arrivals, from MMAs of the leader, come before the CTA
+      // ends; where it has given up, its copies in flight.
+      for (int64_t f = max((int64_t)0, fill - kStages); f < fill; ++f) {
+        const int s = (int)(f % kStages);
+        const uint32_t parity = (uint32_t)(f / kStages) & 1u;
+        if (ok) ok = wait<kPair>(&bars.empty[s], parity, abort, p.limit_ns);
+        if (!ok && rank == 0) settle<false>(&bars.full[s], parity, p.limit_ns);
       }
     }
     __syncwarp();
@@ -595,7 +610,7 @@ __global__ void __launch_bounds__(threads(kE), 1)
         }
       }
       commit(&bars.drain);
-      wait<kPair>(&bars.drain, 0, abort, p.limit_ns);
+      settle<kPair>(&bars.drain, 0, p.limit_ns);
     }
     __syncwarp();
   } else if (warp == 2 + kEpilogueWarps) {
@@ -647,11 +662,8 @@ __global__ void __launch_bounds__(threads(kE), 1)
           }
         }
         if (!ok) {  // copies in flight land before the CTA ends (a bounded wait)
-          for (int64_t q = max((int64_t)0, fetched - 2); q < fetched; ++q) {
-            const uint64_t t0 = ptx::global_timer_ns();
-            while (!ptx::mbar_try_wait(ptx::smem_addr(&bars.ready[q & 1]), (uint32_t)(q >> 1) & 1u))
-              if (ptx::global_timer_ns() - t0 > p.limit_ns) break;
-          }
+          for (int64_t q = max((int64_t)0, fetched - 2); q < fetched; ++q)
+            settle<false>(&bars.ready[q & 1], (uint32_t)(q >> 1) & 1u, p.limit_ns);
         }
         ptx::bulk_wait();
       }
@@ -704,10 +716,27 @@ __global__ void __launch_bounds__(threads(kE), 1)
   }
 
   // Neither CTA of a pair ends, or frees its TMEM, while the other may still
-  // signal it or read its operands.
+  // signal it or read its operands.  The MMAs' arrivals come from the tensor
+  // pipe, which no barrier of the threads orders: the producers have waited for
+  // those on the stages, the epilogues for the accumulators', and the last one,
+  // which follows all MMAs, both CTAs wait for here (the leader has).
   ptx::tc_fence_before_sync();
   __syncthreads();
-  if constexpr (kPair) ptx::cluster_sync();
+  if constexpr (kPair) {
+    if (warp == 1) {
+      if (lane == 0) settle<true>(&bars.drain, 0, p.limit_ns);
+      __syncwarp();
+    }
+    if (threadIdx.x == 0 && *abort) ptx::store_cluster(ptx::cluster_addr(ptx::smem_addr(&bars.abort), rank ^ 1u), 1u);
+    __syncwarp();
+    ptx::cluster_sync();
+  }
+  if (*abort) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (ptx::global_timer_ns() - t0 < kLostNs) {
+    }
+    __syncwarp();
+  }
   if (warp == 1) {
     ptx::tc_fence_after_sync();
     if constexpr (kPair) ptx::tmem_dealloc_pair(tmem, kTmemCols);

@@ -6,6 +6,7 @@ Tolerances are the references' own bounds (tests/block_reference.py) or
 derived in the test.
 """
 import math
+import time
 
 import numpy as np
 import pytest
@@ -245,6 +246,29 @@ def test_feed_forward_is_reproducible():
 def test_feed_forward_reports_nothing_to_fas_status():
     fas.fas_plan(48, 3, 1, 1, 2, 64)
     Block(100, 64, 64).check()
+    assert fas.fas_status() == fas.FAS_OK
+
+
+@pytest.mark.parametrize("shape", [(300, 8200, 520), (6000, 72, 5000), (25000, 264, 136), (25000, 1032, 72), (14960, 2048, 1376)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_feed_forward_pairs_of_ctas_end(shape):
+    """Shapes whose products take pairs of CTAs, with fewer and more steps of 64
+    than there are stages, several tiles a pair and none left over: CTAs wait
+    for every arrival under way to them before they end, and no such wait runs
+    out (half a second each, then fas_status tells).  Calls one behind the
+    other: a CTA's shared memory is the next kernel's at once."""
+    fas.fas_plan(48, 3, 1, 1, 2, 64)
+    b = Block(*shape)
+    b.check()
+    y, kept = b.forward(keep=True)
+    grads = b.backward(kept)
+    torch.cuda.synchronize()
+    start = time.monotonic()
+    for _ in range(20):
+        again = b.forward(), *b.backward(kept)
+    torch.cuda.synchronize()
+    assert time.monotonic() - start < 0.4  # 20 calls of at most 3 ms
+    assert all(torch.equal(p, q) for p, q in zip(again, (y, *grads)))
     assert fas.fas_status() == fas.FAS_OK
 
 
