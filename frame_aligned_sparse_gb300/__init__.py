@@ -25,6 +25,7 @@ __all__ = [
     "FasError", "PlanInfo", "MODES", "library_path", "load",
     "fas_plan", "fas_plan_describe", "fas_prepass", "fas_forward", "fas_free",
     "fas_status", "fas_prepass_readback", "fas_selftest_wait_timeout", "fas_selftest_row_wait_timeout",
+    "fas_selftest_product_wait_timeout",
     "fas_last_launch_count",
     "fas_prepass_noalloc", "fas_forward_host", "fas_set_layout", "LAYOUTS", "fas_forward_ablation",
     "fas_prologue", "fas_prologue_fold_weights", "PROLOGUE_LAYOUTS",
@@ -112,6 +113,7 @@ _SIGS = {
     "fas_prepass_readback": (ctypes.c_int, [ctypes.c_void_p] * 6),
     "fas_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
     "fas_selftest_row_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
+    "fas_selftest_product_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
     "fas_last_launch_count": (ctypes.c_int, []),
     "fas_prepass_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p] + [ctypes.c_int] * 6 +
                             [ctypes.c_void_p] * 4),
@@ -1183,6 +1185,10 @@ def fas_selftest_wait_timeout(limit_us: int, stream=None) -> int:
 
 def fas_selftest_row_wait_timeout(limit_us: int, stream=None) -> int:
     return load().fas_selftest_row_wait_timeout(limit_us, _stream_handle(stream))
+
+
+def fas_selftest_product_wait_timeout(limit_us: int, stream=None) -> int:
+    return load().fas_selftest_product_wait_timeout(limit_us, _stream_handle(stream))
 
 
 def fas_prepass_noalloc(q, k, frame_tokens: int, n_frames: int, ref_frames: int, window_radius: int,

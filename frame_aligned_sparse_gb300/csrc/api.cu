@@ -1408,6 +1408,15 @@ int fas_selftest_row_wait_timeout(int limit_us, void* cuda_stream) {
   return selftest(limit_us, cuda_stream, 2u, fas::launch_row_wait_selftest);
 }
 
+int fas_selftest_product_wait_timeout(int limit_us, void* cuda_stream) {
+  if (limit_us > 5000) return FAS_ERR_ARG;
+  return selftest(limit_us, cuda_stream, 2u, [](unsigned int* result, uint64_t limit_ns, cudaStream_t st) {
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    return rc == FAS_OK && fas::launch_product_wait_selftest(result, limit_ns, sms, st) == FAS_OK ? cudaSuccess : cudaErrorUnknown;
+  });
+}
+
 int fas_last_launch_count(void) { return g_last_launches; }
 
 const char* fas_error_string(int status) {

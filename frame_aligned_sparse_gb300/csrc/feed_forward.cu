@@ -135,6 +135,9 @@ __device__ __forceinline__ bool wait(uint64_t* barrier, uint32_t parity, volatil
   }
 }
 
+// Time for what no barrier counts any more, once a CTA or its partner has given up.
+constexpr uint64_t kLostNs = 1000000;
+
 // The same for what is under way to this CTA: it has to have come before the
 // CTA ends, given up or not.
 template <bool kPair>
@@ -142,12 +145,11 @@ __device__ __forceinline__ void settle(uint64_t* barrier, uint32_t parity, uint6
   const uint32_t bar = ptx::smem_addr(barrier);
   const uint64_t t0 = ptx::global_timer_ns();
   while (!(kPair ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)))
-    if (ptx::global_timer_ns() - t0 > limit_ns) {
+    if (ptx::global_timer_ns() - t0 > max(limit_ns, kLostNs)) {
       atomicOr(&g_gave_up, 1u);
       return;
     }
 }
-constexpr uint64_t kLostNs = 1000000;  // for what no barrier counts any more, once a CTA or its partner has given up
 
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
   return ptx::idesc_bf16_f32(m, n, b_mn) | ((a_mn ? 1u : 0u) << 15);
@@ -1149,6 +1151,47 @@ int launch_feed_forward_backward(const FeedForwardArgs& a, void* workspace, int*
   if (rc == FAS_OK) rc = l.run<true, true, kPlain>(q, dw, N, spread_weights(N, C, F, a.sms));
   *launches = l.launches;
   return rc;
+}
+
+// One tile whose sum takes longer than the limit (2^24 terms, at least 20 ms):
+// its epilogues give up, while the loads and products go on to their end.
+int launch_product_wait_selftest(unsigned int* result, uint64_t limit_ns, int sms, cudaStream_t st) {
+  constexpr int64_t kTerms = 1 << 24, kSide = 8;
+  uint8_t* memory = nullptr;
+  constexpr int64_t kOperand = kTerms * kSide * 2, kMatrix = 256;  // a small matrix [8, 8]; both: [8, 16]
+  if (cudaMalloc(&memory, kOperand + 4 * kMatrix) != cudaSuccess) return FAS_ERR_CUDA;
+  uint8_t *out = memory + kOperand, *gu = out + kMatrix, *dgu = gu + kMatrix, *h = dgu + kMatrix;
+  const Matrix rows{memory, kSide, kTerms}, cols{memory, kTerms, kSide};
+  Launcher l{sms, limit_ns, st};
+  GemmParams p;
+  Maps<true> inner;
+  Spread one;
+  int rc = cudaMemsetAsync(memory, 0, kOperand + 4 * kMatrix, st) == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
+  if (rc == FAS_OK) rc = both_maps(&inner.g, &inner.u, gu, kSide, kSide);
+  if (rc == FAS_OK) rc = both_maps(&inner.dg, &inner.du, dgu, kSide, kSide);
+  if (rc == FAS_OK) rc = matrix_map(&inner.h, h, kSide, kSide);
+  unsigned int gave_up = 0;
+  auto next = [&](int launched) {  // the word is left set after the last
+    if (rc == FAS_OK) rc = launched;
+    if (rc != FAS_OK) return;
+    bool lost = false;
+    if (cudaStreamSynchronize(st) != cudaSuccess || feed_forward_gave_up(&lost) != cudaSuccess) rc = FAS_ERR_CUDA;
+    gave_up += lost;
+  };
+  const Product plain[1] = {{kSide, kSide, rows, rows, out}}, wide[1] = {{kSide, kSide, cols, cols, out}};
+  const Product gate[1] = {{kSide, kSide, rows, {memory, 2 * kSide, kTerms / 2}, out}}, dh[1] = {{kSide, kSide, rows, cols, nullptr}};
+  for (one.form = 0; one.form < 3; ++one.form) {
+    next(l.run<false, false, kPlain>(p, plain, kTerms, one));
+    next(l.run<true, true, kPlain>(p, wide, kTerms, one));
+    if (one.form < 2) next(l.run<false, false, kGateUp>(p, gate, kTerms / 2, one));
+    if (one.form < 2) next(l.run<false, true, kInner>(p, dh, kTerms, one, inner));
+  }
+  const unsigned int right = 2, set = 1;
+  if (rc == FAS_OK && gave_up == 10 &&
+      (cudaMemcpyToSymbol(g_gave_up, &set, sizeof(set)) != cudaSuccess ||
+       cudaMemcpy(result, &right, sizeof(right), cudaMemcpyHostToDevice) != cudaSuccess))
+    rc = FAS_ERR_CUDA;
+  return cudaFree(memory) == cudaSuccess ? rc : FAS_ERR_CUDA;
 }
 
 cudaError_t feed_forward_gave_up(bool* gave_up) {

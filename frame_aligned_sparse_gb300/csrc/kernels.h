@@ -302,6 +302,10 @@ int launch_feed_forward_backward(const FeedForwardArgs& a, void* workspace, int*
 // Whether a wait of the feed-forward kernels ran out since the last call; clears it.  Current device.
 cudaError_t feed_forward_gave_up(bool* gave_up);
 
+// One product in each form whose waits run out of time: 2 in `result` if all
+// did, and feed_forward_gave_up tells.  Waits for the device.  A FAS_* status.
+int launch_product_wait_selftest(unsigned int* result, uint64_t limit_ns, int sms, cudaStream_t stream);
+
 cudaError_t launch_wait_selftest(unsigned int* err, uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace fas

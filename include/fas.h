@@ -287,6 +287,12 @@ int fas_selftest_wait_timeout(int limit_us, void* cuda_stream);
  * FAS_ERR_TIMEOUT once. */
 int fas_selftest_row_wait_timeout(int limit_us, void* cuda_stream);
 
+/* The same for the products of fas_feed_forward and its backward pass, with a
+ * limit of 1..5000 us: one tile in each form, whose sum takes longer.
+ * Allocates 256 MB for the call.  Expected result: FAS_ERR_TIMEOUT (every form
+ * gave up and ended), after which fas_status reports FAS_ERR_TIMEOUT once. */
+int fas_selftest_product_wait_timeout(int limit_us, void* cuda_stream);
+
 /* Bytes of the fixed device array that fas_prepass_noalloc uses as scratch. */
 #define FAS_NOALLOC_SCRATCH_BYTES (4u << 20)
 

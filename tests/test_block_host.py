@@ -146,6 +146,11 @@ def test_feed_forward_workspace_refuses():
     assert lib.fas_feed_forward_workspace(4, 64, 64, 0, 0, None) == fas.FAS_ERR_ARG
 
 
+def test_product_wait_selftest_refuses():
+    for limit_us in (0, 5001):
+        assert fas.load().fas_selftest_product_wait_timeout(limit_us, None) == fas.FAS_ERR_ARG
+
+
 def rotary_call(**kw):
     a = dict(ins=[A, 2 * A, 3 * A], in_strides=[384, 64] * 3, outs=[4 * A, 5 * A, 6 * A], out_strides=[64, 640] * 3, turned=[1, 1, 0],
              n=3, positions=7 * A, axes=2, freq=[1.0, 0.5, 0.25], axis=[0, 1, 1], pairs=3, pairing=0, inverse=0, tokens=10, heads=2,

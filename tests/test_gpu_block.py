@@ -272,6 +272,21 @@ def test_feed_forward_pairs_of_ctas_end(shape):
     assert fas.fas_status() == fas.FAS_OK
 
 
+def test_feed_forward_waits_that_run_out():
+    """A product whose waits run out ends, frees what it holds and is reported
+    once; the products after it are as before."""
+    fas.fas_plan(48, 3, 1, 1, 2, 64)
+    b = Block(300, 8200, 520)
+    y, kept = b.forward(keep=True)
+    grads = b.backward(kept)
+    for limit_us in (1, 2000, 5000):
+        assert fas.fas_selftest_product_wait_timeout(limit_us) == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_status() == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_status() == fas.FAS_OK
+        assert all(torch.equal(p, q) for p, q in zip((b.forward(), *b.backward(kept)), (y, *grads)))
+    assert fas.fas_status() == fas.FAS_OK
+
+
 def test_feed_forward_refuses():
     b = Block(16, 64, 72)
     with pytest.raises(ValueError, match="activation"):
