@@ -25,7 +25,7 @@ __all__ = [
     "FasError", "PlanInfo", "MODES", "library_path", "load",
     "fas_plan", "fas_plan_describe", "fas_prepass", "fas_forward", "fas_free",
     "fas_status", "fas_prepass_readback", "fas_selftest_wait_timeout", "fas_selftest_row_wait_timeout",
-    "fas_selftest_product_wait_timeout",
+    "fas_selftest_product_wait_timeout", "fas_training_status",
     "fas_last_launch_count",
     "fas_prepass_noalloc", "fas_forward_host", "fas_set_layout", "LAYOUTS", "fas_forward_ablation",
     "fas_prologue", "fas_prologue_fold_weights", "PROLOGUE_LAYOUTS",
@@ -110,6 +110,7 @@ _SIGS = {
     "fas_prologue_fold_weights": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int] * 2 + [ctypes.c_void_p]),
     "fas_free": (ctypes.c_int, []),
     "fas_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "fas_training_status": (ctypes.c_int, [ctypes.c_void_p]),
     "fas_prepass_readback": (ctypes.c_int, [ctypes.c_void_p] * 6),
     "fas_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
     "fas_selftest_row_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p]),
@@ -1161,6 +1162,16 @@ def fas_status(stream=None) -> int:
     rc = load().fas_status(_stream_handle(stream))
     if rc not in (FAS_OK, FAS_ERR_TIMEOUT, FAS_ERR_BOUND):
         _check("fas_status", rc)
+    return rc
+
+
+def fas_training_status(stream=None) -> int:
+    """Synchronises the stream; returns FAS_OK or FAS_ERR_TIMEOUT (a device
+    wait of the residual norms or the feed-forward block gave up: what they
+    wrote is incomplete).  Needs no plan; raises on other errors."""
+    rc = load().fas_training_status(_stream_handle(stream))
+    if rc not in (FAS_OK, FAS_ERR_TIMEOUT):
+        _check("fas_training_status", rc)
     return rc
 
 

@@ -1341,19 +1341,26 @@ int fas_free(void) {
   return FAS_OK;
 }
 
+int fas_training_status(void* cuda_stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return FAS_ERR_CUDA;
+  bool rows = false, products = false;
+  if (fas::residual_norm_gave_up(&rows) != cudaSuccess || fas::feed_forward_gave_up(&products) != cudaSuccess)
+    return FAS_ERR_CUDA;
+  return rows || products ? FAS_ERR_TIMEOUT : FAS_OK;
+}
+
 int fas_status(void* cuda_stream) {
   if (!g_state.planned) return FAS_ERR_STATE;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return FAS_ERR_CUDA;
   unsigned int e = 0, f = 0;
   if (cudaMemcpy(&e, g_state.err, sizeof(e), cudaMemcpyDeviceToHost) != cudaSuccess) return FAS_ERR_CUDA;
   if (cudaMemcpy(&f, g_state.flags, sizeof(f), cudaMemcpyDeviceToHost) != cudaSuccess) return FAS_ERR_CUDA;
-  bool rows = false, products = false;
-  if (fas::residual_norm_gave_up(&rows) != cudaSuccess || fas::feed_forward_gave_up(&products) != cudaSuccess)
-    return FAS_ERR_CUDA;
-  if (e == 0 && f == 0 && !rows && !products) return FAS_OK;
+  const int training = fas_training_status(cuda_stream);
+  if (training == FAS_ERR_CUDA) return FAS_ERR_CUDA;
+  if (e == 0 && f == 0 && training == FAS_OK) return FAS_OK;
   if (e && cudaMemset(g_state.err, 0, sizeof(e)) != cudaSuccess) return FAS_ERR_CUDA;
   if (f && cudaMemset(g_state.flags, 0, sizeof(f)) != cudaSuccess) return FAS_ERR_CUDA;
-  return e || rows || products ? FAS_ERR_TIMEOUT : FAS_ERR_BOUND;
+  return e || training != FAS_OK ? FAS_ERR_TIMEOUT : FAS_ERR_BOUND;
 }
 
 int fas_prepass_readback(float* mu, float* frame_max, float* stat, uint8_t* elig, float* row_bound,

@@ -270,6 +270,13 @@ int fas_free(void);
  * safe range (see fas_forward), else FAS_OK; clears both words. */
 int fas_status(void* cuda_stream);
 
+/* The same for the training calls that need no plan, with or without one:
+ * synchronise the stream and report FAS_ERR_TIMEOUT if a bounded wait of
+ * fas_residual_norm, fas_feed_forward or their backward passes gave up on the
+ * current device, else FAS_OK; clears what it reports (fas_status looks at the
+ * same words). */
+int fas_training_status(void* cuda_stream);
+
 /* Copy prepass results to host buffers (each nullable); synchronises the
  * stream.  mu: H*d fp32; frame_max: H*Nf fp32 (largest centred key norm per
  * key frame); stat: H fp32; elig: H bytes; row_bound: H*N fp32 (m_i). */
@@ -443,7 +450,8 @@ int fas_backward(const void* q, const void* k, const void* v, const void* out, c
  * 16-byte aligned (scales: any).  Sums are fp32.  Asynchronous on
  * cuda_stream; allocates nothing.  Should CTAs that share a wide row ever not
  * reach one another within half a second, what hangs on the sums they lack is
- * NaN, the kernel ends, and fas_status (with a plan) reports FAS_ERR_TIMEOUT. */
+ * NaN, the kernel ends, and fas_training_status (and fas_status, with a plan)
+ * reports FAS_ERR_TIMEOUT. */
 int fas_residual_norm(const void* y, const void* x, int residual, const float* gate, const float* gamma_post,
                       const float* gamma_pre, float alpha, float eps, int64_t tokens, int width,
                       const int32_t* frame_tokens, int n_frames, void* x_out, void* h, float* rstd, uint8_t* y_codes,
@@ -525,7 +533,8 @@ int fas_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, 
  * another output returns FAS_ERR_ARG, other overlaps are not supported.  No
  * plan is needed.  Asynchronous on cuda_stream; allocates nothing.  Should a
  * wait inside a kernel ever run out (half a second), the results are
- * incomplete, and fas_status (with a plan) reports FAS_ERR_TIMEOUT. */
+ * incomplete, and fas_training_status reports FAS_ERR_TIMEOUT (as does
+ * fas_status, with a plan). */
 enum {
   FAS_ACT_SILU = 0,
   FAS_ACT_GELU_TANH = 1

@@ -287,6 +287,27 @@ def test_feed_forward_waits_that_run_out():
     assert fas.fas_status() == fas.FAS_OK
 
 
+def test_lost_waits_are_reported_without_a_plan():
+    """A process that only trains has no plan: fas_status is out of order there,
+    fas_training_status tells, on whatever stream, and both clear the same words."""
+    fas.fas_free()
+    b = Block(300, 264, 520)
+    b.check()
+    assert fas.fas_training_status() == fas.FAS_OK
+    for lose in (fas.fas_selftest_product_wait_timeout, fas.fas_selftest_row_wait_timeout):
+        assert lose(1000) == fas.FAS_ERR_TIMEOUT
+        with pytest.raises(fas.FasError) as e:
+            fas.fas_status()
+        assert e.value.code == fas.FAS_ERR_STATE
+        assert fas.fas_training_status(torch.cuda.Stream()) == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_training_status() == fas.FAS_OK
+        fas.fas_plan(48, 3, 1, 1, 2, 64)
+        assert lose(1000) == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_training_status() == fas.FAS_ERR_TIMEOUT
+        assert fas.fas_status() == fas.FAS_OK
+        fas.fas_free()
+
+
 def test_feed_forward_refuses():
     b = Block(16, 64, 72)
     with pytest.raises(ValueError, match="activation"):
