@@ -1122,16 +1122,21 @@ int feed_forward_shape(int64_t tokens, int width, int inner) {
   return FAS_OK;
 }
 
+int feed_forward_device(int* sms, int* pairs) {
+  const int rc = device_sms(sms);
+  return rc == FAS_OK ? fas::feed_forward_pairs(*sms, pairs) : rc;
+}
+
 }  // namespace
 
 int fas_feed_forward_workspace(int64_t tokens, int width, int inner, int backward, int kept, int64_t* bytes) {
   if (!bytes) return FAS_ERR_ARG;
   int rc = feed_forward_shape(tokens, width, inner);
   if (rc != FAS_OK) return rc;
-  int sms = 0;
-  rc = device_sms(&sms);
+  int sms = 0, pairs = 0;
+  rc = feed_forward_device(&sms, &pairs);
   if (rc != FAS_OK) return rc;
-  *bytes = fas::feed_forward_workspace(tokens, width, inner, backward != 0, kept != 0, sms);
+  *bytes = fas::feed_forward_workspace(tokens, width, inner, backward != 0, kept != 0, sms, pairs);
   return FAS_OK;
 }
 
@@ -1145,9 +1150,9 @@ int fas_feed_forward(const void* x, const void* w_in, const void* w_out, int act
   rc = apart(in, out);
   if (rc != FAS_OK) return rc;
   fas::FeedForwardArgs a;
-  rc = device_sms(&a.sms);
+  rc = feed_forward_device(&a.sms, &a.pairs);
   if (rc != FAS_OK) return rc;
-  if (workspace_bytes < fas::feed_forward_workspace(tokens, width, inner, false, true, a.sms)) return FAS_ERR_SCRATCH;
+  if (workspace_bytes < fas::feed_forward_workspace(tokens, width, inner, false, true, a.sms, a.pairs)) return FAS_ERR_SCRATCH;
   a.x = x;
   a.w_in = w_in;
   a.w_out = w_out;
@@ -1174,9 +1179,9 @@ int fas_feed_forward_backward(const void* dy, const void* x, const void* w_in, c
   rc = apart(in, out);
   if (rc != FAS_OK) return rc;
   fas::FeedForwardArgs a;
-  rc = device_sms(&a.sms);
+  rc = feed_forward_device(&a.sms, &a.pairs);
   if (rc != FAS_OK) return rc;
-  if (workspace_bytes < fas::feed_forward_workspace(tokens, width, inner, true, kept != nullptr, a.sms)) return FAS_ERR_SCRATCH;
+  if (workspace_bytes < fas::feed_forward_workspace(tokens, width, inner, true, kept != nullptr, a.sms, a.pairs)) return FAS_ERR_SCRATCH;
   a.dy = dy;
   a.x = x;
   a.w_in = w_in;
@@ -1418,9 +1423,9 @@ int fas_selftest_row_wait_timeout(int limit_us, void* cuda_stream) {
 int fas_selftest_product_wait_timeout(int limit_us, void* cuda_stream) {
   if (limit_us > 5000) return FAS_ERR_ARG;
   return selftest(limit_us, cuda_stream, 2u, [](unsigned int* result, uint64_t limit_ns, cudaStream_t st) {
-    int sms = 0;
-    const int rc = device_sms(&sms);
-    return rc == FAS_OK && fas::launch_product_wait_selftest(result, limit_ns, sms, st) == FAS_OK ? cudaSuccess : cudaErrorUnknown;
+    int sms = 0, pairs = 0;
+    const int rc = feed_forward_device(&sms, &pairs);
+    return rc == FAS_OK && fas::launch_product_wait_selftest(result, limit_ns, sms, pairs, st) == FAS_OK ? cudaSuccess : cudaErrorUnknown;
   });
 }
 

@@ -35,17 +35,18 @@
 #include <type_traits>
 
 #include "fas.h"
+#include "feed_forward_plan.h"
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace fas {
 namespace {
 
-constexpr int kBlock = 64;                        // elements of a TMA block's side: a 128-byte swizzled row
+using namespace feed_forward;
+
 constexpr uint32_t kBlockBytes = kBlock * kBlock * 2;
 constexpr int kEpilogueWarps = 8, kGroups = kEpilogueWarps / 4;  // four warps a group, a group its share of the columns
 
-enum Epilogue { kPlain = 0, kGateUp = 1, kInner = 2 };
 // TMA producer, MMA issuer, epilogue, and kInner's mover.
 __host__ __device__ constexpr int threads(Epilogue e) { return 64 + 32 * kEpilogueWarps + (e == kInner ? 32 : 0); }
 
@@ -756,7 +757,6 @@ __global__ void __launch_bounds__(threads(kE), 1)
 // loads 16 consecutive bytes of its row of W and of X and four lanes cover 64
 // bytes of a row.  The warps of a CTA share the rows and split k; their fp32
 // parts meet in shared memory and are added in order.
-constexpr int kFewTokens = 31;
 // Warps of a CTA: the product onto the width has few rows, each long.
 constexpr int few_warps(bool gate) { return gate ? 8 : 16; }
 
@@ -886,65 +886,6 @@ int both_maps(CUtensorMap* first, CUtensorMap* second, const void* both, int64_t
   return rc != FAS_OK ? rc : matrix_map(second, static_cast<const uint16_t*>(both) + inner, rows, inner, 2 * inner);
 }
 
-// The forms of a tile, and what they take in nanoseconds (measured on long
-// products): a step of 64 along k, what of a tile does not run beside another's
-// products, and writing and adding up a tile of fp32 parts.
-struct Form {
-  int G, cols, step, tile, part;
-  constexpr int rows() const { return 128 * G; }
-  int64_t tiles(int64_t m, int64_t n) const { return (m + rows() - 1) / rows() * ((n + cols - 1) / cols); }
-};
-constexpr Form kForms[3] = {{1, 128, 315, 0, 25}, {2, 256, 358, 0, 100}, {2, 512, 632, 2000, 200}};
-constexpr int64_t kJoinNs = 4000;  // the launch that adds up the parts
-// What each epilogue adds to a tile's steps, and what a tile takes at least
-// (20,000 rows with 2 to 32 steps).
-constexpr struct {
-  int more, least;
-} kEpilogues[3][3] = {{{0, 1000}, {0, 2000}, {0, 4000}}, {{1200, 2000}, {600, 3600}, {}}, {{2000, 5800}, {5300, 11600}, {}}};
-
-// How a launch's tiles are spread.
-struct Spread {
-  int form = 0, splits = 1;
-  int64_t whole = 0;     // tiles done whole
-  int64_t parts = 0;     // of the others, together
-  int64_t ns = INT64_MAX;
-  int64_t bytes() const { return parts * kForms[form].rows() * kForms[form].cols * 4; }
-};
-// The form that is done first.  Whole rounds of tiles, one for every CTA or
-// pair, are done whole; what is left over would keep only some of them busy,
-// and few tiles altogether most of them idle, so those are split along k where
-// that is sooner done.  The products with an epilogue of their own have no
-// parts, and no tiles of 512 columns, whose epilogue the next tile waits for.
-template <class Tiles>
-Spread spread(Epilogue e, const Tiles& tiles, int64_t k, int sms) {
-  const int64_t ksteps = (k + kBlock - 1) / kBlock;
-  Spread best;
-  for (int i = 0; i < (e == kPlain ? 3 : 2); ++i) {
-    const Form& f = kForms[i];
-    const int64_t n = tiles(f), units = sms / f.G, rest = n % units;
-    auto tile = [&](int64_t steps) { return std::max<int64_t>(steps * f.step + kEpilogues[e][i].more, kEpilogues[e][i].least) + f.tile; };
-    auto offer = [&](int64_t whole, int64_t splits, int64_t parts, int64_t ns) {
-      if (ns < best.ns) best = {i, (int)splits, whole, parts, ns};
-    };
-    offer(n, 1, 0, (n + units - 1) / units * tile(ksteps));
-    if (e != kPlain || rest == 0) continue;
-    const int64_t base = n / units * tile(ksteps) + kJoinNs;
-    for (int64_t s = 2; s <= 32 && s * 4 <= ksteps; ++s) {
-      const int64_t per = (ksteps + s - 1) / s;
-      if ((ksteps + per - 1) / per != s) continue;  // a part without a step
-      offer(n - rest, s, rest * s, base + (rest * s + units - 1) / units * tile(per) + rest * s * f.part);
-    }
-  }
-  return best;
-}
-Spread spread(Epilogue e, int64_t m, int64_t n, int64_t k, int sms) {
-  return spread(e, [=](const Form& f) { return f.tiles(m, n); }, k, sms);
-}
-// Both weights' gradients, [2 inner, width] and [width, inner].
-Spread spread_weights(int64_t tokens, int64_t width, int64_t inner, int sms) {
-  return spread(kPlain, [=](const Form& f) { return f.tiles(2 * inner, width) + f.tiles(width, inner); }, tokens, sms);
-}
-
 struct Matrix {
   const void* at;
   int64_t rows, cols;
@@ -958,7 +899,7 @@ struct Product {
 };
 
 struct Launcher {
-  int sms;
+  Machine machine;
   uint64_t limit_ns;
   cudaStream_t st;
   int launches = 0;
@@ -984,34 +925,6 @@ struct Launcher {
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? FAS_OK : FAS_ERR_CUDA;
   }
 
-  // CTAs or pairs that run at once: one CTA an SM; of pairs, as many as the
-  // device takes (it may leave an SM without a partner).
-  template <int G, class K>
-  int at_once(K kern, int threads, size_t smem, int* units) {
-    *units = sms;
-    if constexpr (G > 1) {
-      static std::atomic<int> known[64];
-      int dev = 0;
-      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FAS_ERR_CUDA;
-      *units = known[dev];
-      if (*units == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sms / G * G));
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = G;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(units, kern, &cfg) != cudaSuccess || *units < 1) return FAS_ERR_CUDA;
-        known[dev] = *units;
-      }
-    }
-    return FAS_OK;
-  }
-
   template <int kForm, bool kAMn, bool kBMn, Epilogue kE, int kN>
   int go(GemmParams p, const Product (&products)[kN], int64_t k, const Spread& s, Maps<kE == kInner> maps) {
     constexpr int G = kForms[kForm].G, kBm = 128 * G, kBn = kForms[kForm].cols, kOut = kE == kGateUp ? kBn / 2 : kBn;
@@ -1032,11 +945,8 @@ struct Launcher {
     auto kern = feed_forward_gemm<G, kBn, kAMn, kBMn, kE>;
     const size_t smem = smem_bytes(kE, G, kBn);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FAS_ERR_CUDA;
-    int units = 0;
-    int rc = at_once<G>(kern, threads(kE), smem, &units);
-    if (rc != FAS_OK) return rc;
     g_launched = true;
-    rc = start(kern, std::min<int64_t>(p.whole + s.parts, units) * G, threads(kE), smem, G, maps, p);
+    const int rc = start(kern, std::min<int64_t>(p.whole + s.parts, machine.units(G)) * G, threads(kE), smem, G, maps, p);
     if (rc != FAS_OK || s.parts == 0) return rc;
     return start(feed_forward_join<kBm, kBn>, (int64_t)(p.tiles - p.whole) * (kBm * kBn / 2048), 256, 0, 1, p);
   }
@@ -1062,33 +972,6 @@ struct Launcher {
   }
 };
 
-constexpr int64_t align_up(int64_t n) { return (n + 255) / 256 * 256; }
-
-// The workspace: h [tokens, inner]; in the backward pass also (dg, du)
-// [tokens, 2 inner] and, where they were not kept, (g, u) and their low parts
-// [tokens, inner]; then the fp32 parts of one launch at a time.
-struct Workspace {
-  int64_t h = 0, dgu = 0, gu = 0, low = 0, parts = 0, bytes = 0;
-  Workspace(int64_t tokens, int width, int inner, bool backward, bool kept, int sms) {
-    int64_t at = align_up(tokens * inner * 2);
-    int64_t most = 0;
-    if (backward) {
-      dgu = at;
-      at += align_up(tokens * inner * 4);
-      gu = at;
-      if (!kept) at += align_up(tokens * inner * 4);
-      low = at;
-      if (!kept) at += align_up(tokens * inner * 2);
-      most = std::max(spread(kPlain, tokens, width, 2 * (int64_t)inner, sms).bytes(),
-                      spread_weights(tokens, width, inner, sms).bytes());
-    } else {
-      most = tokens <= kFewTokens ? 0 : spread(kPlain, tokens, width, inner, sms).bytes();
-    }
-    parts = at;
-    bytes = at + align_up(most);
-  }
-};
-
 // h, g and u, and the low parts of g and u from x, those that are given.
 int project(Launcher& l, const FeedForwardArgs& a, void* h, void* gu, uint16_t* low) {
   const int64_t N = a.tokens, C = a.width, F = a.inner;
@@ -1098,27 +981,69 @@ int project(Launcher& l, const FeedForwardArgs& a, void* h, void* gu, uint16_t* 
   p.low = low;
   p.silu = a.activation == FAS_ACT_SILU;
   const Product d[1] = {{N, F, {a.x, N, C}, {a.w_in, 2 * F, C}, h}};
-  return l.run<false, false, kGateUp>(p, d, C, spread(kGateUp, N, 2 * F, C, a.sms));
+  return l.run<false, false, kGateUp>(p, d, C, spread(kGateUp, N, 2 * F, C, l.machine));
 }
 
 }  // namespace
 
-int64_t feed_forward_workspace(int64_t tokens, int width, int inner, bool backward, bool kept, int sms) {
-  return Workspace(tokens, width, inner, backward, kept, sms).bytes;
+// Of pairs of CTAs, as many run at once as the device takes of the kernel that
+// it takes fewest of: the plan, the workspace and every launch go by that.
+int feed_forward_pairs(int sms, int* pairs) {
+  static std::atomic<int> known[64];  // + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FAS_ERR_CUDA;
+  *pairs = known[dev] - 1;
+  if (*pairs >= 0) return FAS_OK;
+  int most = sms / 2;
+  auto of = [&](auto kern, Epilogue e, int cols) {
+    const size_t smem = smem_bytes(e, 2, cols);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::max(2, sms / 2 * 2));
+    cfg.blockDim = dim3(threads(e));
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return false;
+    most = std::min(most, n);
+    return true;
+  };
+  if (!of(feed_forward_gemm<2, 256, false, false, kGateUp>, kGateUp, 256) ||
+      !of(feed_forward_gemm<2, 256, false, true, kInner>, kInner, 256) ||
+      !of(feed_forward_gemm<2, 256, false, false, kPlain>, kPlain, 256) ||
+      !of(feed_forward_gemm<2, 256, false, true, kPlain>, kPlain, 256) ||
+      !of(feed_forward_gemm<2, 256, true, true, kPlain>, kPlain, 256) ||
+      !of(feed_forward_gemm<2, 512, false, false, kPlain>, kPlain, 512) ||
+      !of(feed_forward_gemm<2, 512, false, true, kPlain>, kPlain, 512) ||
+      !of(feed_forward_gemm<2, 512, true, true, kPlain>, kPlain, 512))
+    return FAS_ERR_CUDA;
+  known[dev] = most + 1;
+  *pairs = most;
+  return FAS_OK;
+}
+
+int64_t feed_forward_workspace(int64_t tokens, int width, int inner, bool backward, bool kept, int sms, int pairs) {
+  return Workspace(tokens, width, inner, backward, kept, {sms, pairs}).bytes;
 }
 
 int launch_feed_forward(const FeedForwardArgs& a, void* workspace, int* launches, cudaStream_t stream) {
   const int64_t N = a.tokens, C = a.width, F = a.inner;
-  const Workspace ws(N, a.width, a.inner, false, true, a.sms);
+  const Machine machine = {a.sms, a.pairs};
+  const Workspace ws(N, a.width, a.inner, false, true, machine);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  Launcher l{a.sms, a.limit_ns, stream};
+  Launcher l{machine, a.limit_ns, stream};
   int rc = project(l, a, w + ws.h, a.kept_out, nullptr);
   GemmParams p;
   p.parts = reinterpret_cast<float*>(w + ws.parts);
   const Product y[1] = {{N, C, {w + ws.h, N, F}, {a.w_out, C, F}, a.y}};
   if (rc == FAS_OK) {
     rc = N <= kFewTokens ? l.few<false>(w + ws.h, a.w_out, a.y, nullptr, nullptr, N, C, F, false)
-                         : l.run<false, false, kPlain>(p, y, F, spread(kPlain, N, C, F, a.sms));
+                         : l.run<false, false, kPlain>(p, y, F, spread(kPlain, N, C, F, machine));
   }
   *launches = l.launches;
   return rc;
@@ -1126,9 +1051,10 @@ int launch_feed_forward(const FeedForwardArgs& a, void* workspace, int* launches
 
 int launch_feed_forward_backward(const FeedForwardArgs& a, void* workspace, int* launches, cudaStream_t stream) {
   const int64_t N = a.tokens, C = a.width, F = a.inner;
-  const Workspace ws(N, a.width, a.inner, true, a.kept != nullptr, a.sms);
+  const Machine machine = {a.sms, a.pairs};
+  const Workspace ws(N, a.width, a.inner, true, a.kept != nullptr, machine);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  Launcher l{a.sms, a.limit_ns, stream};
+  Launcher l{machine, a.limit_ns, stream};
   uint16_t* const low = a.kept ? nullptr : reinterpret_cast<uint16_t*>(w + ws.low);
   int rc = a.kept ? FAS_OK : project(l, a, nullptr, w + ws.gu, low);
   const Matrix x{a.x, N, C}, dy{a.dy, N, C}, w_in{a.w_in, 2 * F, C}, w_out{a.w_out, C, F}, h{w + ws.h, N, F},
@@ -1142,27 +1068,27 @@ int launch_feed_forward_backward(const FeedForwardArgs& a, void* workspace, int*
   p.low = low;
   if (rc == FAS_OK && low) rc = matrix_map(&maps.low, low, N, F);
   const Product dh[1] = {{N, F, dy, w_out, nullptr}};
-  if (rc == FAS_OK) rc = l.run<false, true, kInner>(p, dh, C, spread(kInner, N, F, C, a.sms), maps);
+  if (rc == FAS_OK) rc = l.run<false, true, kInner>(p, dh, C, spread(kInner, N, F, C, machine), maps);
   GemmParams q;
   q.parts = reinterpret_cast<float*>(w + ws.parts);
   const Product dx[1] = {{N, C, dgu, w_in, a.dx}};
-  if (rc == FAS_OK) rc = l.run<false, true, kPlain>(q, dx, 2 * F, spread(kPlain, N, C, 2 * F, a.sms));
+  if (rc == FAS_OK) rc = l.run<false, true, kPlain>(q, dx, 2 * F, spread(kPlain, N, C, 2 * F, machine));
   const Product dw[2] = {{2 * F, C, dgu, x, a.dw_in}, {C, F, dy, h, a.dw_out}};
-  if (rc == FAS_OK) rc = l.run<true, true, kPlain>(q, dw, N, spread_weights(N, C, F, a.sms));
+  if (rc == FAS_OK) rc = l.run<true, true, kPlain>(q, dw, N, spread_weights(N, C, F, machine));
   *launches = l.launches;
   return rc;
 }
 
 // One tile whose sum takes longer than the limit (2^24 terms, at least 20 ms):
 // its epilogues give up, while the loads and products go on to their end.
-int launch_product_wait_selftest(unsigned int* result, uint64_t limit_ns, int sms, cudaStream_t st) {
+int launch_product_wait_selftest(unsigned int* result, uint64_t limit_ns, int sms, int pairs, cudaStream_t st) {
   constexpr int64_t kTerms = 1 << 24, kSide = 8;
   uint8_t* memory = nullptr;
   constexpr int64_t kOperand = kTerms * kSide * 2, kMatrix = 256;  // a small matrix [8, 8]; both: [8, 16]
   if (cudaMalloc(&memory, kOperand + 4 * kMatrix) != cudaSuccess) return FAS_ERR_CUDA;
   uint8_t *out = memory + kOperand, *gu = out + kMatrix, *dgu = gu + kMatrix, *h = dgu + kMatrix;
   const Matrix rows{memory, kSide, kTerms}, cols{memory, kTerms, kSide};
-  Launcher l{sms, limit_ns, st};
+  Launcher l{{sms, pairs}, limit_ns, st};
   GemmParams p;
   Maps<true> inner;
   Spread one;

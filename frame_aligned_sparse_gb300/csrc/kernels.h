@@ -291,10 +291,12 @@ struct FeedForwardArgs {
   int activation = 0;
   int64_t tokens = 0;
   int width = 0, inner = 0;
-  int sms = 1;
+  int sms = 1, pairs = 0;  // of CTAs that run at once
   uint64_t limit_ns = kWaitLimitNs;
 };
-int64_t feed_forward_workspace(int64_t tokens, int width, int inner, bool backward, bool kept, int sms);
+// How many pairs of CTAs run at once on the current device (may be none).  A FAS_* status.
+int feed_forward_pairs(int sms, int* pairs);
+int64_t feed_forward_workspace(int64_t tokens, int width, int inner, bool backward, bool kept, int sms, int pairs);
 // Return a FAS_* status; `launches` receives the number of kernels.
 int launch_feed_forward(const FeedForwardArgs& a, void* workspace, int* launches, cudaStream_t stream);
 int launch_feed_forward_backward(const FeedForwardArgs& a, void* workspace, int* launches, cudaStream_t stream);
@@ -304,7 +306,7 @@ cudaError_t feed_forward_gave_up(bool* gave_up);
 
 // One product in each form whose waits run out of time: 2 in `result` if all
 // did, and feed_forward_gave_up tells.  Waits for the device.  A FAS_* status.
-int launch_product_wait_selftest(unsigned int* result, uint64_t limit_ns, int sms, cudaStream_t stream);
+int launch_product_wait_selftest(unsigned int* result, uint64_t limit_ns, int sms, int pairs, cudaStream_t stream);
 
 cudaError_t launch_wait_selftest(unsigned int* err, uint64_t limit_ns, cudaStream_t stream);
 

@@ -3,6 +3,9 @@ differences and with each other, and bad arguments are refused before any
 device work."""
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -149,6 +152,79 @@ def test_feed_forward_workspace_refuses():
 def test_product_wait_selftest_refuses():
     for limit_us in (0, 5001):
         assert fas.load().fas_selftest_product_wait_timeout(limit_us, None) == fas.FAS_ERR_ARG
+
+
+SPREADS = r"""
+#include "feed_forward_plan.h"
+
+#include <cstdio>
+#include <random>
+
+using namespace fas::feed_forward;
+
+static int bad(const char* what, Machine m, long n, long c, long f) {
+  std::printf("%s: %d CTAs, %d pairs, %ld x %ld x %ld\n", what, m.ctas, m.pairs, n, c, f);
+  return 1;
+}
+
+int main() {
+  std::mt19937 rng(7);
+  auto size = [&](double most) { return (long)std::exp(std::uniform_real_distribution<double>(0, std::log(most))(rng)); };
+  const Machine machines[] = {{152, 76}, {152, 70}, {152, 75}, {148, 1}, {152, 0}, {1, 0}, {2, 1}};
+  for (int i = 0; i < 20000; ++i) {
+    const long n = size(300000), c = 8 * size(2048), f = 8 * size(4096);
+    for (const Machine& m : machines) {
+      struct {
+        Epilogue e;
+        long rows, cols, rows2, k;
+        const Spread s;
+        const Workspace* ws;
+      } const products[] = {
+          {kGateUp, n, 2 * f, 0, c, spread(kGateUp, n, 2 * f, c, m), nullptr},
+          {kInner, n, f, 0, c, spread(kInner, n, f, c, m), nullptr},
+          {kPlain, n, c, 0, f, spread(kPlain, n, c, f, m), nullptr},
+          {kPlain, n, c, 0, 2 * f, spread(kPlain, n, c, 2 * f, m), nullptr},
+          {kPlain, 2 * f, c, c, n, spread_weights(n, c, f, m), nullptr},
+      };
+      const Workspace forward(n, (int)c, (int)f, false, true, m), kept(n, (int)c, (int)f, true, true, m),
+          again(n, (int)c, (int)f, true, false, m);
+      const Workspace* const room[][2] = {{}, {}, {&forward, &forward}, {&kept, &again}, {&kept, &again}};
+      for (int j = 0; j < 5; ++j) {
+        const auto& p = products[j];
+        const Spread& s = p.s;
+        const Form& form = kForms[s.form];
+        const long units = form.G == 1 ? m.ctas : m.pairs;
+        if (units < 1) return bad("a form that cannot run", m, n, c, f);
+        if (p.e != kPlain && (s.form == 2 || s.parts)) return bad("an epilogue in parts", m, n, c, f);
+        const long tiles = form.tiles(p.rows, p.cols) + (p.rows2 ? form.tiles(p.rows2, f) : 0), steps = (p.k + 63) / 64;
+        const long per = (steps + s.splits - 1) / s.splits;
+        if (s.whole + s.parts / s.splits != tiles || s.parts % s.splits) return bad("tiles", m, n, c, f);
+        if (s.parts && (s.whole % units || s.splits < 2 || s.parts / s.splits >= units)) return bad("rounds", m, n, c, f);
+        if (s.parts && (s.splits - 1) * per >= steps) return bad("a part without a step", m, n, c, f);
+        if (!s.parts && s.splits != 1) return bad("splits of nothing", m, n, c, f);
+        for (const Workspace* w : room[j])
+          if (w && (j != 2 || n > kFewTokens) && w->bytes - w->parts < s.parts * form.rows() * form.cols * 4)
+            return bad("workspace", m, n, c, f);
+      }
+    }
+  }
+  return 0;
+}
+"""
+
+
+def test_feed_forward_products_are_spread_over_what_runs(tmp_path):
+    """Tiles, rounds, parts and workspace go by the CTAs and pairs that run at
+    once, which need not be all SMs' worth of pairs."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host compiler")
+    csrc = os.path.join(os.path.dirname(fas.__file__), "csrc")
+    (tmp_path / "spreads.cpp").write_text("#include <cmath>\n" + SPREADS)
+    exe = str(tmp_path / "spreads")
+    subprocess.run([gxx, "-O1", "-std=c++17", "-Wall", "-Werror", "-I" + csrc, str(tmp_path / "spreads.cpp"), "-o", exe], check=True)
+    got = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert got.returncode == 0, got.stdout
 
 
 def rotary_call(**kw):
