@@ -6,7 +6,8 @@
 // in an order that the sizes fix, so the norm is bit-reproducible.  Where a
 // thread's fp32 sum overflowed or came out so small that squares may have
 // been lost below fp32's range, the thread reads its share again and adds it
-// in 64 bits.  The second kernel adds the first one's sums (every CTA for
+// in 64 bits (not for a share of zeros: gradients of rows that no token took
+// are ordinary, and 300 M of them in 16 bits took 1.13 ms so, 0.09 now).  The second kernel adds the first one's sums (every CTA for
 // itself: a few KB from L2, and nothing waits on another CTA) and scales.
 // It goes through the pieces backwards, so that what the first kernel read
 // last is still in L2.  Tensor addresses travel in the launch's parameters:
@@ -93,10 +94,12 @@ __device__ __forceinline__ double piece_squares(const void* base, int64_t from, 
   const Span<kF32> sp(base, from, n);
   constexpr int kVec = Span<kF32>::kVec;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t bits = 0;  // of all values
   auto add = [&](uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      bits |= w[e];
       if constexpr (kF32) {
         s[e] = fmaf(__uint_as_float(w[e]), __uint_as_float(w[e]), s[e]);
       } else {
@@ -121,15 +124,28 @@ __device__ __forceinline__ double piece_squares(const void* base, int64_t from, 
   for (int i = threadIdx.x; i < sp.loose(); i += kThreads) {
     const float x = element<kF32>(base, sp.loose_at(i));
     s[0] = fmaf(x, x, s[0]);
+    bits |= __float_as_uint(x);
   }
   const float all = (s[0] + s[1]) + (s[2] + s[3]);
   if (all >= kSafe && all < INFINITY) return (double)all;
+  if ((bits & (kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return 0.0;
   double d = 0.0;
   auto add64 = [&](float x) {
     if (x != 0.f) d = fma((double)x, (double)x, d);
   };
-  for (int v = threadIdx.x; v < sp.vecs; v += kThreads)
-    for (int e = 0; e < kVec; ++e) add64(element<kF32>(base, sp.vec_at(v) + e));
+  for (int v = threadIdx.x; v < sp.vecs; v += kThreads) {
+    const uint4 x = at(v);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (kF32) {
+        add64(__uint_as_float(w[e]));
+      } else {
+        add64(bf16_lo(w[e]));
+        add64(bf16_hi(w[e]));
+      }
+    }
+  }
   for (int i = threadIdx.x; i < sp.loose(); i += kThreads) add64(element<kF32>(base, sp.loose_at(i)));
   return d;
 }

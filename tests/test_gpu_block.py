@@ -655,6 +655,33 @@ def test_gradient_norm_beyond_the_range_of_squares(scale):
             check_norm(fas.fas_gradient_norm(mixed), mixed)
 
 
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_gradient_norm_of_zeros(dtype):
+    """Gradients of zero (rows that no token took) are read once like any
+    others: they take no longer.  Zeros of both signs, and one value among them."""
+    n = 300_000_000 if dtype == BF16 else 150_000_000  # 600 MB, several times L2
+    dense, zeros = torch.ones(n, device="cuda", dtype=dtype), torch.zeros(n, device="cuda", dtype=dtype)
+    zeros[1::2] = -0.0
+    assert float(fas.fas_gradient_norm([zeros])) == 0.0
+
+    def once(t):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        for _ in range(4):
+            fas.fas_gradient_norm([t])
+        end.record()
+        end.synchronize()
+        return start.elapsed_time(end)
+
+    times = [(once(dense), once(zeros)) for _ in range(12)][2:]
+    took = [sorted(t)[len(t) // 2] for t in zip(*times)]
+    assert took[1] <= 1.25 * took[0], took
+    for i, x in ((0, 3.0), (n // 2 + 1, 1e-30), (n - 1, -2e30)):
+        zeros[i] = x
+        check_norm(fas.fas_gradient_norm([zeros, zeros[:7]]), [zeros[i:i + 1], zeros[:7]])
+        zeros[i] = 0
+
+
 def test_gradient_norm_not_finite():
     x = [torch.ones(100, device="cuda"), torch.ones(50, device="cuda", dtype=BF16)]
     x[1][7] = float("inf")
