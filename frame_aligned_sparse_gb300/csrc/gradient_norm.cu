@@ -7,11 +7,14 @@
 // thread's fp32 sum overflowed or came out so small that squares may have
 // been lost below fp32's range, the thread reads its share again and adds it
 // in 64 bits (not for a share of zeros: gradients of rows that no token took
-// are ordinary, and 300 M of them in 16 bits took 1.13 ms so, 0.09 now).  The second kernel adds the first one's sums (every CTA for
-// itself: a few KB from L2, and nothing waits on another CTA) and scales.
-// It goes through the pieces backwards, so that what the first kernel read
-// last is still in L2.  Tensor addresses travel in the launch's parameters:
-// nothing is copied to the device, and a captured graph holds them.
+// are ordinary, and 300 M of them in 16 bits took 1.13 ms so, 0.09 now).  The
+// second kernel adds the first one's sums (every CTA for itself: a few KB from
+// L2, and nothing waits on another CTA) and scales, by a factor in fp32 where
+// that holds it with all its bits and in 64 bits where the norm is so large
+// that it does not.  It goes through the pieces backwards, so that what the
+// first kernel read last is still in L2.  Tensor addresses travel in the
+// launch's parameters: nothing is copied to the device, and a captured graph
+// holds them.
 
 #include <cuda_runtime.h>
 #include <math.h>
@@ -191,14 +194,15 @@ __global__ void __launch_bounds__(kThreads) gradient_total(const double* partial
   if (threadIdx.x == 0) *norm = (float)total;
 }
 
-template <bool kF32>
-__device__ __forceinline__ void piece_scale(const void* in, void* out, int64_t from, int64_t n, float f, uint64_t policy) {
+// F: float, or double for factors below fp32's normal numbers.
+template <bool kF32, class F>
+__device__ __forceinline__ void piece_scale(const void* in, void* out, int64_t from, int64_t n, F f, uint64_t policy) {
   constexpr int kElem = kF32 ? 4 : 2;
   const Span<kF32> sp(in, from, n);
   const uint8_t* src = static_cast<const uint8_t*>(in);
   uint8_t* dst = static_cast<uint8_t*>(out);
   auto one = [&](int64_t i) {
-    const float x = element<kF32>(in, i) * f;
+    const float x = (float)(element<kF32>(in, i) * f);
     if constexpr (kF32) static_cast<float*>(out)[i] = x;
     else static_cast<uint16_t*>(out)[i] = (uint16_t)ptx::pack_bf16x2(x, 0.f);
   };
@@ -206,7 +210,8 @@ __device__ __forceinline__ void piece_scale(const void* in, void* out, int64_t f
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      w[e] = kF32 ? __float_as_uint(__uint_as_float(w[e]) * f) : ptx::pack_bf16x2(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f);
+      w[e] = kF32 ? __float_as_uint((float)(__uint_as_float(w[e]) * f))
+                  : ptx::pack_bf16x2((float)(bf16_lo(w[e]) * f), (float)(bf16_hi(w[e]) * f));
     return make_uint4(w[0], w[1], w[2], w[3]);
   };
   if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
@@ -233,24 +238,30 @@ template <int kMost>
 __global__ void __launch_bounds__(kThreads)
     gradient_scale(const __grid_constant__ Table<kMost> t, const double* partial, int count, float max_norm, float eps,
                    float* norm) {
-  __shared__ float factor;
+  __shared__ double factor;
   ptx::grid_wait_previous();
   const double total = norm_of(partial, count);
   if (threadIdx.x == 0) {
     if (blockIdx.x == 0 && norm) *norm = (float)total;
     const double limit = total + (double)eps;
-    factor = limit <= (double)max_norm ? 1.f : (float)((double)max_norm / limit);  // NaN stays NaN
+    factor = limit <= (double)max_norm ? 1.0 : (double)max_norm / limit;  // NaN stays NaN
   }
   __syncthreads();
-  const float f = factor;
+  const float f = (float)factor;
+  const bool small = factor > 0.0 && factor < 0x1p-126;
   const uint64_t pass = ptx::policy_evict_first();
   for (int64_t q = blockIdx.x; q < t.pieces; q += gridDim.x) {
     const int64_t p = t.pieces - 1 - q;
     const int i = tensor_of(t, p);
     if (f == 1.f && t.in[i] == t.out[i]) continue;
     const int64_t from = (p - t.first[i]) * kPiece;
-    if (t.f32[i]) piece_scale<true>(t.in[i], t.out[i], from, t.n[i], f, pass);
-    else piece_scale<false>(t.in[i], t.out[i], from, t.n[i], f, pass);
+    if (small) {
+      if (t.f32[i]) piece_scale<true>(t.in[i], t.out[i], from, t.n[i], factor, pass);
+      else piece_scale<false>(t.in[i], t.out[i], from, t.n[i], factor, pass);
+    } else {
+      if (t.f32[i]) piece_scale<true>(t.in[i], t.out[i], from, t.n[i], f, pass);
+      else piece_scale<false>(t.in[i], t.out[i], from, t.n[i], f, pass);
+    }
   }
 }
 

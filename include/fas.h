@@ -601,9 +601,11 @@ int fas_rotary(const void* const* in, const int64_t* in_strides, void* const* ou
  * Squares are summed in fp32 in runs of at most 32 and in 64 bits from there,
  * with values whose squares leave fp32's range added in 64 bits throughout;
  * the order is fixed, so the norm is bit-reproducible on one device.  In
- * place, gradients whose norm needs no clipping are not written.  A norm that
- * is not finite scales as the formula says (infinite: by 0, which turns
- * infinite values into NaN; NaN: everything becomes NaN).  fas_gradient_norm
+ * place, gradients whose norm needs no clipping are not written.  The scaling
+ * goes by the norm in 64 bits, also where that is beyond fp32 and `norm` gets
+ * infinity.  A norm that is not finite in 64 bits (a gradient is not) scales as
+ * the formula says (infinite: by 0, which turns infinite values into NaN; NaN:
+ * everything becomes NaN); an infinite max_norm leaves all but NaN norms alone.  fas_gradient_norm
  * reads a tensor that is given twice twice; outputs of fas_clip_gradients that
  * overlap another tensor return FAS_ERR_ARG, as do a negative or NaN max_norm
  * or eps.  n >= 0; one kernel per 960 tensors (64 in the smallest form) and

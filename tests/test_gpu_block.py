@@ -655,6 +655,30 @@ def test_gradient_norm_beyond_the_range_of_squares(scale):
             check_norm(fas.fas_gradient_norm(mixed), mixed)
 
 
+@pytest.mark.parametrize("scale,max_norm", [(1e37, 1.0), (3e38, 1.0), (3e38, 1e-6), (3e38, 1e-30), (1e30, 1e-12)])
+def test_clipping_by_factors_below_fp32(scale, max_norm):
+    """Huge gradients clipped to small norms: the factor is below fp32's normal
+    numbers, the results need not be.  The norm itself may be beyond fp32."""
+    rnd = gen(21)
+    max_norm = float(np.float32(max_norm))
+    for dtype in (BF16, torch.float32):
+        grads = [(rnd(1_000_000).clamp(-1, 1) * scale).to(dtype), (rnd(8193)[1:] * 1e30).to(dtype), torch.ones(9, dtype=dtype, device="cuda")]
+        norm = norm64(grads)
+        assert max_norm / norm < 2.0 ** -126
+        out = [torch.empty_like(t) for t in grads]
+        got = float(fas.fas_clip_gradients(grads, max_norm, eps=0.0, out=out))
+        assert got == math.inf if norm > 3.41e38 else abs(got - norm) <= 20 * U32 * norm
+        check_clipped(out, grads, norm, max_norm, eps=0.0)
+        fas.fas_clip_gradients(grads, max_norm, eps=0.0)
+        assert all(torch.equal(a, b) for a, b in zip(grads, out))
+    grads = [torch.full((100,), 3e38, device="cuda")]
+    fas.fas_clip_gradients(grads, 0.0)
+    assert bool((grads[0] == 0).all())
+    grads = [torch.full((100,), 3e38, device="cuda")]
+    fas.fas_clip_gradients(grads, math.inf)
+    assert bool((grads[0] == 3e38).all())
+
+
 @pytest.mark.parametrize("dtype", [BF16, torch.float32])
 def test_gradient_norm_of_zeros(dtype):
     """Gradients of zero (rows that no token took) are read once like any
