@@ -1243,6 +1243,7 @@ int fas_rotary(const void* const* in, const int64_t* in_strides, void* const* ou
   p.axes = axes;
   p.tokens = tokens;
   p.heads = heads;
+  p.pairs = pairs;
   p.sign = inverse ? -1.f : 1.f;
   int sms = 0;
   const int rc = device_sms(&sms);

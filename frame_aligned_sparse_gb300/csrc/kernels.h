@@ -254,6 +254,7 @@ struct RotaryParams {
   int axes = 0;
   int64_t tokens = 0;
   int heads = 0;
+  int pairs = 0;                      // of a head that turn
   float sign = 1.f;                   // -1: the opposite turn
   float turns[kRotaryMaxPairs] = {};  // each pair's frequency in turns a step, and what fp32 leaves of it
   float turns_low[kRotaryMaxPairs] = {};

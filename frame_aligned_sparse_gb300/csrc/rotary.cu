@@ -58,6 +58,30 @@ __device__ __forceinline__ void turn(uint4& x, uint4& y, const float (&c)[8], co
   y = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The same where only the first n of the eight pairs turn: the others keep
+// their bits (a turn by zero would not: infinity times the sine is NaN).
+template <bool kHalf>
+__device__ __forceinline__ void turn(uint4& x, uint4& y, const float (&c)[8], const float (&s)[8], int n) {
+  const uint4 x0 = x, y0 = y;
+  turn<kHalf>(x, y, c, s);
+  if (n == 8) return;
+  uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+  const uint32_t u0[4] = {x0.x, x0.y, x0.z, x0.w}, w0[4] = {y0.x, y0.y, y0.z, y0.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (kHalf) {  // pairs 2 e and 2 e + 1 in the halves of both
+      const uint32_t turned = (2 * e < n ? 0x0000FFFFu : 0u) | (2 * e + 1 < n ? 0xFFFF0000u : 0u);
+      u[e] = (u[e] & turned) | (u0[e] & ~turned);
+      w[e] = (w[e] & turned) | (w0[e] & ~turned);
+    } else {  // pair e in x, pair 4 + e in y
+      if (e >= n) u[e] = u0[e];
+      if (4 + e >= n) w[e] = w0[e];
+    }
+  }
+  x = make_uint4(u[0], u[1], u[2], u[3]);
+  y = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Grid: x over tokens, y over (tensor, run of heads).
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ RotaryParams p) {
@@ -75,7 +99,8 @@ __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Rotar
   const uint16_t* in = t.in + token * t.in_token + h0 * t.in_head + at;
   uint16_t* out = t.out + token * t.out_token + h0 * t.out_head + at;
   float c[8], s[8];
-  if (t.turned) {
+  const int pairs = t.turned ? min(8, p.pairs - piece * 8) : 0;  // that turn (0 or less: none)
+  if (pairs > 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int i = piece * 8 + e;
@@ -97,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Rotar
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k)
       if (h + k < h1) {
-        if (t.turned) turn<kHalf>(x[k], y[k], c, s);
+        if (pairs > 0) turn<kHalf>(x[k], y[k], c, s, pairs);
         *reinterpret_cast<uint4*>(out + k * t.out_head) = x[k];
         *reinterpret_cast<uint4*>(out + k * t.out_head + second) = y[k];
       }

@@ -564,7 +564,7 @@ int fas_feed_forward_workspace(int64_t tokens, int width, int inner, int backwar
  * or by the opposite angle where `inverse` (a gradient's way back: the turn is
  * orthogonal).  Pair j: elements j and j + head_dim / 2 (FAS_PAIRS_HALF, as
  * fas_prologue) or 2 j and 2 j + 1 (FAS_PAIRS_INTERLEAVED); pairs from `pairs`
- * on do not turn.
+ * on do not turn: they are copied bit by bit, whatever the position.
  *   positions : device fp32 [tokens, axes], of magnitude up to 2^90;
  *   frequencies: host, [pairs] radians per unit of position, of magnitude up to
  *               2^32 (FAS_ERR_ARG);

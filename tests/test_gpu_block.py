@@ -478,6 +478,29 @@ def test_rotary_in_place_zero_positions_and_round_trip():
     assert torch.all((back.double() - x.double()).abs() <= (2.5 * U16 * (a + b)).repeat(1, 1, 2))
 
 
+@pytest.mark.parametrize("pairing", list(fas.PAIRINGS))
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("count", [0, 1, 2, 3, 5, 7, 8, 9, 12, 15, 16, 31])
+def test_rotary_copies_the_pairs_that_do_not_turn(count, d, pairing):
+    """Bit by bit: next to infinities, NaN with their own bits, zeros of either
+    sign, and at positions that are infinite or NaN, as padding may be."""
+    rnd = gen(30 + count)
+    bits = torch.tensor([0x7F80, -0x80, 0x7FC1, -0x3F, -0x8000, 0x0001, 0x3F80], device="cuda", dtype=torch.int16)
+    for layout in fas.LAYOUTS:
+        x = lay(rnd(3, 41, d).to(BF16), layout)
+        where = torch.rand(x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(count)) < 0.2
+        some = bits[torch.randint(0, len(bits), x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1))]
+        x = torch.where(where, some, x.view(torch.int16)).view(BF16)
+        pos = positions(1, 1, 41)[:, :2].contiguous()
+        pos[3], pos[4, 0], pos[5, 1] = math.inf, math.nan, -math.inf
+        pair = torch.arange(d, device="cuda") % (d // 2) if pairing == "half" else torch.arange(d, device="cuda") // 2
+        still = pair >= count
+        for inverse in (False, True):
+            got = fas.fas_rotary(x, pos, pairs=(count - count // 2, count // 2), layout=layout, pairing=pairing, inverse=inverse)
+            assert torch.equal(got[..., still].view(torch.int16), x[..., still].view(torch.int16))
+            assert count == 0 or not torch.equal(got[..., ~still].view(torch.int16), x[..., ~still].view(torch.int16))
+
+
 def test_rotary_of_rows_further_apart():
     """The projection's output and its gradient as columns of wider matrices."""
     H, d, n = 3, 64, 37
