@@ -748,9 +748,7 @@ __global__ void __launch_bounds__(threads(kE), 1)
 }
 
 // Few tokens: the weights' bytes bound it, and a tile of 128 rows of A would
-// be mostly empty (2048 x 5504, in us, this way and with the tiles: one token
-// 17 and 30, 16 tokens 22 and 28, 24 tokens 30 and 27; 256 x 1024, 24 tokens 19
-// and 24).
+// be mostly empty (few_gate_up and few_out say up to how many).
 // Out[f, n] = sum_k W[f, k] X[n, k] by mma.sync with 16 rows of W as its m and
 // 8 tokens as its n, fed from memory without staging: which elements of k an
 // instruction takes together is free as long as both operands agree, so a lane
@@ -975,7 +973,7 @@ struct Launcher {
 // h, g and u, and the low parts of g and u from x, those that are given.
 int project(Launcher& l, const FeedForwardArgs& a, void* h, void* gu, uint16_t* low) {
   const int64_t N = a.tokens, C = a.width, F = a.inner;
-  if (N <= kFewTokens) return l.few<true>(a.x, a.w_in, h, gu, low, N, F, C, a.activation == FAS_ACT_SILU);
+  if (few_gate_up(N, F)) return l.few<true>(a.x, a.w_in, h, gu, low, N, F, C, a.activation == FAS_ACT_SILU);
   GemmParams p;
   p.gu = gu;
   p.low = low;
@@ -1042,8 +1040,8 @@ int launch_feed_forward(const FeedForwardArgs& a, void* workspace, int* launches
   p.parts = reinterpret_cast<float*>(w + ws.parts);
   const Product y[1] = {{N, C, {w + ws.h, N, F}, {a.w_out, C, F}, a.y}};
   if (rc == FAS_OK) {
-    rc = N <= kFewTokens ? l.few<false>(w + ws.h, a.w_out, a.y, nullptr, nullptr, N, C, F, false)
-                         : l.run<false, false, kPlain>(p, y, F, spread(kPlain, N, C, F, machine));
+    rc = few_out(N, C, F) ? l.few<false>(w + ws.h, a.w_out, a.y, nullptr, nullptr, N, C, F, false)
+                          : l.run<false, false, kPlain>(p, y, F, spread(kPlain, N, C, F, machine));
   }
   *launches = l.launches;
   return rc;

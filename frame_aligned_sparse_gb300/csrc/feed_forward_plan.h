@@ -14,7 +14,25 @@ constexpr int kBlock = 64;  // elements of a TMA block's side: a 128-byte swizzl
 
 enum Epilogue { kPlain = 0, kGateUp = 1, kInner = 2 };
 
-constexpr int kFewTokens = 31;  // so many take one pass over the weights (feed_forward_few)
+// Few tokens take one pass over the weights (feed_forward_few): up to 8 at any
+// size, more where what each further 8 tokens cost is less than what the pass
+// saves.  Of the gate-up product that grows with the inner features, its CTAs; of
+// the product onto the width with the inner features too, its sums, and it is
+// most where few columns make few CTAs, or so many that they fill the GPU
+// twice.  In us, that way and with the tiles, weights in HBM: 2048 x 5504, one
+// token 15.8 and 29.0, 16 tokens 19.5 and 26.1, 24 tokens 27.7 and 25.9;
+// 256 x 1024, 24 tokens 6.7 and 12.8.  The product onto the width alone, 12
+// tokens, longer than the tiles by: 1024 x 16384 2.3, 1024 x 8192 -2.1, 4096 x
+// 16384 -3.0.  What is left: the 512 CTAs of the gate-up product of 8192 x 8192
+// just miss one round (12 tokens 92 and 82).
+constexpr int kFewTokens = 31;  // at most
+inline bool few_gate_up(int64_t tokens, int64_t inner) {
+  return tokens <= 16 || (tokens <= kFewTokens && inner <= 4096);
+}
+inline bool few_out(int64_t tokens, int64_t width, int64_t inner) {
+  if (tokens <= 16) return tokens <= 8 || inner <= 8192 || width >= 2048;
+  return tokens <= kFewTokens && width <= 4096 && inner <= (width < 1024 ? 4096 : 6144);
+}
 
 // What runs at once: CTAs, one an SM, and pairs of CTAs (an SM may be left
 // without a partner).
@@ -104,7 +122,7 @@ struct Workspace {
       most = std::max(spread(kPlain, tokens, width, 2 * (int64_t)inner, machine).bytes(),
                       spread_weights(tokens, width, inner, machine).bytes());
     } else {
-      most = tokens <= kFewTokens ? 0 : spread(kPlain, tokens, width, inner, machine).bytes();
+      most = few_out(tokens, width, inner) ? 0 : spread(kPlain, tokens, width, inner, machine).bytes();
     }
     parts = at;
     bytes = at + align_up(most);

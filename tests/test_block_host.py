@@ -227,6 +227,34 @@ def test_feed_forward_products_are_spread_over_what_runs(tmp_path):
     assert got.returncode == 0, got.stdout
 
 
+# Width, inner, tokens; us of a forward pass with both products over the weights
+# in one pass, with the gate-up product only, with the other only, and with
+# tiles for both (medians, weights in HBM).
+FEW = [(64, 64, 31, 4.9, 5.7, 6.1, 7.2), (256, 1024, 24, 6.7, 10.8, 8.4, 12.8), (1024, 2728, 12, 10.9, 15.4, 14.5, 18.9),
+       (1024, 2728, 31, 16.0, 18.1, 17.1, 19.1), (2048, 5504, 1, 15.8, 22.1, 22.7, 29.0), (2048, 5504, 16, 19.5, 23.2, 22.4, 26.1),
+       (2048, 5504, 17, 26.9, 28.0, 25.1, 26.2), (2048, 5504, 24, 27.7, 28.3, 25.3, 25.9), (2048, 5504, 31, 28.4, 29.3, 25.7, 26.2),
+       (4096, 11008, 16, 56.1, 59.8, 69.0, 71.7), (4096, 11008, 24, 80.6, 77.3, 75.9, 72.1), (8192, 1024, 8, 22.6, 25.4, 46.3, 49.2),
+       (8192, 1024, 24, 46.2, 44.1, 51.2, 49.4), (1024, 16384, 12, 36.2, 33.4, 37.4, 35.3), (1024, 16384, 24, 54.3, 41.9, 44.5, 33.2),
+       (104, 9336, 12, 18.8, 18.0, 21.2, 19.9), (104, 9336, 24, 28.6, 21.8, 27.5, 20.2)]
+
+
+def test_few_tokens_take_the_form_that_was_measured_faster(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host compiler")
+    calls = "".join(f'  std::printf("%d %d\\n", few_gate_up({n}, {f}), few_out({n}, {c}, {f}));\n' for c, f, n, *_ in FEW)
+    (tmp_path / "few.cpp").write_text('#include "feed_forward_plan.h"\n#include <cstdio>\nusing namespace fas::feed_forward;\n'
+                                      "int main() {\n" + calls + "}\n")
+    exe = str(tmp_path / "few")
+    csrc = os.path.join(os.path.dirname(fas.__file__), "csrc")
+    subprocess.run([gxx, "-std=c++17", "-I" + csrc, str(tmp_path / "few.cpp"), "-o", exe], check=True)
+    got = subprocess.run([exe], capture_output=True, text=True, check=True, timeout=60).stdout.split("\n")
+    for (c, f, n, *us), line in zip(FEW, got):
+        gate_up, out = (bool(int(v)) for v in line.split())
+        chosen = us[(0 if gate_up else 2) + (0 if out else 1)]
+        assert chosen <= 1.04 * min(us), (c, f, n, gate_up, out)  # the measurements' own spread
+
+
 def rotary_call(**kw):
     a = dict(ins=[A, 2 * A, 3 * A], in_strides=[384, 64] * 3, outs=[4 * A, 5 * A, 6 * A], out_strides=[64, 640] * 3, turned=[1, 1, 0],
              n=3, positions=7 * A, axes=2, freq=[1.0, 0.5, 0.25], axis=[0, 1, 1], pairs=3, pairing=0, inverse=0, tokens=10, heads=2,

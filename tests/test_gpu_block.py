@@ -85,6 +85,12 @@ def test_feed_forward_and_its_backward(shape, act):
     Block(*shape).check(act)
 
 
+@pytest.mark.parametrize("shape", [(17, 64, 4104), (31, 2048, 5504), (12, 104, 8200), (20, 4104, 64), (16, 264, 16384), (8, 72, 16384),
+                                   (30, 264, 4096)], ids=lambda s: "x".join(map(str, s)))
+def test_feed_forward_of_few_tokens_by_either_form(shape):
+    Block(*shape).check("gelu_tanh")
+
+
 @pytest.mark.parametrize("shape", [(14960, 2048, 1376), (20000, 1000, 2728)], ids=lambda s: "x".join(map(str, s)))
 def test_feed_forward_of_many_tiles(shape):
     Block(*shape).check()
