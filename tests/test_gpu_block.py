@@ -96,6 +96,15 @@ def test_feed_forward_of_many_tiles(shape):
     Block(*shape).check()
 
 
+@pytest.mark.parametrize("act", list(fas.ACTIVATIONS))
+@pytest.mark.parametrize("shape", [(9000, 104, 1032), (6001, 72, 5000), (23374, 104, 136), (3000, 8, 9336), (20000, 256, 1024)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_feed_forward_of_narrow_widths_and_many_tokens(shape, act):
+    """Sums of one to four steps of 64 over many tiles, some left over after
+    whole rounds, in the forms of both single CTAs and pairs."""
+    Block(*shape).check(act)
+
+
 @pytest.mark.parametrize("shape", [(700, 200, 328), (4, 96, 64)], ids=str)
 def test_feed_forward_matches_differences(shape):
     """Along a random direction, the 64-bit loss's central difference against
